@@ -40,4 +40,28 @@ hipError_t launch_dense_gemm(const uint16_t* x, const uint16_t* w, int64_t M, in
 hipError_t launch_repack(const uint16_t* vals, const uint8_t* idx, const float* scale, int64_t M,
                          int64_t K, void* workspace, hipStream_t stream);
 
+// Rotary positions.  One tensor [batch, tokens, heads, dim] and its result
+// (strides in elements); heads == 0 for an absent second tensor.
+struct RopeSide {
+  const void* x;
+  void* y;
+  int64_t xb, xt, xh, yb, yt, yh;
+  int heads;
+  bool in_place;                         // y is x: copied channels need no copy
+};
+struct RopeArgs {
+  RopeSide t[2];
+  const int64_t* positions;
+  const double* inv_freq;
+  int64_t total, tokens;                 // batch * tokens, tokens
+  int64_t pos_b, pos_t;
+  int dim, rot;
+  int axis_end[3];                       // first pair of axes 1, 2 and 3
+  float scale;
+  bool inverse;
+  int group;                             // tokens per workgroup (set by launch_rope)
+};
+hipError_t launch_rope(RopeArgs a, int elem_bytes, bool fp16, bool interleaved, int compute_units,
+                       hipStream_t stream);
+
 }  // namespace rtl

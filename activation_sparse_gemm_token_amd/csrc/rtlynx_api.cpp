@@ -11,11 +11,10 @@
 #include <cstring>
 #include <mutex>
 
+#include "rtl_api.hpp"
 #include "rtl_common.hpp"
 #include "rtl_kernels.hpp"
 #include "rtlynx.h"
-
-#define RTL_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 
@@ -53,9 +52,37 @@ bool layer_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
   return bytes_ok(L.mp, L.kp, 1) && bytes_ok(L.mp, L.rp, 4);
 }
 
-// Checks that a gfx950 device is current and that `stream` (NULL: the null
-// stream) belongs to it; sets *cus to its CU count.
-rtl_status check_device(hipStream_t stream, int* cus = nullptr) {
+// Scratch of rtl_sparse_linear_noalloc: the workspace of the layer, held in
+// a device array of fixed size that each GPU running the library keeps
+// until the process ends.  Host code never uses the array's name as an
+// address (on the host it names a stand-in, not device memory): the device
+// address is read once per device with hipGetSymbolAddress, with that
+// device current, and kept in g_scratch_ptr.
+static __device__ __align__(256) char scratch[RTL_NOALLOC_SCRATCH_BYTES];
+
+std::atomic<void*> g_scratch_ptr[kMaxDevices];
+std::mutex g_scratch_mu;
+
+// Device address of `scratch` on the current device `dev`, or nullptr if
+// the runtime cannot provide it.
+void* scratch_address(int dev) {
+  void* p = g_scratch_ptr[dev].load(std::memory_order_acquire);
+  if (p != nullptr) return p;
+  std::lock_guard<std::mutex> lock(g_scratch_mu);
+  p = g_scratch_ptr[dev].load(std::memory_order_relaxed);
+  if (p == nullptr) {
+    if (hipGetSymbolAddress(&p, HIP_SYMBOL(scratch)) != hipSuccess || p == nullptr) {
+      (void)hipGetLastError();
+      return nullptr;
+    }
+    g_scratch_ptr[dev].store(p, std::memory_order_release);
+  }
+  return p;
+}
+
+}  // namespace
+
+rtl_status rtl::check_device(hipStream_t stream, int* cus) {
   int count = 0;
   if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
     (void)hipGetLastError();
@@ -92,37 +119,8 @@ rtl_status check_device(hipStream_t stream, int* cus = nullptr) {
   return known == 1 ? RTL_OK : RTL_ERR_UNSUPPORTED_ARCH;
 }
 
-rtl_status from_hip(hipError_t e) { return e == hipSuccess ? RTL_OK : RTL_ERR_HIP; }
-
-// Scratch of rtl_sparse_linear_noalloc: the workspace of the layer, held in
-// a device array of fixed size that each GPU running the library keeps
-// until the process ends.  Host code never uses the array's name as an
-// address (on the host it names a stand-in, not device memory): the device
-// address is read once per device with hipGetSymbolAddress, with that
-// device current, and kept in g_scratch_ptr.
-static __device__ __align__(256) char scratch[RTL_NOALLOC_SCRATCH_BYTES];
-
-std::atomic<void*> g_scratch_ptr[kMaxDevices];
-std::mutex g_scratch_mu;
-
-// Device address of `scratch` on the current device `dev`, or nullptr if
-// the runtime cannot provide it.
-void* scratch_address(int dev) {
-  void* p = g_scratch_ptr[dev].load(std::memory_order_acquire);
-  if (p != nullptr) return p;
-  std::lock_guard<std::mutex> lock(g_scratch_mu);
-  p = g_scratch_ptr[dev].load(std::memory_order_relaxed);
-  if (p == nullptr) {
-    if (hipGetSymbolAddress(&p, HIP_SYMBOL(scratch)) != hipSuccess || p == nullptr) {
-      (void)hipGetLastError();
-      return nullptr;
-    }
-    g_scratch_ptr[dev].store(p, std::memory_order_release);
-  }
-  return p;
-}
-
-}  // namespace
+using rtl::check_device;
+using rtl::from_hip;
 
 RTL_API rtl_status rtl_sparsify_2of4(const uint16_t* x, int64_t M, int64_t K, uint16_t* vals,
                                      uint8_t* idx, float* scale, uint32_t flags, void* hip_stream) {

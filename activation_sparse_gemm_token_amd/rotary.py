@@ -1,0 +1,224 @@
+"""Rotary positions (include/rtlynx_rope.h): the rotation of the queries and
+keys that a block's projections make, its gradient, and the frequency tables.
+
+``rope`` and ``rope_backward`` take strided tensors (slices of a fused Q/K/V
+projection included), rotate one or two of them in one launch and need only
+the channel stride to be 1.  Argument marshalling only, as in the package's
+other bindings; the tables are small host-side vectors in float64.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import _check, _on, _stream, _torch, lib
+
+__all__ = ["rope", "rope_backward", "frequencies", "frequencies_by_parts", "LAYOUTS"]
+
+LAYOUTS = ("half", "interleaved")
+_INTERLEAVED, _INVERSE = 0x10, 0x20
+
+_c_i64, _c_vp = ctypes.c_int64, ctypes.c_void_p
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("x", _c_vp), ("y", _c_vp), ("heads", _c_i64)] + [
+        (f"{t}_{d}_stride", _c_i64) for t in "xy" for d in ("batch", "token", "head")]
+
+
+_SIG = (ctypes.c_int, [ctypes.POINTER(_Tensor), ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
+                       ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), _c_vp, ctypes.c_float, ctypes.c_uint32, _c_vp])
+
+
+def _fn():
+    fn = lib().rtl_rope
+    if fn.argtypes is None:
+        fn.restype, fn.argtypes = _SIG
+    return fn
+
+
+def frequencies(rot_dim: int, base: float = 10000.0, linear: float = 1.0, ntk: float = 1.0):
+    """Radians per position of each of ``rot_dim / 2`` pairs, float64 on the
+    host: base^(-2 i / rot_dim).  ``linear`` divides every frequency (positions
+    stretched by that factor); ``ntk`` stretches the base so that the slowest
+    pair slows by that factor and the fastest not at all."""
+    torch = _torch()
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and >= 0")
+    if not (base > 0 and linear > 0 and ntk > 0):
+        raise ValueError("base, linear and ntk must be positive")
+    if ntk != 1.0 and rot_dim > 2:
+        base = base * ntk ** (rot_dim / (rot_dim - 2))
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    return torch.exp(i * (-2.0 / max(rot_dim, 1) * math.log(base))) / linear
+
+
+def frequencies_by_parts(rot_dim: int, factor: float, trained_length: int, base: float = 10000.0,
+                         fast_turns: float = 32.0, slow_turns: float = 1.0):
+    """Frequencies scaled by parts for contexts ``factor`` times the trained
+    one, and the scale that goes with them: pairs that turn more than
+    ``fast_turns`` times over ``trained_length`` positions keep their
+    frequency, those below ``slow_turns`` are divided by ``factor``, and
+    between the two the share moves linearly with the pair's index.
+    Returns (float64 host tensor, scale = 0.1 ln(factor) + 1)."""
+    torch = _torch()
+    if factor < 1 or trained_length < 1 or not fast_turns > slow_turns > 0:
+        raise ValueError("need factor >= 1, trained_length >= 1 and fast_turns > slow_turns > 0")
+    f = frequencies(rot_dim, base)
+
+    def index(turns):                        # pair that turns so often over the trained length
+        return rot_dim * math.log(trained_length / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    lo, hi = max(math.floor(index(fast_turns)), 0), min(math.ceil(index(slow_turns)), rot_dim - 1)
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    return f * (1 - slow) + f / factor * slow, 0.1 * math.log(factor) + 1.0
+
+
+def _span(t):
+    """Bytes [first, past the last) that a tensor's elements lie in."""
+    lo = hi = t.data_ptr()
+    for n, s in zip(t.shape, t.stride()):
+        if n == 0:
+            return t.data_ptr(), t.data_ptr()
+        if s < 0:
+            lo += (n - 1) * s * t.element_size()
+        else:
+            hi += (n - 1) * s * t.element_size()
+    return lo, hi + t.element_size()
+
+
+def _distinct(t):
+    """Whether no two index tuples name one element (by nested extents)."""
+    inner = 1
+    for s, n in sorted((abs(s), n) for n, s in zip(t.shape, t.stride()) if n > 1):
+        if s < inner:
+            return False
+        inner = s * (n - 1) + inner
+    return True
+
+
+def _same(a, b):
+    return a.data_ptr() == b.data_ptr() and a.stride() == b.stride() and a.shape == b.shape
+
+
+def _apart(a, b):
+    """Whether two tensors share no element: disjoint extents, or slices of
+    one tensor side by side along heads."""
+    (al, ah), (bl, bh) = _span(a), _span(b)
+    if ah <= bl or bh <= al:
+        return True
+    if a.stride() != b.stride() or a.shape[:-2] != b.shape[:-2]:
+        return False
+    if a.data_ptr() > b.data_ptr():
+        a, b = b, a
+    off, size = b.data_ptr() - a.data_ptr(), a.element_size()
+    room = min((s * size for n, s in zip(a.shape[:-2], a.stride()[:-2]) if n > 1), default=None)
+    head = a.stride(-2) * size
+    if head <= 0 or (room is not None and room <= 0):
+        return False
+    first, second = (a.shape[-2] - 1) * head + a.shape[-1] * size, (b.shape[-2] - 1) * head + b.shape[-1] * size
+    if room is None:
+        return off >= first
+    nested = a.dim() < 4 or a.shape[0] <= 1 or a.shape[1] <= 1 or \
+        a.stride(0) * size >= a.stride(1) * size * a.shape[1] or a.stride(1) * size >= a.stride(0) * size * a.shape[0]
+    return nested and off >= first and off + second <= room
+
+
+def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, inverse):
+    torch = _torch()
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be one of {LAYOUTS}, got {layout!r}")
+    if x.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim]")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    ins = [("x", x, out)] + ([("k", k, k_out)] if k is not None else [])
+    lead, dim, outs = tuple(x.shape[:-2]), x.shape[-1], []
+    for name, t, o in ins:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.dtype != x.dtype:
+            raise TypeError(f"{name} must be {x.dtype} like x, got {t.dtype}")
+        if t.dim() != x.dim() or tuple(t.shape[:-2]) != lead or t.shape[-1] != dim:
+            raise ValueError(f"{name} must have shape {lead + ('heads', dim)}, got {tuple(t.shape)}")
+        if dim > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the channel stride must be 1")
+        if o is None:
+            o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        else:
+            if o.dtype != t.dtype:
+                raise TypeError(f"out of {name} must be {t.dtype}, got {o.dtype}")
+            if o.device != t.device or o.shape != t.shape:
+                raise ValueError(f"out of {name} must be on {t.device} with shape {tuple(t.shape)}")
+            if (dim > 1 and o.stride(-1) != 1) or not _distinct(o):
+                raise ValueError(f"out of {name} must have a channel stride of 1 and no overlapping elements")
+        outs.append(o)
+    given = out is not None or k_out is not None
+    for i, o in enumerate(outs if given else ()):
+        for j, (name, t, _) in enumerate(ins):
+            if o.numel() and t.numel() and not (i == j and _same(o, t)) and not _apart(o, t):
+                raise ValueError(f"an output overlaps {name} (it may be its own input, or share no element with any)")
+    if given and len(outs) == 2 and outs[0].numel() and outs[1].numel() and not _apart(outs[0], outs[1]):
+        raise ValueError("the two outputs overlap")
+
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous float64 vector")
+    rot = 2 * inv_freq.shape[0]
+    if rot > dim:
+        raise ValueError(f"inv_freq has {rot // 2} pairs, a head {dim} channels")
+    axes = 1 if sections is None else len(sections)
+    if sections is not None and (any(int(s) < 0 for s in sections) or sum(int(s) for s in sections) != rot // 2):
+        raise ValueError(f"sections must be counts that sum to {rot // 2} pairs, got {list(sections)}")
+    if positions.dtype != torch.int64:
+        raise TypeError(f"positions must be int64, got {positions.dtype}")
+    tail = () if sections is None else (axes,)
+    if tuple(positions.shape) == lead + tail:
+        pos = positions
+    elif len(lead) == 2 and tuple(positions.shape) == lead[1:] + tail:
+        pos = positions.unsqueeze(0).expand(lead + tail)
+    else:
+        raise ValueError(f"positions must have shape {lead + tail}" +
+                         (f" or {lead[1:] + tail}" if len(lead) == 2 else "") + f", got {tuple(positions.shape)}")
+    if sections is not None and axes > 1 and pos.stride(-1) != 1:
+        raise ValueError("positions: the axis stride must be 1")
+    batch, tokens = (1, lead[0]) if len(lead) == 1 else lead
+    pos_b, pos_t = (0, pos.stride(0)) if len(lead) == 1 else (pos.stride(0), pos.stride(1))
+
+    def strides(t):
+        return (0, t.stride(0), t.stride(1)) if len(lead) == 1 else (t.stride(0), t.stride(1), t.stride(2))
+
+    arr = (_Tensor * len(ins))(*[_Tensor(t.data_ptr(), o.data_ptr(), t.shape[-2], *strides(t), *strides(o))
+                                 for (_, t, _), o in zip(ins, outs)])
+    pairs = (ctypes.c_int32 * axes)(*[int(s) for s in sections]) if sections is not None else None
+    flags = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[x.dtype]
+    flags |= (_INTERLEAVED if layout == "interleaved" else 0) | (_INVERSE if inverse else 0)
+    with _on(x.device, k=k, positions=positions, inv_freq=inv_freq):
+        st = _fn()(arr, len(ins), batch, tokens, dim, rot, pos.data_ptr(), pos_b, pos_t, axes, pairs,
+                   inv_freq.data_ptr(), float(scale), flags, _stream())
+    _check(st, "rtl_rope")
+    return outs[0] if k is None else tuple(outs)
+
+
+def rope(x, positions, inv_freq, k=None, layout: str = "half", sections=None, scale: float = 1.0, out=None,
+         k_out=None):
+    """Rotates x (and k) [batch, tokens, heads, head_dim] or [tokens, heads,
+    head_dim] (bf16, fp16 or fp32; k may have another number of heads) by
+    position * inv_freq.
+
+    ``positions`` int64 [batch, tokens] or [tokens]; with ``sections`` (pairs
+    per position axis, at most 4 axes, e.g. frame, row and column) it has a
+    last dimension of that many axes.  ``inv_freq`` float64 [rot / 2] on the
+    device (``frequencies``); channels past rot are copied.  ``layout``
+    "half" pairs channels (i, i + rot / 2), "interleaved" (2i, 2i + 1).
+    ``out`` / ``k_out`` may be the input itself.  Returns y, or (y, k's y)."""
+    return _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, False)
+
+
+def rope_backward(dy, positions, inv_freq, k=None, layout: str = "half", sections=None, scale: float = 1.0,
+                  out=None, k_out=None):
+    """Gradient of ``rope`` with respect to its tensors from the gradients dy
+    (and k) of its results; arguments as there."""
+    return _rope(dy, positions, inv_freq, k, layout, sections, scale, out, k_out, True)
