@@ -64,4 +64,11 @@ struct RopeArgs {
 hipError_t launch_rope(RopeArgs a, int elem_bytes, bool fp16, bool interleaved, int compute_units,
                        hipStream_t stream);
 
+// 4-bit weights: tiles of 16 rows x 128 channels (1 KiB of codes each).
+inline int64_t w4_tiles(int64_t N, int64_t K) { return ((N + 15) / 16) * ((K + 127) / 128); }
+hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t N,
+                          int64_t K, int group, void* packed, hipStream_t stream);
+hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, int64_t N, int64_t K,
+                            int group, bool zeros, uint16_t* y, hipStream_t stream);
+
 }  // namespace rtl
