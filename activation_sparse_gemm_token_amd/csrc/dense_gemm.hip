@@ -27,10 +27,12 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kWaveM = 128, kWaveN = 64;
 constexpr int kRB = kWaveM / 16, kCB = kWaveN / 16;
 
-template <int KM>
+// OUT: uint16_t for a bf16 result, float for an fp32 one (stored from the
+// accumulators: 16 lanes write 64 contiguous bytes of a row).
+template <int KM, typename OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
-                  int64_t M, int64_t N, int64_t K, uint16_t* __restrict__ y) {
+                  int64_t M, int64_t N, int64_t K, OUT* __restrict__ y) {
   constexpr int kWStages = 3, kAStages = 2;
   // One LDS block: the W ring, then the A ring; the epilogue reuses all of it.
   constexpr int kLdsBytes = (kWStages + kAStages) * kTileBytes;
@@ -148,23 +150,48 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   wait_vm<0>();
   barrier_no_fence();                     // every wave is done with the rings
 
-  if (N % 8 == 0) store_tile_via_lds<kRB, kCB>(acc, lds, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
+  if constexpr (std::is_same_v<OUT, float>) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int rb = 0; rb < kRB; ++rb)
+#pragma unroll
+      for (int cb = 0; cb < kCB; ++cb) {
+        const int64_t n = n0 + wn * kWaveN + 16 * cb + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t m = m0 + wm * kWaveM + 16 * rb + 4 * (lane >> 4) + i;
+          if (m < M && n < N) y[m * N + n] = acc[rb][cb][i];
+        }
+      }
+  }
+  else if (N % 8 == 0) store_tile_via_lds<kRB, kCB>(acc, lds, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
   else store_acc_bf16<kRB, kCB>(acc, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
+}
+
+template <typename OUT>
+hipError_t launch_dense(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K, OUT* y,
+                        hipStream_t stream) {
+  const int64_t tiles = ((M + kTileM - 1) / kTileM) * ((N + kTileN - 1) / kTileN);
+  const dim3 grid((unsigned)tiles), block(kThreads);
+  // 16 x 16 blocks: a form of the same loop on v_mfma_f32_32x32x16_bf16
+  // (4 x 2 blocks of 32 x 32 per wavefront) measured 8 % slower (253
+  // against 235 us at M = 4096, K = 3072, N = 12288).
+  auto* k = K % kTileK == 0 ? &dense_gemm_kernel<kFullK, OUT>
+            : K % 8 == 0   ? &dense_gemm_kernel<kAligned16, OUT>
+                           : &dense_gemm_kernel<kAligned8, OUT>;
+  return launch(k, grid, block, stream, x, w, M, N, K, y);
 }
 
 }  // namespace
 
 hipError_t launch_dense_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
                              int64_t K, uint16_t* y, hipStream_t stream) {
-  const int64_t tiles = ((M + kTileM - 1) / kTileM) * ((N + kTileN - 1) / kTileN);
-  const dim3 grid((unsigned)tiles), block(kThreads);
-  // 16 x 16 blocks: a form of the same loop on v_mfma_f32_32x32x16_bf16
-  // (4 x 2 blocks of 32 x 32 per wavefront) measured 8 % slower (253
-  // against 235 us at M = 4096, K = 3072, N = 12288).
-  auto* k = K % kTileK == 0 ? &dense_gemm_kernel<kFullK>
-            : K % 8 == 0   ? &dense_gemm_kernel<kAligned16>
-                           : &dense_gemm_kernel<kAligned8>;
-  return launch(k, grid, block, stream, x, w, M, N, K, y);
+  return launch_dense(x, w, M, N, K, y, stream);
+}
+
+hipError_t launch_dense_gemm_f32(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
+                                 int64_t K, float* y, hipStream_t stream) {
+  return launch_dense(x, w, M, N, K, y, stream);
 }
 
 }  // namespace rtl

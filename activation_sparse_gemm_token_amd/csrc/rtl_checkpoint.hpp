@@ -1,0 +1,47 @@
+// Device-side reading of the 8-bit checkpoint (include/rtlynx_train.h).
+#pragma once
+
+#include "rtl_common.hpp"
+
+namespace rtl {
+
+// Code in byte b of word q times 2^(e - 133), fp32.
+template <int B>
+__device__ __forceinline__ float ckpt_value(uint32_t q, int e) {
+  return __builtin_amdgcn_ldexpf((float)((int)(q << (24 - 8 * B)) >> 24), e - 133);
+}
+
+// 8 codes as 8 bf16: 7 significant bits and a power of two, so the upper half of
+// the fp32 value is the value (below 2^-126 too: the smallest step is bf16's).
+__device__ __forceinline__ u32x4 ckpt_values(u32x2 q, int e) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, ckpt_value<0>(q[i], e));
+    const uint32_t b = __builtin_bit_cast(uint32_t, ckpt_value<1>(q[i], e));
+    const uint32_t c = __builtin_bit_cast(uint32_t, ckpt_value<2>(q[i], e));
+    const uint32_t d = __builtin_bit_cast(uint32_t, ckpt_value<3>(q[i], e));
+    v[2 * i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    v[2 * i + 1] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+  }
+  return v;
+}
+
+// Kept channels of one group's code (idx0 | idx1 << 2) as bits 0..3.
+__device__ __forceinline__ uint32_t kept_bits(uint32_t code) {
+  return (1u << (code & 3u)) | (1u << ((code >> 2) & 3u));
+}
+
+// 16-bit lane masks of the 8 channels that one idx byte describes.
+__device__ __forceinline__ u32x4 kept_masks(uint32_t byte) {
+  u32x4 m;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t b = kept_bits(byte >> (4 * i));
+    m[2 * i] = (b & 1u) * 0xffffu | ((b >> 1) & 1u) * 0xffff0000u;
+    m[2 * i + 1] = ((b >> 2) & 1u) * 0xffffu | ((b >> 3) & 1u) * 0xffff0000u;
+  }
+  return m;
+}
+
+}  // namespace rtl

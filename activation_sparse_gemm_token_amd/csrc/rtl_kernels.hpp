@@ -35,6 +35,10 @@ int sparse_gemm_tile_n(int64_t M, int64_t N, int64_t K, int compute_units);
 hipError_t launch_dense_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
                              int64_t K, uint16_t* y, hipStream_t stream);
 
+// The same product with an fp32 result.
+hipError_t launch_dense_gemm_f32(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
+                                 float* y, hipStream_t stream);
+
 // Canonical compressed activation (vals, idx, scale or null) into the
 // workspace regions of ws_layout(M, K, 0).
 hipError_t launch_repack(const uint16_t* vals, const uint8_t* idx, const float* scale, int64_t M,
@@ -70,5 +74,31 @@ hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, const ui
                           int64_t K, int group, void* packed, hipStream_t stream);
 hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, int64_t N, int64_t K,
                             int group, bool zeros, uint16_t* y, hipStream_t stream);
+
+// 8-bit activation checkpoint (include/rtlynx_train.h).
+struct Ckpt {
+  const int8_t* codes;
+  const uint8_t* exps;
+  const uint8_t* idx;
+  const float* stats;
+};
+hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
+                                  uint8_t* idx, float* stats, int compute_units, hipStream_t stream);
+hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K,
+                                    uint16_t* y, hipStream_t stream);
+
+// Sizes, splits and workspace regions of the layer's backward pass.  Rank is
+// padded to 32, 64 or 128, channels and tokens to 64 (zeros).
+struct BackwardLayout {
+  int64_t M, N, K, r;
+  int64_t rp, np, kp, mp;
+  int64_t row_chunk, row_splits_g, row_splits_x;   // channel ranges of the token-by-rank products
+  int64_t col_chunk, col_splits;                   // token ranges of the products over tokens
+  size_t off_ap, off_at, off_bt, off_u_rows, off_u_cols, off_t_cols, off_d, off_part, off_p, total;
+};
+BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t r);
+hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
+                           const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx,
+                           uint16_t* da, uint16_t* db, char* workspace, hipStream_t stream);
 
 }  // namespace rtl

@@ -1,0 +1,148 @@
+"""Training the LoRA branch of the sparse layer (include/rtlynx_train.h): the
+layer's input kept in 8 bits, and the backward pass that reads it.
+
+    y    = sparse_linear(x, w, a, b, alpha)         # forward
+    kept = training.checkpoint(x)                   # instead of keeping x
+    dx, da, db = training.sparse_linear_backward(dy, kept, w_t, a, b, alpha)
+
+Argument marshalling only, as in the package's other bindings.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _as_2d, _check, _on, _out, _stream, _torch, _workspace, lib
+
+__all__ = ["Checkpoint", "checkpoint", "unpack", "sparse_linear_backward", "backward_workspace_bytes"]
+
+_c_i64, _c_vp, _c_size, _c_int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_SIGNATURES = {
+    "rtl_checkpoint_pack": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "rtl_checkpoint_unpack": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
+    "rtl_sparse_linear_backward_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "rtl_sparse_linear_backward": (_c_int, [_c_vp] * 8 + [_c_i64] * 4 + [ctypes.c_float] + [_c_vp] * 4 +
+                                   [_c_size, _c_vp]),
+}
+
+
+def _fn(name):
+    fn = getattr(lib(), name)
+    if fn.argtypes is None:
+        fn.restype, fn.argtypes = _SIGNATURES[name]
+    return fn
+
+
+class Checkpoint:
+    """A layer's input [m, k] in 8 bits: ``codes`` int8 [m, k] times
+    2^(``exps`` - 133) per 32 channels (uint8 [m, ceil(k / 32)]), the kept
+    channels ``idx`` uint8 [m, ceil(k / 8)] and ``stats`` fp32 [m, 2] (the
+    token's scale, the L1 norm of its kept channels).  ``lead`` is the shape of
+    x without its channels."""
+
+    def __init__(self, codes, exps, idx, stats, lead=None):
+        torch = _torch()
+        if codes.dim() != 2:
+            raise ValueError("codes must be [m, k]")
+        m, k = codes.shape
+        if k < 4 or k % 4:
+            raise ValueError(f"k must be a multiple of 4, got {k}")
+        for name, t, dtype, shape in (("codes", codes, torch.int8, (m, k)),
+                                      ("exps", exps, torch.uint8, (m, (k + 31) // 32)),
+                                      ("idx", idx, torch.uint8, (m, (k + 7) // 8)),
+                                      ("stats", stats, torch.float32, (m, 2))):
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous device tensor")
+            if t.device != codes.device:
+                raise ValueError(f"{name} is on {t.device}, codes on {codes.device}")
+        self.codes, self.exps, self.idx, self.stats = codes, exps, idx, stats
+        self.m, self.k, self.lead = m, k, (m,) if lead is None else tuple(lead)
+
+    def unpack(self, out=None):
+        """The stored values [*lead, k] in bf16 (exact)."""
+        y = unpack(self.codes, self.exps, out=out)
+        return y.reshape(*self.lead, self.k)
+
+
+def checkpoint(x) -> Checkpoint:
+    """Keeps x [..., k] (bf16, finite) in 8 bits for the backward pass."""
+    torch = _torch()
+    x2 = _as_2d(x, "x")
+    m, k = x2.shape
+    codes = torch.empty((m, k), dtype=torch.int8, device=x2.device)
+    exps = torch.empty((m, (k + 31) // 32), dtype=torch.uint8, device=x2.device)
+    idx = torch.empty((m, (k + 7) // 8), dtype=torch.uint8, device=x2.device)
+    stats = torch.empty((m, 2), dtype=torch.float32, device=x2.device)
+    with _on(x2.device):
+        st = _fn("rtl_checkpoint_pack")(x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), idx.data_ptr(),
+                                        stats.data_ptr(), _stream())
+    _check(st, "rtl_checkpoint_pack")
+    return Checkpoint(codes, exps, idx, stats, x.shape[:-1])
+
+
+def unpack(codes, exps, out=None):
+    """bf16 values [m, k] of int8 codes [m, k] and exponents [m, ceil(k / 32)]."""
+    torch = _torch()
+    if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
+        raise TypeError("codes must be int8 and exps uint8")
+    if codes.dim() != 2 or tuple(exps.shape) != (codes.shape[0], (codes.shape[1] + 31) // 32):
+        raise ValueError("codes must be [m, k] and exps [m, ceil(k / 32)]")
+    if not codes.is_cuda or not codes.is_contiguous() or not exps.is_contiguous():
+        raise ValueError("codes and exps must be contiguous device tensors")
+    m, k = codes.shape
+    y = _out(out, m, k, (m,), codes.device)
+    with _on(codes.device, exps=exps):
+        st = _fn("rtl_checkpoint_unpack")(codes.data_ptr(), exps.data_ptr(), m, k, y.data_ptr(), _stream())
+    _check(st, "rtl_checkpoint_unpack")
+    return y
+
+
+def backward_workspace_bytes(m: int, n: int, k: int, r: int) -> int:
+    return int(_fn("rtl_sparse_linear_backward_workspace_bytes")(m, n, k, r))
+
+
+def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, lora_scale: float = 1.0,
+                           need_dx: bool = True, need_lora: bool = True, workspace=None):
+    """Gradients of ``sparse_linear`` from g = dL/dy [..., n] and the input's
+    checkpoint: (dx [..., k], da [r, k], db [n, r]), bf16, None where not
+    asked for (da and db are None without a LoRA branch).
+
+    ``w_t`` [k, n] is the frozen weight transposed, laid out once
+    (``w.t().contiguous()``); it may be None when ``need_dx`` is False."""
+    torch = _torch()
+    g2 = _as_2d(g, "g")
+    m, n = g2.shape
+    k = kept.k
+    if m != kept.m:
+        raise ValueError(f"g has {m} tokens, the checkpoint {kept.m}")
+    if w_t is None and need_dx:
+        raise ValueError("dx needs w_t")
+    if w_t is not None:
+        w_t = _as_2d(w_t, "w_t")
+        if tuple(w_t.shape) != (k, n):
+            raise ValueError(f"w_t must be [{k}, {n}], got {tuple(w_t.shape)}")
+    r = 0
+    if lora_a is not None or lora_b is not None:
+        if lora_a is None or lora_b is None:
+            raise ValueError("lora_a and lora_b go together")
+        lora_a, lora_b = _as_2d(lora_a, "lora_a"), _as_2d(lora_b, "lora_b")
+        r = lora_a.shape[0]
+        if lora_a.shape[1] != k or tuple(lora_b.shape) != (n, r):
+            raise ValueError(f"LoRA shapes {tuple(lora_a.shape)}, {tuple(lora_b.shape)} do not match K={k}, N={n}")
+    dev = g2.device
+    dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev) if need_dx else None
+    lora = need_lora and r > 0
+    da = torch.empty((r, k), dtype=torch.bfloat16, device=dev) if lora else None
+    db = torch.empty((n, r), dtype=torch.bfloat16, device=dev) if lora else None
+    workspace = _workspace(workspace, backward_workspace_bytes(m, n, k, r), dev)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    with _on(dev, kept=kept.codes, w_t=w_t, lora_a=lora_a, lora_b=lora_b):
+        st = _fn("rtl_sparse_linear_backward")(
+            g2.data_ptr(), kept.codes.data_ptr(), kept.exps.data_ptr(), kept.idx.data_ptr(), kept.stats.data_ptr(),
+            ptr(w_t), ptr(lora_a) if r else None, ptr(lora_b) if r else None, m, n, k, r, float(lora_scale), ptr(dx),
+            ptr(da), ptr(db), workspace.data_ptr(), workspace.numel(), _stream())
+    _check(st, "rtl_sparse_linear_backward")
+    return None if dx is None else dx.reshape(*g.shape[:-1], k), da, db

@@ -1,0 +1,97 @@
+/*
+ * rtlynx_train.h - training the LoRA branch of the sparse layer: the layer's
+ * input kept in 8 bits, and the backward pass that reads it.
+ *
+ * The forward pass is rtl_sparse_linear (per-token compensation, LoRA on the
+ * pruned residual):
+ *
+ *   Y = s (M * X) W^T + alpha R A^T B^T,   R = X - s (M * X),
+ *   s = L1(X) / L1(M * X) per token (1 where that is 0 / 0)
+ *
+ * with M the 0/1 pattern of the kept channels.  W is frozen; A and B learn.
+ * Beside X's checkpoint the backward pass needs nothing from the forward.
+ *
+ * Conventions are those of rtlynx.h (bf16 tensors as raw words, 16-byte
+ * aligned bases, each tensor below 2 GiB counting 256 rows past its end, K a
+ * multiple of 4).
+ */
+#ifndef RTLYNX_TRAIN_H
+#define RTLYNX_TRAIN_H
+
+#include "rtlynx.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Channels that share one exponent. */
+#define RTL_CKPT_BLOCK 32
+
+/*
+ * rtl_checkpoint_pack - the input of a sparse layer in 8 bits.
+ *
+ *   x      [M, K] bf16, finite.
+ *   codes  [M, K] int8 and exps [M, ceil(K / 32)] uint8: x is stored as
+ *          code * 2^(exp - 133), exp the biased exponent of the block's
+ *          largest magnitude (so the largest code is 64 .. 127) and code the
+ *          nearest integer, ties to even, clamped to +-127.  A power of two as
+ *          the step makes every stored value exact in bf16; the error is at most
+ *          half a step, 2^-7 of the block's largest magnitude.
+ *   idx    [M, ceil(K / 8)] uint8: the kept channels of every group of 4, in
+ *          the format of rtl_sparsify_2of4 (bit-exact with it).
+ *   stats  [M, 2] fp32: s, and the L1 norm of the kept channels, of x itself.
+ *
+ * 1.16 bytes per channel instead of 2.  M == 0 is a no-op.
+ */
+rtl_status rtl_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
+                               uint8_t* idx, float* stats, void* hip_stream);
+
+/* rtl_checkpoint_unpack - y [M, K] bf16: the values that codes and exps stand
+ * for (exact). */
+rtl_status rtl_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K,
+                                 uint16_t* y, void* hip_stream);
+
+/* Device workspace of rtl_sparse_linear_backward; 0 for invalid sizes and for
+ * M == 0. */
+size_t rtl_sparse_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
+
+/*
+ * rtl_sparse_linear_backward - gradients of the layer from G = dL / dY.
+ *
+ * With X, M, s, Lk = L1 of the kept channels as the checkpoint holds them:
+ *
+ *   U  = alpha G B                      [M, r]
+ *   E  = G W - U A                      gradient at s (M * X)
+ *   D  = sum over kept channels of X E  gradient at s
+ *   dX = U A + s (M * E) + (D / Lk) sign(X) (1 - s M)     (last term 0 if Lk is 0)
+ *   dA = U^T R                          [r, K]
+ *   dB = alpha G^T (R A^T)              [N, r]
+ *
+ *   g        [M, N] bf16.
+ *   codes, exps, idx, stats: as rtl_checkpoint_pack wrote them.
+ *   w_t      [K, N] bf16, the frozen weight transposed (laid out once: it does
+ *            not change in training).  Needed for dx only.
+ *   lora_a   [r, K], lora_b [N, r] bf16; ignored when r == 0.
+ *   dx       [M, K] bf16 or NULL (a first layer's input needs no gradient).
+ *   da, db   [r, K], [N, r] bf16, both or neither; required NULL when r == 0.
+ *   workspace  rtl_sparse_linear_backward_workspace_bytes(M, N, K, r) bytes,
+ *            16-byte aligned, overwritten.
+ *
+ * N % 4 == 0 (N >= 4), K % 4 == 0, 0 <= r <= RTL_MAX_LORA_RANK.  Products have bf16
+ * operands and fp32 sums; U and R A^T are carried between them as two bf16
+ * words (16 significant bits), G W and all sums in fp32; each result is rounded
+ * once.  M == 0 writes zeros to da and db.  Deterministic: the order of every
+ * sum depends on the sizes only.
+ */
+rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* codes, const uint8_t* exps,
+                                      const uint8_t* idx, const float* stats, const uint16_t* w_t,
+                                      const uint16_t* lora_a, const uint16_t* lora_b, int64_t M,
+                                      int64_t N, int64_t K, int64_t r, float lora_scale,
+                                      uint16_t* dx, uint16_t* da, uint16_t* db, void* workspace,
+                                      size_t workspace_bytes, void* hip_stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* RTLYNX_TRAIN_H */
