@@ -1,34 +1,37 @@
 // rtl_sparse_linear_backward (include/rtlynx_train.h).
 //
 // The work is one large product, G W [M, K] over N channels, which runs on the
-// dense GEMM's ring (dense_gemm.hip, fp32 result), and the LoRA branch, whose
-// products all have one dimension of at most 128 and are bound by reading G
-// and the checkpoint:
+// dense GEMM's ring (dense_gemm.hip), and the LoRA branch, whose products all
+// have one dimension of at most 128 and are bound by reading G and the
+// checkpoint:
 //
-//   1. transpose_factors   A as [r][K] and [K][r], B as [r][N], zero-padded, so
-//                          every operand is contiguous along its contraction.
-//   2. rows_kernel         G B, and of the checkpoint (pruned A^T) and (kept
-//                          A^T): token-by-rank products over the channels, split
-//                          over channel ranges.
-//   3. join_rows           sums the ranges in order, forms U = alpha G B and
-//                          T = alpha (pruned A^T + (1 - s) kept A^T), the part of D
-//                          that needs no G W, and lays U, (1 - s) U and T out for
-//                          the products that follow, each as two bf16 words (hi + lo: 16 bits).
-//   4. columns_kernel      G^T T and [pruned; kept]^T [U; (1 - s) U]: products over the
-//                          tokens, split over token ranges.  Both operands run along
-//                          tokens, which are rows in memory: the tile goes through
-//                          LDS and is read transposed (ds_read_b64_tr_b16).
-//   5. join_columns        sums the ranges in order into dA and dB.
-//   6. the dense GEMM      P = G W.
-//   7. finish_kernel       D per token, then dX; U A is formed again, a 16-token
-//                          strip at a time, on the matrix cores (r is small), so it
-//                          never goes to memory.
+//   1. factors_kernel       A and B as matrix-core fragments, zero-padded.
+//   2. rows_kernel          G B, and of the checkpoint (pruned A^T) and (kept
+//                           A^T): token-by-rank products over the channels.
+//   3. join_rows_kernel     sums the channel ranges in order, forms U = alpha G B,
+//                           T = alpha (pruned A^T + (1 - s) kept A^T) and the part
+//                           of D that needs no G W, and writes U, (1 - s) U and T as
+//                           the fragments of the products that follow, each value as
+//                           two bf16 words (hi + lo: 16 significant bits).
+//   4. columns_kernel       G^T T and [pruned; kept]^T [U; (1 - s) U]: products over
+//                           the tokens.  Both operands run along tokens, which are
+//                           rows in memory: the tile goes through LDS and is read
+//                           transposed (ds_read_b64_tr_b16).
+//   5. join_columns_kernel  sums the token ranges in order into dA and dB.
+//   6. the dense GEMM       P = G W, in 16 x 16 blocks of fp32.
+//   7. finish_kernel        D per token, then dX; U A is formed again, a 16-token
+//                           strip at a time, on the matrix cores (r is small), so it
+//                           never goes to memory.
 //
 // A kept value's residual (1 - s) x is not a bf16 number; multiplying U (or the
 // joined sum) by 1 - s instead keeps the checkpoint's values exact operands.
+//
+// Fragments instead of transposed matrices: a matrix whose rows are N channels
+// apart puts the 16 rows of an operand load on one memory channel; as 1 KiB
+// blocks in the order of use every such load is contiguous.
 #include "rtl_checkpoint.hpp"
 #include "rtl_common.hpp"
-#include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 
 namespace rtl {
 
@@ -37,10 +40,19 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // fp32 as two bf16 words: hi + lo holds 16 significant bits.
-__device__ __forceinline__ void split_bf16(float v, uint16_t& hi, uint16_t& lo) {
-  const uint32_t h = f32_to_bf16_rne(v);
-  hi = (uint16_t)h;
-  lo = (uint16_t)f32_to_bf16_rne(v - __builtin_bit_cast(float, h << 16));
+struct Split {
+  u32x4 hi, lo;
+};
+__device__ __forceinline__ Split split8(const float (&v)[8]) {
+  Split r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = v[2 * i], b = v[2 * i + 1];
+    const uint32_t h = cvt_pk_bf16(a, b);
+    r.hi[i] = h;
+    r.lo[i] = cvt_pk_bf16(a - bf16_lo_to_f32(h), b - bf16_hi_to_f32(h));
+  }
+  return r;
 }
 
 // 8 channels of a row at channel c of C (C % 4 == 0): rows are 16-byte aligned
@@ -65,10 +77,7 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t c, int64_t C
   return v;
 }
 
-// The checkpoint's 8 channels at channel c: pruned and kept values apart.
-struct CkptUnit {
-  u32x4 pruned, kept;
-};
+// The checkpoint's 8 channels at channel c, raw, then pruned and kept values.
 struct CkptRaw {
   u32x2 q;
   uint32_t e, idx;
@@ -89,354 +98,466 @@ __device__ __forceinline__ CkptRaw ckpt_load(const Ckpt& k, int64_t row, int64_t
   }
   return r;
 }
-__device__ __forceinline__ CkptUnit ckpt_split(const CkptRaw& r) {
+__device__ __forceinline__ void ckpt_split(const CkptRaw& r, u32x4& pruned, u32x4& kept) {
   const u32x4 v = ckpt_values(r.q, (int)r.e), m = kept_masks(r.idx);
-  CkptUnit u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    u.kept[i] = v[i] & m[i];
-    u.pruned[i] = v[i] & ~m[i];
+    kept[i] = v[i] & m[i];
+    pruned[i] = v[i] & ~m[i];
   }
-  return u;
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// --- 1. factors ------------------------------------------------------------
-// One thread per 8 words of an output row.
-__global__ void __launch_bounds__(256)
-transpose_factors_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, BackwardLayout L,
-                         uint16_t* __restrict__ ap, uint16_t* __restrict__ at, uint16_t* __restrict__ bt) {
-  const int64_t na = L.rp * L.kp / 8, nb = L.rp * L.np / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * na + nb; i += (int64_t)gridDim.x * 256) {
-    uint16_t v[8];
-    if (i < na) {                                   // ap[j][k]: neighbouring threads along k
-      const int64_t j = i / (L.kp / 8), k = 8 * (i - j * (L.kp / 8));
-      for (int e = 0; e < 8; ++e) v[e] = j < L.r && k + e < L.K ? a[j * L.K + k + e] : 0;
-      *reinterpret_cast<u32x4*>(ap + j * L.kp + k) = *reinterpret_cast<u32x4*>(v);
-    } else if (i < 2 * na) {                        // at[k][j]: neighbouring threads along k
-      const int64_t q = i - na, j = 8 * (q / L.kp), k = q % L.kp;
-      for (int e = 0; e < 8; ++e) v[e] = j + e < L.r && k < L.K ? a[(j + e) * L.K + k] : 0;
-      *reinterpret_cast<u32x4*>(at + k * L.rp + j) = *reinterpret_cast<u32x4*>(v);
-    } else {                                        // bt[j][n]: neighbouring threads along j
-      const int64_t q = i - 2 * na, n = 8 * (q / L.rp), j = q % L.rp;
-      for (int e = 0; e < 8; ++e) v[e] = j < L.r && n + e < L.N ? b[(n + e) * L.r + j] : 0;
-      *reinterpret_cast<u32x4*>(bt + j * L.np + n) = *reinterpret_cast<u32x4*>(v);
+constexpr f32x4 kZero4 = {0, 0, 0, 0};
+
+// Sums COUNT accumulators over the 4 wavefronts of a workgroup into wavefront
+// 0, in the order (0 + 2) + (1 + 3).
+template <int COUNT>
+__device__ __forceinline__ void join_waves(f32x4* acc, f32x4* lds, int wave, int lane) {
+#pragma unroll
+  for (int half = 2; half >= 1; half /= 2) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) lds[((wave - half) * COUNT + i) * 64 + lane] = acc[i];
     }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) acc[i] += lds[(wave * COUNT + i) * 64 + lane];
+    }
+  }
+}
+
+// --- 1. factors ------------------------------------------------------------
+// One thread per lane of a fragment.  a_down [kp / 32][rp / 16]: rows ranks,
+// contraction channels; a_up [kp / 16][rp / 32]: rows channels in the order of
+// P's blocks (row 4 q + e of block t of four: channel 16 q + 4 t + e of the 64),
+// contraction ranks; b [np / 32][rp / 16]: rows ranks, contraction output channels.
+__global__ void __launch_bounds__(256)
+factors_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, BackwardLayout L,
+               u32x4* __restrict__ a_down, u32x4* __restrict__ a_up, u32x4* __restrict__ b_down) {
+  const int64_t na = L.rp * L.kp / 8, nb = L.rp * L.np / 8;
+  const int64_t jt = L.rp / 16, rt = L.rp / 32;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * na + nb; i += (int64_t)gridDim.x * 256) {
+    const int lane = (int)(i & 63), row = lane & 15, at = 8 * (lane >> 4);
+    uint32_t v[8];
+    if (i < na) {
+      const int64_t f = i >> 6, j = 16 * (f % jt) + row, k = 32 * (f / jt) + at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = j < L.r && k + e < L.K ? a[j * L.K + k + e] : 0;
+    } else if (i < 2 * na) {
+      const int64_t f = (i - na) >> 6, t = f / rt, j = 32 * (f % rt) + at;
+      const int64_t k = 64 * (t >> 2) + 16 * (row >> 2) + 4 * (t & 3) + (row & 3);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = j + e < L.r && k < L.K ? a[(j + e) * L.K + k] : 0;
+    } else {
+      const int64_t f = (i - 2 * na) >> 6, j = 16 * (f % jt) + row, n = 32 * (f / jt) + at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = j < L.r && n + e < L.N ? b[(n + e) * L.r + j] : 0;
+    }
+    const u32x4 w = {v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+    if (i < na) a_down[i] = w;
+    else if (i < 2 * na) a_up[i - na] = w;
+    else b_down[i - 2 * na] = w;
   }
 }
 
 // --- 2. token-by-rank products --------------------------------------------
-// 4 wavefronts of 32 tokens, JT tiles of 16 ranks; channels [lo, hi), a
-// multiple of 64 apart from the end.
-template <int JT, bool WIDE>
-__device__ __forceinline__ void g_rows(const uint16_t* __restrict__ g, const uint16_t* __restrict__ bt,
-                                       const BackwardLayout& L, int64_t m0, int64_t lo, int64_t hi,
+// A workgroup takes 16 MT tokens and a range of channels, its 4 wavefronts 64
+// channels in turn; each keeps the next 64 channels' loads in flight.
+template <int MT, int JT, bool WIDE>
+__device__ __forceinline__ void g_rows(const uint16_t* __restrict__ g, const u32x4* __restrict__ b,
+                                       const BackwardLayout& L, int64_t m0, int64_t lo, int64_t hi, f32x4* lds,
                                        float* __restrict__ out) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
-  f32x4 acc[2][JT];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  struct Stage {
+    u32x4 x[MT][2], w[2][JT];
+  };
+  f32x4 acc[MT * JT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MT * JT; ++i) acc[i] = kZero4;
+  const uint16_t* row[MT];
+  bool ok[MT];
 #pragma unroll
-    for (int j = 0; j < JT; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
-  const int64_t r0 = m0 + col, r1 = r0 + 16;
-  const bool ok0 = r0 < L.M, ok1 = r1 < L.M;
-  const uint16_t* g0 = g + (ok0 ? r0 : 0) * L.N;
-  const uint16_t* g1 = g + (ok1 ? r1 : 0) * L.N;
-  const uint16_t* bp = bt + (int64_t)col * L.np;
-  for (int64_t c0 = lo; c0 < hi; c0 += 64) {
-    u32x4 x0[2], x1[2], w[2][JT];
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + 16 * i + col;
+    ok[i] = m < L.M;
+    row[i] = g + (ok[i] ? m : 0) * L.N;
+  }
+  auto load = [&](Stage& s, int64_t c) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t c = c0 + 32 * h + 8 * quad;
-      x0[h] = load8<WIDE>(g0, c, L.N, ok0);
-      x1[h] = load8<WIDE>(g1, c, L.N, ok1);
 #pragma unroll
-      for (int j = 0; j < JT; ++j) w[h][j] = *reinterpret_cast<const u32x4*>(bp + (int64_t)16 * j * L.np + c);
+      for (int i = 0; i < MT; ++i) s.x[i][h] = load8<WIDE>(row[i], c + 32 * h + 8 * quad, L.N, ok[i]);
+#pragma unroll
+      for (int j = 0; j < JT; ++j) s.w[h][j] = b[((c / 32 + h) * JT + j) * 64 + lane];
     }
+  };
+  auto use = [&](const Stage& s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        acc[0][j] = mfma(x0[h], w[h][j], acc[0][j]);
-        acc[1][j] = mfma(x1[h], w[h][j], acc[1][j]);
-      }
-  }
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < JT; ++j) acc[i * JT + j] = mfma(s.x[i][h], s.w[h][j], acc[i * JT + j]);
+  };
+  Stage s0, s1;
+  int64_t c = lo + 64 * wave;
+  if (c < hi) load(s0, c);
+  for (; c < hi; c += 512) {
+    if (c + 256 < hi) load(s1, c + 256);
+    use(s0);
+    if (c + 512 < hi) load(s0, c + 512);
+    if (c + 256 < hi) use(s1);
+  }
+  join_waves<MT * JT>(acc, lds, wave, lane);
+  if (wave != 0) return;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < JT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int64_t m = m0 + 16 * i + 4 * quad + e;
-        if (m < L.M) out[m * L.rp + 16 * j + col] = acc[i][j][e];
+        if (m < L.M) out[m * L.rp + 16 * j + col] = acc[i * JT + j][e];
       }
 }
 
-template <int JT, bool WIDE>
-__device__ __forceinline__ void x_rows(const Ckpt& ck, const uint16_t* __restrict__ ap, const BackwardLayout& L,
-                                       int64_t m0, int64_t lo, int64_t hi, float* __restrict__ out_pruned,
-                                       float* __restrict__ out_kept) {
+template <int MT, int JT, bool WIDE>
+__device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__ a, const BackwardLayout& L,
+                                       int64_t m0, int64_t lo, int64_t hi, f32x4* lds, float* __restrict__ out) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
-  f32x4 pr[2][JT], ke[2][JT];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) pr[i][j] = ke[i][j] = (f32x4){0, 0, 0, 0};
-  const int64_t r0 = m0 + col, r1 = r0 + 16;
-  const bool ok0 = r0 < L.M, ok1 = r1 < L.M;
-  const uint16_t* wp = ap + (int64_t)col * L.kp;
-  for (int64_t c0 = lo; c0 < hi; c0 += 64) {
-    CkptRaw x0[2], x1[2];
-    u32x4 w[2][JT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t c = c0 + 32 * h + 8 * quad;
-      x0[h] = ckpt_load<WIDE>(ck, r0, c, L.K, ok0);
-      x1[h] = ckpt_load<WIDE>(ck, r1, c, L.K, ok1);
-#pragma unroll
-      for (int j = 0; j < JT; ++j) w[h][j] = *reinterpret_cast<const u32x4*>(wp + (int64_t)16 * j * L.kp + c);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const CkptUnit u0 = ckpt_split(x0[h]), u1 = ckpt_split(x1[h]);
-#pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        pr[0][j] = mfma(u0.pruned, w[h][j], pr[0][j]);
-        ke[0][j] = mfma(u0.kept, w[h][j], ke[0][j]);
-        pr[1][j] = mfma(u1.pruned, w[h][j], pr[1][j]);
-        ke[1][j] = mfma(u1.kept, w[h][j], ke[1][j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < JT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + 16 * i + 4 * quad + e;
-        if (m < L.M) {
-          out_pruned[m * L.rp + 16 * j + col] = pr[i][j][e];
-          out_kept[m * L.rp + 16 * j + col] = ke[i][j][e];
-        }
-      }
-}
-
-template <int JT, bool WIDE_G, bool WIDE_X>
-__global__ void __launch_bounds__(256)
-rows_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ bt, const uint16_t* __restrict__ ap, Ckpt ck,
-            BackwardLayout L, float* __restrict__ part) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t splits = L.row_splits_g + L.row_splits_x;
-  const int64_t s = blockIdx.x % splits;                // channel range: G's first, then the checkpoint's
-  const int64_t m0 = blockIdx.x / splits * 128 + 32 * wave;
-  if (m0 >= L.M) return;
-  const int64_t slab = L.M * L.rp;
-  if (s < L.row_splits_g) {
-    const int64_t lo = s * L.row_chunk, hi = lo + L.row_chunk < L.np ? lo + L.row_chunk : L.np;
-    g_rows<JT, WIDE_G>(g, bt, L, m0, lo, hi, part + s * slab);
-  } else {
-    const int64_t q = s - L.row_splits_g;
-    const int64_t lo = q * L.row_chunk, hi = lo + L.row_chunk < L.kp ? lo + L.row_chunk : L.kp;
-    float* p = part + (L.row_splits_g + 2 * q) * slab;
-    x_rows<JT, WIDE_X>(ck, ap, L, m0, lo, hi, p, p + slab);
-  }
-}
-
-// --- 3. U, T and what follows from them -------------------------------------
-// 32 tokens per workgroup.  Tokens past M are written as zeros up to mp, so the
-// products over tokens need no guard.
-__global__ void __launch_bounds__(256)
-join_rows_kernel(const float* __restrict__ part, const float* __restrict__ stats, BackwardLayout L, float alpha,
-                 uint16_t* __restrict__ u_rows, uint16_t* __restrict__ u_cols, uint16_t* __restrict__ t_cols,
-                 float* __restrict__ d_lora) {
-  extern __shared__ float lds[];                        // U and U (kept A^T) [32][rp + 1], T [32][rp]
-  const int rp = (int)L.rp, pitch = rp + 1;
-  float* const us = lds;
-  float* const ds = lds + 32 * pitch;
-  float* const ts = lds + 2 * 32 * pitch;
-  const int64_t m0 = (int64_t)blockIdx.x * 32, slab = L.M * L.rp;
-  for (int i = threadIdx.x; i < 32 * rp; i += 256) {
-    const int r = i / rp, j = i - r * rp;
-    const int64_t m = m0 + r;
-    float u = 0.f, pr = 0.f, ke = 0.f, s = 1.f;
-    if (m < L.M) {
-      const float* p = part + m * L.rp + j;
-      for (int64_t q = 0; q < L.row_splits_g; ++q) u += p[q * slab];
-      p += L.row_splits_g * slab;
-      for (int64_t q = 0; q < L.row_splits_x; ++q) {
-        pr += p[2 * q * slab];
-        ke += p[(2 * q + 1) * slab];
+  struct Stage {
+    CkptRaw x[MT][2];
+    u32x4 w[2][JT];
+  };
+  f32x4 acc[2 * MT * JT];                               // pruned, kept
+#pragma unroll
+  for (int i = 0; i < 2 * MT * JT; ++i) acc[i] = kZero4;
+  auto load = [&](Stage& s, int64_t c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + 16 * i + col;
+        s.x[i][h] = ckpt_load<WIDE>(ck, m, c + 32 * h + 8 * quad, L.K, m < L.M);
       }
-      s = stats[2 * m];
+#pragma unroll
+      for (int j = 0; j < JT; ++j) s.w[h][j] = a[((c / 32 + h) * JT + j) * 64 + lane];
     }
-    u *= alpha;
-    us[r * pitch + j] = u;
-    ds[r * pitch + j] = u * ke;                         // for D: sum over ranks of U (kept A^T)
-    const float t = alpha * (pr + (1.f - s) * ke);
-    uint16_t hi, lo;
-    if (m < L.M) {
-      split_bf16(u, hi, lo);
-      u_rows[m * 2 * L.rp + j] = hi;
-      u_rows[m * 2 * L.rp + L.rp + j] = lo;
-    }
-    ts[i] = t;
-  }
-  __syncthreads();
-  if (threadIdx.x < 32 && m0 + threadIdx.x < L.M) {
-    float d = 0.f;
-    for (int j = 0; j < rp; ++j) d += ds[threadIdx.x * pitch + j];
-    d_lora[m0 + threadIdx.x] = d;
-  }
-  // Transposed: lanes along tokens.
-  const int r = threadIdx.x & 31;
-  const int64_t m = m0 + r;
-  const float keep = m < L.M ? 1.f - stats[2 * m] : 0.f;
-  for (int j = threadIdx.x >> 5; j < rp; j += 8) {
-    uint16_t hi, lo;
-    const float u = us[r * pitch + j];
-    split_bf16(u, hi, lo);
-    u_cols[(int64_t)j * L.mp + m] = hi;
-    u_cols[(int64_t)(L.rp + j) * L.mp + m] = lo;
-    split_bf16(u * keep, hi, lo);
-    u_cols[(int64_t)(2 * L.rp + j) * L.mp + m] = hi;
-    u_cols[(int64_t)(3 * L.rp + j) * L.mp + m] = lo;
-    split_bf16(ts[r * rp + j], hi, lo);
-    t_cols[(int64_t)j * L.mp + m] = hi;
-    t_cols[(int64_t)(L.rp + j) * L.mp + m] = lo;
-  }
-}
-
-// --- 4. products over tokens ------------------------------------------------
-// A workgroup's tile: 64 tokens x 128 channels in LDS, 4 wavefronts of 32
-// channels.  Row pitch 272 bytes: 16-byte aligned, rows shifted by 4 banks.
-constexpr int kColPitch = 136;                          // bf16 words
-constexpr int kColTile = 64 * kColPitch;
-
-// The operand of 16 channels (from c) x 32 tokens (from t) of such a tile:
-// lane l gets tokens 8 (l / 16) + [0, 8) of channel l % 16.  One transposing
-// read gives a lane 4 tokens: its 16 lanes name 4 rows of 16 channels.
-__device__ __forceinline__ u32x4 transposed_operand(const uint16_t* tile, int t, int c) {
-  const int lane = threadIdx.x & 63;
-  const uint16_t* p = tile + (t + 8 * (lane >> 4) + ((lane & 15) >> 2)) * kColPitch + c + 4 * (lane & 3);
-  using lds_s16x4 = __attribute__((address_space(3))) s16x4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * kColPitch));
-  const u32x2 a2 = __builtin_bit_cast(u32x2, a), b2 = __builtin_bit_cast(u32x2, b);
-  return (u32x4){a2[0], a2[1], b2[0], b2[1]};
-}
-
-template <int JT, bool WIDE_G, bool WIDE_X>
-__global__ void __launch_bounds__(256)
-columns_kernel(const uint16_t* __restrict__ g, Ckpt ck, const uint16_t* __restrict__ u_cols,
-               const uint16_t* __restrict__ t_cols, BackwardLayout L, float* __restrict__ part) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[2 * kColTile];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, quad = lane >> 4;
-  const int64_t tiles_g = (L.N + 127) / 128;
-  const bool is_g = (int64_t)blockIdx.x < tiles_g;
-  const int64_t c0 = 128 * (is_g ? (int64_t)blockIdx.x : (int64_t)blockIdx.x - tiles_g);
-  const int64_t t_lo = (int64_t)blockIdx.y * L.col_chunk;
-  const int64_t t_hi = t_lo + L.col_chunk < L.mp ? t_lo + L.col_chunk : L.mp;
-  const int lr = threadIdx.x >> 4, lc = 8 * (threadIdx.x & 15);   // loader: rows lr + 16 i, channels c0 + lc
-  f32x4 acc[2][JT];
+  };
+  auto use = [&](const Stage& s) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < JT; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
-
-  if (is_g) {
-    u32x4 v[4];
-    auto load = [&](int64_t t0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = t0 + lr + 16 * i;
-        v[i] = load8<WIDE_G>(g + (m < L.M ? m : 0) * L.N, c0 + lc, L.N, m < L.M);
-      }
-    };
-    const uint16_t* q = t_cols + (int64_t)col * L.mp + 8 * quad;
-    load(t_lo);
-    for (int64_t t0 = t_lo; t0 < t_hi; t0 += 64) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(tile + (lr + 16 * i) * kColPitch + lc) = v[i];
-      __syncthreads();
-      if (t0 + 64 < t_hi) load(t0 + 64);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 x0 = transposed_operand(tile, 32 * h, 32 * wave), x1 = transposed_operand(tile, 32 * h, 32 * wave + 16);
+      for (int i = 0; i < MT; ++i) {
+        u32x4 pruned, kept;
+        ckpt_split(s.x[i][h], pruned, kept);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
-          const uint16_t* w = q + (int64_t)16 * j * L.mp + t0 + 32 * h;
-          const u32x4 hi = *reinterpret_cast<const u32x4*>(w), lo = *reinterpret_cast<const u32x4*>(w + L.rp * L.mp);
-          acc[0][j] = mfma(x0, hi, acc[0][j]);
-          acc[1][j] = mfma(x1, hi, acc[1][j]);
-          acc[0][j] = mfma(x0, lo, acc[0][j]);
-          acc[1][j] = mfma(x1, lo, acc[1][j]);
+          acc[i * JT + j] = mfma(pruned, s.w[h][j], acc[i * JT + j]);
+          acc[(MT + i) * JT + j] = mfma(kept, s.w[h][j], acc[(MT + i) * JT + j]);
         }
       }
-    }
-    float* out = part + (int64_t)blockIdx.y * L.N * L.rp;
+  };
+  Stage s0, s1;
+  int64_t c = lo + 64 * wave;
+  if (c < hi) load(s0, c);
+  for (; c < hi; c += 512) {
+    if (c + 256 < hi) load(s1, c + 256);
+    use(s0);
+    if (c + 512 < hi) load(s0, c + 512);
+    if (c + 256 < hi) use(s1);
+  }
+  join_waves<2 * MT * JT>(acc, lds, wave, lane);
+  if (wave != 0) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < JT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t n = c0 + 32 * wave + 16 * i + 4 * quad + e;
-          if (n < L.N) out[n * L.rp + 16 * j + col] = acc[i][j][e];
+          const int64_t m = m0 + 16 * i + 4 * quad + e;
+          if (m < L.M) out[(p * L.M + m) * L.rp + 16 * j + col] = acc[(p * MT + i) * JT + j][e];
         }
+}
+
+template <int JT, bool WIDE_G, bool WIDE_X>
+__global__ void __launch_bounds__(256)
+rows_kernel(const uint16_t* __restrict__ g, const u32x4* __restrict__ b, const u32x4* __restrict__ a, Ckpt ck,
+            BackwardLayout L, float* __restrict__ part) {
+  constexpr int kG = JT == 8 ? 2 : 4, kX = kG / 2;      // 16-token tiles per workgroup
+  __shared__ f32x4 lds[2 * kG * JT * 64];
+  const int64_t groups_g = (L.M + 16 * kG - 1) / (16 * kG) * L.splits_g;
+  const int64_t slab = L.M * L.rp;
+  int64_t id = blockIdx.x;
+  if (id < groups_g) {
+    const int64_t s = id % L.splits_g, lo = s * L.chunk_g, hi = lo + L.chunk_g < L.np ? lo + L.chunk_g : L.np;
+    g_rows<kG, JT, WIDE_G>(g, b, L, id / L.splits_g * (16 * kG), lo, hi, lds, part + s * slab);
   } else {
-    CkptRaw v[4];
-    auto load = [&](int64_t t0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = t0 + lr + 16 * i;
-        v[i] = ckpt_load<WIDE_X>(ck, m, c0 + lc, L.K, m < L.M);
-      }
-    };
-    const uint16_t* q = u_cols + (int64_t)col * L.mp + 8 * quad;
-    load(t_lo);
-    for (int64_t t0 = t_lo; t0 < t_hi; t0 += 64) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const CkptUnit u = ckpt_split(v[i]);
-        *reinterpret_cast<u32x4*>(tile + (lr + 16 * i) * kColPitch + lc) = u.pruned;
-        *reinterpret_cast<u32x4*>(tile + kColTile + (lr + 16 * i) * kColPitch + lc) = u.kept;
-      }
-      __syncthreads();
-      if (t0 + 64 < t_hi) load(t0 + 64);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int part_of = 0; part_of < 2; ++part_of) {    // pruned with U, kept with (1 - s) U
-          const uint16_t* src = tile + part_of * kColTile;
-          const u32x4 x0 = transposed_operand(src, 32 * h, 32 * wave), x1 = transposed_operand(src, 32 * h, 32 * wave + 16);
-#pragma unroll
-          for (int j = 0; j < JT; ++j) {
-            const uint16_t* w = q + (2 * part_of * L.rp + 16 * j) * L.mp + t0 + 32 * h;
-            const u32x4 hi = *reinterpret_cast<const u32x4*>(w), lo = *reinterpret_cast<const u32x4*>(w + L.rp * L.mp);
-            acc[0][j] = mfma(x0, hi, acc[0][j]);
-            acc[1][j] = mfma(x1, hi, acc[1][j]);
-            acc[0][j] = mfma(x0, lo, acc[0][j]);
-            acc[1][j] = mfma(x1, lo, acc[1][j]);
-          }
-        }
-      }
-    }
-    float* out = part + (int64_t)L.col_splits * L.N * L.rp + (int64_t)blockIdx.y * L.kp * L.rp;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const int64_t k = c0 + 32 * wave + 16 * i + 4 * quad;
-        if (k < L.K) *reinterpret_cast<f32x4*>(out + (int64_t)(16 * j + col) * L.kp + k) = acc[i][j];
-      }
+    id -= groups_g;
+    const int64_t s = id % L.splits_x, lo = s * L.chunk_x, hi = lo + L.chunk_x < L.kp ? lo + L.chunk_x : L.kp;
+    x_rows<kX, JT, WIDE_X>(ck, a, L, id / L.splits_x * (16 * kX), lo, hi, lds, part + (L.splits_g + 2 * s) * slab);
   }
+}
+
+// --- 3. U, T and what follows from them -------------------------------------
+// 32 tokens per workgroup: one contraction step of the products over tokens.
+// Tokens past M are written as zeros.  u [mp / 16][rp / 32][hi, lo]: rows tokens,
+// contraction ranks; uc [mp / 32][U, (1 - s) U][rp / 16][hi, lo] and
+// tc [mp / 32][rp / 16][hi, lo]: rows ranks, contraction tokens.
+constexpr int kJoinThreads = 512;
+
+template <int RP>
+__global__ void __launch_bounds__(kJoinThreads)
+join_rows_kernel(const float* __restrict__ part, const float* __restrict__ stats, BackwardLayout L, float alpha,
+                 u32x4* __restrict__ u_out, u32x4* __restrict__ uc_out, u32x4* __restrict__ tc_out,
+                 float* __restrict__ d_lora) {
+  constexpr int kPitch = RP + 4;
+  __shared__ __attribute__((aligned(16))) float us[32 * kPitch], ts[32 * kPitch], ds[32 * (RP / 4 + 1)];
+  const int64_t m0 = (int64_t)blockIdx.x * 32, slab = L.M * RP;
+#pragma unroll
+  for (int i = threadIdx.x; i < 32 * RP / 4; i += kJoinThreads) {
+    const int r = i / (RP / 4), j = 4 * (i % (RP / 4));
+    const int64_t m = m0 + r;
+    f32x4 u = kZero4, pr = kZero4, ke = kZero4;
+    float keep = 0.f;
+    if (m < L.M) {
+      const float* p = part + m * RP + j;
+#pragma unroll 4
+      for (int64_t q = 0; q < L.splits_g; ++q) u += *reinterpret_cast<const f32x4*>(p + q * slab);
+      p += L.splits_g * slab;
+#pragma unroll 2
+      for (int64_t q = 0; q < L.splits_x; ++q) {
+        pr += *reinterpret_cast<const f32x4*>(p + 2 * q * slab);
+        ke += *reinterpret_cast<const f32x4*>(p + (2 * q + 1) * slab);
+      }
+      keep = 1.f - stats[2 * m];
+    }
+    f32x4 t;
+    float d = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[e] *= alpha;
+      d += u[e] * ke[e];                                // of D: U (kept A^T), summed over the ranks below
+      t[e] = alpha * (pr[e] + keep * ke[e]);
+    }
+    *reinterpret_cast<f32x4*>(us + r * kPitch + j) = u;
+    *reinterpret_cast<f32x4*>(ts + r * kPitch + j) = t;
+    ds[r * (RP / 4 + 1) + j / 4] = d;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    float d = 0.f;
+#pragma unroll
+    for (int j = 0; j < RP / 4; ++j) d += ds[threadIdx.x * (RP / 4 + 1) + j];
+    d_lora[m0 + threadIdx.x] = d;
+  }
+  for (int i = threadIdx.x; i < 2 * (RP / 32) * 64; i += kJoinThreads) {      // u
+    const int lane = i & 63, f = i >> 6, tile = f / (RP / 32), step = f % (RP / 32);
+    const float* p = us + (16 * tile + (lane & 15)) * kPitch + 32 * step + 8 * (lane >> 4);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[e];
+    const Split s = split8(v);
+    u32x4* o = u_out + (((m0 / 16 + tile) * (RP / 32) + step) * 2) * 64 + lane;
+    o[0] = s.hi;
+    o[64] = s.lo;
+  }
+  for (int i = threadIdx.x; i < (RP / 16) * 64; i += kJoinThreads) {          // uc, tc
+    const int lane = i & 63, jt = i >> 6, j = 16 * jt + (lane & 15), r0 = 8 * (lane >> 4);
+    float u[8], k[8], t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t m = m0 + r0 + e;
+      u[e] = us[(r0 + e) * kPitch + j];
+      k[e] = u[e] * (m < L.M ? 1.f - stats[2 * m] : 0.f);
+      t[e] = ts[(r0 + e) * kPitch + j];
+    }
+    u32x4* o = uc_out + ((int64_t)blockIdx.x * 2 * (RP / 16) + jt) * 128 + lane;
+    Split s = split8(u);
+    o[0] = s.hi;
+    o[64] = s.lo;
+    s = split8(k);
+    o += (RP / 16) * 128;
+    o[0] = s.hi;
+    o[64] = s.lo;
+    s = split8(t);
+    o = tc_out + ((int64_t)blockIdx.x * (RP / 16) + jt) * 128 + lane;
+    o[0] = s.hi;
+    o[64] = s.lo;
+  }
+}
+
+// --- 4. products over tokens ------------------------------------------------
+// A workgroup takes 16 CT channels and a range of tokens, its 4 wavefronts 32
+// tokens in turn.  Each stages its own 32 tokens in LDS (row pitch: 16 bytes
+// past the row, aligned, rows 4 banks apart) and needs no barrier.
+template <int CT>
+constexpr int col_pitch() { return 16 * CT + 8; }       // bf16 words
+
+// The operand of 16 channels (from c) x 32 tokens of such a tile: lane l gets
+// tokens 8 (l / 16) + [0, 8) of channel c + l % 16.  One transposing read
+// gives a lane 4 tokens: its 16 lanes name 4 rows of 16 channels.
+template <int CT>
+__device__ __forceinline__ u32x4 transposed_operand(const uint16_t* tile, int c) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* p = tile + (8 * (lane >> 4) + ((lane & 15) >> 2)) * col_pitch<CT>() + c + 4 * (lane & 3);
+  using lds_s16x4 = __attribute__((address_space(3))) s16x4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * col_pitch<CT>()));
+  const u32x2 a2 = __builtin_bit_cast(u32x2, a), b2 = __builtin_bit_cast(u32x2, b);
+  return (u32x4){a2[0], a2[1], b2[0], b2[1]};
+}
+
+// One 32-token step of one staged tile against its fragments (hi, lo).
+template <int CT, int JT>
+__device__ __forceinline__ void col_step(const uint16_t* tile, const u32x4 (&w)[2 * JT], f32x4* acc) {
+#pragma unroll
+  for (int i = 0; i < CT; ++i) {
+    const u32x4 x = transposed_operand<CT>(tile, 16 * i);
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+      acc[i * JT + j] = mfma(x, w[2 * j], acc[i * JT + j]);
+      acc[i * JT + j] = mfma(x, w[2 * j + 1], acc[i * JT + j]);
+    }
+  }
+}
+
+// Where a lane's loads go in a wavefront's tile: 16 bytes of rows lr, lr +
+// kRows, ...
+template <int CT>
+struct ColTile {
+  static constexpr int kLanes = 2 * CT, kRows = 64 / kLanes, kLoads = 32 / kRows;
+  static constexpr int kWords = 32 * col_pitch<CT>();
+  static constexpr int kStage = 4 * kWords * 2;         // bytes, all four wavefronts
+};
+
+template <int CT, int JT, bool WIDE>
+__device__ __forceinline__ void g_columns(const uint16_t* __restrict__ g, const u32x4* __restrict__ tc,
+                                          const BackwardLayout& L, int64_t c0, int64_t lo, int64_t hi, char* lds,
+                                          float* __restrict__ out) {
+  using T = ColTile<CT>;
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint16_t* const tile = reinterpret_cast<uint16_t*>(lds) + wave * T::kWords;
+  const int lr = lane / T::kLanes, lc = 8 * (lane % T::kLanes);
+  uint16_t* const dst = tile + lr * col_pitch<CT>() + lc;
+  f32x4 acc[CT * JT];
+#pragma unroll
+  for (int i = 0; i < CT * JT; ++i) acc[i] = kZero4;
+  u32x4 v[T::kLoads], w[2 * JT];
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) {
+      const int64_t m = t + lr + T::kRows * i;
+      v[i] = load8<WIDE>(g + (m < L.M ? m : 0) * L.N, c0 + lc, L.N, m < L.M);
+    }
+  };
+  int64_t t = lo + 32 * wave;
+  if (t < hi) load(t);
+  for (; t < hi; t += 128) {
+#pragma unroll
+    for (int i = 0; i < 2 * JT; ++i) w[i] = tc[(t / 32 * 2 * JT + i) * 64 + lane];
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) *reinterpret_cast<u32x4*>(dst + T::kRows * i * col_pitch<CT>()) = v[i];
+    if (t + 128 < hi) load(t + 128);
+    __builtin_amdgcn_wave_barrier();
+    col_step<CT, JT>(tile, w, acc);
+    __builtin_amdgcn_wave_barrier();
+  }
+  join_waves<CT * JT>(acc, reinterpret_cast<f32x4*>(lds), wave, lane);
+  if (wave != 0) return;
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t n = c0 + 16 * i + 4 * quad + e;
+        if (n < L.N) out[n * L.rp + 16 * j + col] = acc[i * JT + j][e];
+      }
+}
+
+template <int CT, int JT, bool WIDE>
+__device__ __forceinline__ void x_columns(const Ckpt& ck, const u32x4* __restrict__ uc, const BackwardLayout& L,
+                                          int64_t c0, int64_t lo, int64_t hi, char* lds, float* __restrict__ out) {
+  using T = ColTile<CT>;
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint16_t* const tile = reinterpret_cast<uint16_t*>(lds) + wave * T::kWords;
+  const int lr = lane / T::kLanes, lc = 8 * (lane % T::kLanes);
+  uint16_t* const dst = tile + lr * col_pitch<CT>() + lc;
+  f32x4 acc[CT * JT];
+#pragma unroll
+  for (int i = 0; i < CT * JT; ++i) acc[i] = kZero4;
+  CkptRaw v[T::kLoads];
+  u32x4 w[2 * JT];
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) {
+      const int64_t m = t + lr + T::kRows * i;
+      v[i] = ckpt_load<WIDE>(ck, m, c0 + lc, L.K, m < L.M);
+    }
+  };
+  int64_t t = lo + 32 * wave;
+  if (t < hi) load(t);
+  for (; t < hi; t += 128) {
+    u32x4 kept[T::kLoads];
+#pragma unroll
+    for (int i = 0; i < 2 * JT; ++i) w[i] = uc[(t / 32 * 4 * JT + i) * 64 + lane];
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) {
+      u32x4 pruned;
+      ckpt_split(v[i], pruned, kept[i]);
+      *reinterpret_cast<u32x4*>(dst + T::kRows * i * col_pitch<CT>()) = pruned;
+    }
+    if (t + 128 < hi) load(t + 128);
+    __builtin_amdgcn_wave_barrier();
+    col_step<CT, JT>(tile, w, acc);                     // pruned with U
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 2 * JT; ++i) w[i] = uc[(t / 32 * 4 * JT + 2 * JT + i) * 64 + lane];
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) *reinterpret_cast<u32x4*>(dst + T::kRows * i * col_pitch<CT>()) = kept[i];
+    __builtin_amdgcn_wave_barrier();
+    col_step<CT, JT>(tile, w, acc);                     // kept with (1 - s) U
+    __builtin_amdgcn_wave_barrier();
+  }
+  join_waves<CT * JT>(acc, reinterpret_cast<f32x4*>(lds), wave, lane);
+  if (wave != 0) return;
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+      const int64_t k = c0 + 16 * i + 4 * quad;
+      if (k < L.K) *reinterpret_cast<f32x4*>(out + (int64_t)(16 * j + col) * L.kp + k) = acc[i * JT + j];
+    }
+}
+
+// CT: 16-channel tiles of G per workgroup; half as many of the checkpoint,
+// whose step needs twice the operands.
+template <int CT, int JT, bool WIDE_G, bool WIDE_X>
+__global__ void __launch_bounds__(256, 2)
+columns_kernel(const uint16_t* __restrict__ g, Ckpt ck, const u32x4* __restrict__ uc, const u32x4* __restrict__ tc,
+               BackwardLayout L, float* __restrict__ part) {
+  constexpr int kJoin = 2 * CT * JT * 64 * 16;
+  __shared__ __attribute__((aligned(16))) char lds[kJoin > ColTile<CT>::kStage ? kJoin : ColTile<CT>::kStage];
+  const int64_t tiles_g = (L.N + 16 * CT - 1) / (16 * CT), id = blockIdx.x;
+  const int64_t lo = (int64_t)blockIdx.y * L.chunk_t, hi = lo + L.chunk_t < L.mp ? lo + L.chunk_t : L.mp;
+  if (id < tiles_g)
+    g_columns<CT, JT, WIDE_G>(g, tc, L, 16 * CT * id, lo, hi, lds, part + (int64_t)blockIdx.y * L.N * L.rp);
+  else
+    x_columns<CT / 2, JT, WIDE_X>(ck, uc, L, 8 * CT * (id - tiles_g), lo, hi, lds,
+                                  part + (L.splits_t * L.N + (int64_t)blockIdx.y * L.kp) * L.rp);
 }
 
 // --- 5. dA and dB -------------------------------------------------------------
@@ -444,32 +565,42 @@ __global__ void __launch_bounds__(256)
 join_columns_kernel(const float* __restrict__ part, BackwardLayout L, uint16_t* __restrict__ da,
                     uint16_t* __restrict__ db) {
   const int64_t nb = L.N * L.r, na = L.r * L.K;
-  const float* pa = part + L.col_splits * L.N * L.rp;
+  const float* pa = part + L.splits_t * L.N * L.rp;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nb + na; i += (int64_t)gridDim.x * 256) {
     float v = 0.f;
     if (i < nb) {
       const int64_t n = i / L.r, j = i - n * L.r;
-      for (int64_t s = 0; s < L.col_splits; ++s) v += part[(s * L.N + n) * L.rp + j];
+#pragma unroll 4
+      for (int64_t s = 0; s < L.splits_t; ++s) v += part[(s * L.N + n) * L.rp + j];
       db[i] = (uint16_t)f32_to_bf16_rne(v);
     } else {
       const int64_t q = i - nb, j = q / L.K, k = q - j * L.K;
-      for (int64_t s = 0; s < L.col_splits; ++s) v += pa[(s * L.rp + j) * L.kp + k];
+#pragma unroll 4
+      for (int64_t s = 0; s < L.splits_t; ++s) v += pa[(s * L.rp + j) * L.kp + k];
       da[q] = (uint16_t)f32_to_bf16_rne(v);
     }
   }
 }
 
 // --- 7. dX -----------------------------------------------------------------------
-// 16 tokens per workgroup, 8 wavefronts along the channels.  A lane's unit is
-// the 4 channels (one group) of a token that the matrix core's result layout
-// gives it: token l % 16, channels 4 (l / 16) + [0, 4) of 16.
+// 16 tokens per workgroup, 8 wavefronts along the channels, 64 channels (four of
+// P's blocks) at a time: lane l has token l % 16, channels 16 (l / 16) + [0, 16),
+// i.e. 16 bytes of codes, one exponent, two position bytes and 32 bytes of dX.
+// dX needs D first, a sum over the whole token.  With HOLD > 0 a wavefront keeps
+// what it read (HOLD times 64 channels: tokens of up to 512 HOLD channels) in
+// registers over that sum; otherwise it reads P and the checkpoint again.
 constexpr int kFinWaves = 8;
 
-template <int RT>                                       // rp / 32, 0 without LoRA
+struct FinUnit {
+  f32x4 p[4];                                           // P of channels 4 t + [0, 4)
+  u32x4 codes;
+  uint32_t exp, idx;
+};
+
+template <int RT, int HOLD>                             // RT: rp / 32, 0 without LoRA
 __global__ void __launch_bounds__(64 * kFinWaves)
-finish_kernel(const float* __restrict__ p, Ckpt ck, const uint16_t* __restrict__ u_rows,
-              const uint16_t* __restrict__ at, const float* __restrict__ d_lora, BackwardLayout L,
-              uint16_t* __restrict__ dx) {
+finish_kernel(const float* __restrict__ p, Ckpt ck, const u32x4* __restrict__ u, const u32x4* __restrict__ a_up,
+              const float* __restrict__ d_lora, BackwardLayout L, uint16_t* __restrict__ dx) {
   __shared__ float red[kFinWaves][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
@@ -480,21 +611,58 @@ finish_kernel(const float* __restrict__ p, Ckpt ck, const uint16_t* __restrict__
   const int8_t* codes = ck.codes + row * L.K;
   const uint8_t* exps = ck.exps + row * ((L.K + 31) / 32);
   const uint8_t* idx = ck.idx + row * ((L.K + 7) / 8);
-  const float* pr = p + row * L.K;
-  const int64_t tiles = (L.K + 15) / 16;
+  const int64_t steps = L.kp / 64;
+  const f32x4* pr = reinterpret_cast<const f32x4*>(p) + (int64_t)blockIdx.x * steps * 256 + lane;
 
+  // Channels past K have code 0 and count as pruned; nothing past a row is read.
+  auto load = [&](FinUnit& f, int64_t t) {
+    const int64_t k = 64 * t + 16 * quad;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.p[i] = pr[(4 * t + i) * 64];
+    f.codes = (u32x4){0, 0, 0, 0};
+    f.exp = f.idx = 0;
+    if (k + 16 <= L.K) {
+      __builtin_memcpy(&f.codes, codes + k, 16);
+      f.exp = exps[k / 32];
+      uint16_t two;
+      __builtin_memcpy(&two, idx + k / 8, 2);
+      f.idx = two;
+    } else if (k < L.K) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + 4 * i < L.K) f.codes[i] = *reinterpret_cast<const uint32_t*>(codes + k + 4 * i);
+      f.exp = exps[k / 32];
+      f.idx = idx[k / 8];
+      if (k + 8 < L.K) f.idx |= (uint32_t)idx[k / 8 + 1] << 8;
+    }
+  };
+  auto partial = [&](const FinUnit& f) {
+    float d = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = kept_bits(f.idx >> (4 * i)), q = f.codes[i];
+      d += (b & 1u) ? (float)((int)(q << 24) >> 24) * f.p[i][0] : 0.f;
+      d += (b & 2u) ? (float)((int)(q << 16) >> 24) * f.p[i][1] : 0.f;
+      d += (b & 4u) ? (float)((int)(q << 8) >> 24) * f.p[i][2] : 0.f;
+      d += (b & 8u) ? (float)((int)q >> 24) * f.p[i][3] : 0.f;
+    }
+    return __builtin_amdgcn_ldexpf(d, (int)f.exp - 133);
+  };
+
+  FinUnit held[HOLD > 0 ? HOLD : 1];
   float d = 0.f;
-  for (int64_t t = wave; t < tiles; t += kFinWaves) {
-    const int64_t k = 16 * t + 4 * quad;
-    if (k < L.K) {
-      const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + k);
-      const int e = exps[k / 32];
-      const uint32_t b = kept_bits((uint32_t)idx[k / 8] >> (k & 4));
-      const f32x4 v = *reinterpret_cast<const f32x4*>(pr + k);
-      d += (b & 1u) ? ckpt_value<0>(q, e) * v[0] : 0.f;
-      d += (b & 2u) ? ckpt_value<1>(q, e) * v[1] : 0.f;
-      d += (b & 4u) ? ckpt_value<2>(q, e) * v[2] : 0.f;
-      d += (b & 8u) ? ckpt_value<3>(q, e) * v[3] : 0.f;
+  if constexpr (HOLD > 0) {
+#pragma unroll
+    for (int h = 0; h < HOLD; ++h)
+      if (wave + kFinWaves * h < steps) load(held[h], wave + kFinWaves * h);
+#pragma unroll
+    for (int h = 0; h < HOLD; ++h)
+      if (wave + kFinWaves * h < steps) d += partial(held[h]);
+  } else {
+#pragma unroll 2
+    for (int64_t t = wave; t < steps; t += kFinWaves) {
+      load(held[0], t);
+      d += partial(held[0]);
     }
   }
   d += __shfl_xor(d, 16, 64);
@@ -511,70 +679,88 @@ finish_kernel(const float* __restrict__ p, Ckpt ck, const uint16_t* __restrict__
   u32x4 uh[RT > 0 ? RT : 1], ul[RT > 0 ? RT : 1];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    const uint16_t* u = u_rows + row * 2 * L.rp + 32 * i + 8 * quad;
-    uh[i] = *reinterpret_cast<const u32x4*>(u);
-    ul[i] = *reinterpret_cast<const u32x4*>(u + L.rp);
+    uh[i] = u[(((int64_t)blockIdx.x * RT + i) * 2) * 64 + lane];
+    ul[i] = u[(((int64_t)blockIdx.x * RT + i) * 2 + 1) * 64 + lane];
   }
-  for (int64_t t = wave; t < tiles; t += kFinWaves) {
-    f32x4 v = {0, 0, 0, 0};
+  auto finish = [&](const FinUnit& f, int64_t t) {
+    uint32_t out[8];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(at + (16 * t + col) * L.rp + 32 * i + 8 * quad);
-      v = mfma(a, uh[i], v);
-      v = mfma(a, ul[i], v);
-    }
-    const int64_t k = 16 * t + 4 * quad;
-    if (ok && k < L.K) {
-      const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + k);
-      const uint32_t b = kept_bits((uint32_t)idx[k / 8] >> (k & 4));
-      const f32x4 e = *reinterpret_cast<const f32x4*>(pr + k);
+    for (int n = 0; n < 4; ++n) {
+      f32x4 v = kZero4;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const u32x4 a = a_up[((4 * t + n) * RT + i) * 64 + lane];
+        v = mfma(a, uh[i], v);
+        v = mfma(a, ul[i], v);
+      }
+      const uint32_t b = kept_bits(f.idx >> (4 * n)), q = f.codes[n];
       float o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = (int)(q << (24 - 8 * i)) >> 24;
         const float sign = c > 0 ? 1.f : c < 0 ? -1.f : 0.f;
-        o[i] = (b >> i) & 1u ? v[i] + s * (e[i] - v[i]) + sign * per_kept : v[i] + sign * per;
+        o[i] = (b >> i) & 1u ? v[i] + s * (f.p[n][i] - v[i]) + sign * per_kept : v[i] + sign * per;
       }
-      *reinterpret_cast<u32x2*>(dx + row * L.K + k) = (u32x2){pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+      out[2 * n] = cvt_pk_bf16(o[0], o[1]);
+      out[2 * n + 1] = cvt_pk_bf16(o[2], o[3]);
+    }
+    const int64_t k = 64 * t + 16 * quad;
+    uint16_t* y = dx + row * L.K + k;
+    if (ok && k + 16 <= L.K) {
+      __builtin_memcpy(__builtin_assume_aligned(y, 8), out, 32);
+    } else if (ok) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + 4 * i < L.K) *reinterpret_cast<u32x2*>(y + 4 * i) = (u32x2){out[2 * i], out[2 * i + 1]};
+    }
+  };
+  if constexpr (HOLD > 0) {
+#pragma unroll
+    for (int h = 0; h < HOLD; ++h)
+      if (wave + kFinWaves * h < steps) finish(held[h], wave + kFinWaves * h);
+  } else {
+    for (int64_t t = wave; t < steps; t += kFinWaves) {
+      load(held[0], t);
+      finish(held[0], t);
     }
   }
+}
+
+template <int RT>
+hipError_t launch_finish(const float* p, const Ckpt& ck, const BackwardLayout& L, const char* ws, uint16_t* dx,
+                         hipStream_t stream) {
+  const int64_t held = (L.kp / 64 + kFinWaves - 1) / kFinWaves;
+  auto* k = held <= 2 ? &finish_kernel<RT, 2> : held <= 6 ? &finish_kernel<RT, 6> : &finish_kernel<RT, 0>;
+  return launch(k, dim3((unsigned)((L.M + 15) / 16)), dim3(64 * kFinWaves), stream, p, ck,
+                reinterpret_cast<const u32x4*>(ws + L.off_u), reinterpret_cast<const u32x4*>(ws + L.off_a_up),
+                reinterpret_cast<const float*>(ws + L.off_d), L, dx);
 }
 
 template <int JT>
 hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a, const uint16_t* lora_b,
                        const BackwardLayout& L, float alpha, uint16_t* da, uint16_t* db, char* ws, hipStream_t stream) {
-  uint16_t* ap = reinterpret_cast<uint16_t*>(ws + L.off_ap);
-  uint16_t* at = reinterpret_cast<uint16_t*>(ws + L.off_at);
-  uint16_t* bt = reinterpret_cast<uint16_t*>(ws + L.off_bt);
-  uint16_t* u_rows = reinterpret_cast<uint16_t*>(ws + L.off_u_rows);
-  uint16_t* u_cols = reinterpret_cast<uint16_t*>(ws + L.off_u_cols);
-  uint16_t* t_cols = reinterpret_cast<uint16_t*>(ws + L.off_t_cols);
+  constexpr int kCT = JT == 8 ? 4 : 8, kG = JT == 8 ? 2 : 4, kX = kG / 2;
+  auto frag = [&](size_t off) { return reinterpret_cast<u32x4*>(ws + off); };
   float* d_lora = reinterpret_cast<float*>(ws + L.off_d);
   float* part = reinterpret_cast<float*>(ws + L.off_part);
   auto blocks = [](int64_t items) { const int64_t b = (items + 255) / 256; return dim3((unsigned)(b < 4096 ? b : 4096)); };
-  hipError_t e = launch(&transpose_factors_kernel, blocks(L.rp * (2 * L.kp + L.np) / 8), dim3(256), stream, lora_a,
-                        lora_b, L, ap, at, bt);
+  hipError_t e = launch(&factors_kernel, blocks(L.rp * (2 * L.kp + L.np) / 8), dim3(256), stream, lora_a, lora_b, L,
+                        frag(L.off_a_down), frag(L.off_a_up), frag(L.off_b));
   if (e != hipSuccess) return e;
   const bool wg = L.N % 8 == 0, wx = L.K % 8 == 0;
   auto* rk = wg ? (wx ? &rows_kernel<JT, true, true> : &rows_kernel<JT, true, false>)
                 : (wx ? &rows_kernel<JT, false, true> : &rows_kernel<JT, false, false>);
-  e = launch(rk, dim3((unsigned)((L.row_splits_g + L.row_splits_x) * ((L.M + 127) / 128))), dim3(256), stream,
-             g, bt, ap, ck, L, part);
+  const int64_t row_groups = (L.M + 16 * kG - 1) / (16 * kG) * L.splits_g + (L.M + 16 * kX - 1) / (16 * kX) * L.splits_x;
+  e = launch(rk, dim3((unsigned)row_groups), dim3(256), stream, g, frag(L.off_b), frag(L.off_a_down), ck, L, part);
   if (e != hipSuccess) return e;
-  {
-    BackwardLayout l = L;
-    const float* pp = part;
-    const float* st = ck.stats;
-    void* args[] = {&pp, &st, &l, &alpha, &u_rows, &u_cols, &t_cols, &d_lora};
-    const size_t lds = (size_t)(2 * 32 * (L.rp + 1) + 32 * L.rp) * sizeof(float);
-    e = hipLaunchKernel(reinterpret_cast<const void*>(&join_rows_kernel), dim3((unsigned)(L.mp / 32)), dim3(256), args,
-                        lds, stream);
-  }
+  e = launch(&join_rows_kernel<16 * JT>, dim3((unsigned)(L.mp / 32)), dim3(kJoinThreads), stream, part, ck.stats, L,
+             alpha, frag(L.off_u), frag(L.off_uc), frag(L.off_tc), d_lora);
   if (e != hipSuccess || da == nullptr) return e;
-  auto* ckn = wg ? (wx ? &columns_kernel<JT, true, true> : &columns_kernel<JT, true, false>)
-                 : (wx ? &columns_kernel<JT, false, true> : &columns_kernel<JT, false, false>);
-  e = launch(ckn, dim3((unsigned)((L.N + 127) / 128 + (L.K + 127) / 128), (unsigned)L.col_splits), dim3(256), stream,
-             g, ck, u_cols, t_cols, L, part);
+  auto* cn = wg ? (wx ? &columns_kernel<kCT, JT, true, true> : &columns_kernel<kCT, JT, true, false>)
+                : (wx ? &columns_kernel<kCT, JT, false, true> : &columns_kernel<kCT, JT, false, false>);
+  const int64_t col_groups = (L.N + 16 * kCT - 1) / (16 * kCT) + (L.K + 8 * kCT - 1) / (8 * kCT);
+  e = launch(cn, dim3((unsigned)col_groups, (unsigned)L.splits_t), dim3(256), stream, g, ck, frag(L.off_uc),
+             frag(L.off_tc), L, part);
   if (e != hipSuccess) return e;
   return launch(&join_columns_kernel, blocks(L.r * (L.N + L.K)), dim3(256), stream, part, L, da, db);
 }
@@ -583,7 +769,7 @@ hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a
 
 hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
                            const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx, uint16_t* da,
-                           uint16_t* db, char* ws, hipStream_t stream) {
+                           uint16_t* db, char* ws, int compute_units, hipStream_t stream) {
   if (L.M == 0) {                                       // no tokens: no ranges to sum, zeros
     const int64_t b = (L.r * (L.N + L.K) + 255) / 256;
     return launch(&join_columns_kernel, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), stream,
@@ -597,15 +783,12 @@ hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_
   }
   if (dx == nullptr) return hipSuccess;
   float* p = reinterpret_cast<float*>(ws + L.off_p);
-  const hipError_t e = launch_dense_gemm_f32(g, w_t, L.M, L.K, L.N, p, stream);
+  const hipError_t e = launch_dense_gemm_f32(g, w_t, L.M, L.K, L.N, p, compute_units, stream);
   if (e != hipSuccess) return e;
-  auto* k = L.r == 0     ? &finish_kernel<0>
-            : L.rp == 32 ? &finish_kernel<1>
-            : L.rp == 64 ? &finish_kernel<2>
-                         : &finish_kernel<4>;
-  return launch(k, dim3((unsigned)((L.M + 15) / 16)), dim3(64 * kFinWaves), stream, p, ck,
-                reinterpret_cast<const uint16_t*>(ws + L.off_u_rows), reinterpret_cast<const uint16_t*>(ws + L.off_at),
-                reinterpret_cast<const float*>(ws + L.off_d), L, dx);
+  return L.r == 0     ? launch_finish<0>(p, ck, L, ws, dx, stream)
+         : L.rp == 32 ? launch_finish<1>(p, ck, L, ws, dx, stream)
+         : L.rp == 64 ? launch_finish<2>(p, ck, L, ws, dx, stream)
+                      : launch_finish<4>(p, ck, L, ws, dx, stream);
 }
 
 }  // namespace rtl

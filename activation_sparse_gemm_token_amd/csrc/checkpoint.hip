@@ -11,7 +11,7 @@
 // of their own beyond the one to an integer.  Both kernels are bound by
 // HBM: 2 bytes in, 1.16 out per channel, and the other way round.
 #include "rtl_common.hpp"
-#include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 #include "rtl_checkpoint.hpp"
 
 namespace rtl {

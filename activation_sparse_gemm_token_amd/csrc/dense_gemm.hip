@@ -9,10 +9,19 @@
 // The A tile (256 tokens x 64 channels of X per step) goes through LDS in
 // the same swizzled row-major layout as W, copied by the same DMA routine,
 // in a 2-stage ring next to the 3-stage W ring (96 + 64 KiB of LDS).
+//
+// A second form serves the layer's backward pass (G W, launch_dense_gemm_f32):
+// an fp32 result in blocks of 16 x 16, 1 KiB each, in the order in which the
+// matrix core leaves them with its operands swapped, so the stores, and the
+// loads of the kernel that follows, are contiguous.  Every 64 rows of W enter
+// LDS in the order that gives a lane 16 consecutive columns over four blocks
+// (lane l, block t of 4: row l % 16 of X, columns 16 (l / 16) + 4 t + [0, 4)).
+// It also has 192-column tiles.
 #include <type_traits>
 
 #include "gemm_common.hpp"
 #include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 
 namespace rtl {
 
@@ -24,24 +33,121 @@ namespace {
 // matrix cores idled through every such wait and a step took 30 % longer.)
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kWaveM = 128, kWaveN = 64;
-constexpr int kRB = kWaveM / 16, kCB = kWaveN / 16;
 
-// OUT: uint16_t for a bf16 result, float for an fp32 one (stored from the
-// accumulators: 16 lanes write 64 contiguous bytes of a row).
-template <int KM, typename OUT>
+// The tiled form's W copy: LDS row R = 16 t + 4 q + e of every 64 holds W's row
+// 16 q + 4 t + e.  Instruction I fills LDS rows 8 I + [0, 8), lane l's row being
+// 8 I + l / 8, so W's row is a per-lane part, 16 ((l / 8) / 4) + (l / 8) % 4,
+// and a uniform part of I.  NI instructions per wavefront (gemm_common.hpp's
+// dma_w_tile_asm with these rows; the same hazards and waits).
+__device__ __forceinline__ uint32_t w_row_of_instruction(uint32_t I) {
+  return 64 * (I >> 3) + 32 * (I & 1) + 4 * ((I >> 1) & 3);
+}
+__device__ __forceinline__ WTileOffsets w_order_offsets(int64_t K, int64_t n0) {
+  const int lane = threadIdx.x & 63, lr = lane >> 3;
+  WTileOffsets o;
+  o.k_lane = 8 * ((lane & 7) ^ lr);
+  o.base = (uint32_t)(((n0 + 16 * (lr >> 2) + (lr & 3)) * K + o.k_lane) * 2);
+  o.row8 = 0;
+  return o;
+}
+template <int NI>
+__device__ __forceinline__ void dma_w_ordered_asm(__amdgpu_buffer_rsrc_t wr, const WTileOffsets& o, int64_t K,
+                                                  int64_t k0, uint32_t lds_stage_addr, bool guard_k) {
+  static_assert(NI == 3 || NI == 4, "192 or 256 rows");
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)(k0 * 2));
+  const bool chunk_ok = !guard_k || k0 + o.k_lane + 8 <= K;
+  uint32_t v[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const uint32_t row = __builtin_amdgcn_readfirstlane(w_row_of_instruction(NI * wave + i) * (uint32_t)(K * 2));
+    v[i] = chunk_ok ? o.base + row : kOobOffset - soff;
+  }
+  const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds_stage_addr + 1024u * NI * wave);
+  uint32_t saved;
+  if constexpr (NI == 4) {
+    asm volatile(
+        "s_nop 4\n\t"
+        "s_mov_b32 %[sv], m0\n\t"
+        "s_mov_b32 m0, %[l0]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v0], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[l1]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v1], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[l2]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v2], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[l3]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v3], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[sv]"
+        : [sv] "=&s"(saved)
+        : [v0] "v"(v[0]), [v1] "v"(v[1]), [v2] "v"(v[2]), [v3] "v"(v[NI - 1]), [rs] "s"(wr), [so] "s"(soff),
+          [l0] "s"(l0), [l1] "s"(l0 + 0x400u), [l2] "s"(l0 + 0x800u), [l3] "s"(l0 + 0xc00u)
+        : "memory");
+  } else {
+    asm volatile(
+        "s_nop 4\n\t"
+        "s_mov_b32 %[sv], m0\n\t"
+        "s_mov_b32 m0, %[l0]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v0], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[l1]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v1], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[l2]\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %[v2], %[rs], %[so] offen lds\n\t"
+        "s_mov_b32 m0, %[sv]"
+        : [sv] "=&s"(saved)
+        : [v0] "v"(v[0]), [v1] "v"(v[1]), [v2] "v"(v[2]), [rs] "s"(wr), [so] "s"(soff), [l0] "s"(l0),
+          [l1] "s"(l0 + 0x400u), [l2] "s"(l0 + 0x800u)
+        : "memory");
+  }
+  (void)saved;
+}
+
+// The same order for K % 8 == 4 (dma_w_tile_dword's 4-byte copies).
+__device__ __forceinline__ void dma_w_ordered_dword(__amdgpu_buffer_rsrc_t wr, int64_t N, int64_t K, int64_t n0,
+                                                    int64_t k0, char* lds_stage) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int b = 0; b < 128 / kWaves; ++b) {
+    const int row = (256 / kWaves) * wave + 2 * b + (lane >> 5);
+    const int chunk = ((lane & 31) >> 2) ^ (row & 7);
+    const int64_t n = n0 + (row & ~63) + 16 * ((row >> 2) & 3) + 4 * ((row >> 4) & 3) + (row & 3);
+    const int64_t k = k0 + 8 * chunk + 2 * (lane & 3);
+    const uint32_t voff = (k + 2 <= K && n < N) ? (uint32_t)((n * K + k) * 2) : kOobOffset;
+    char* dst = lds_stage + ((256 / kWaves) * wave + 2 * b) * 128;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (__attribute__((address_space(3))) void*)(dst), 4, voff, 0, 0, 0);
+  }
+}
+
+// KM: how channel tails are handled.  TN: tile columns, 256 or 192.  TILED: fp32
+// result in 16 x 16 blocks [M / 16][4 (N / 64)][lane][4] instead of a bf16
+// row-major one.  256 columns: 2 x 4 wavefronts of 128 x 64; 192: 4 x 2 of
+// 64 x 96, which read 160 rows of operands from LDS per step instead of the
+// 176 of 2 x 4.
+template <int KM, int TN, bool TILED>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
-                  int64_t M, int64_t N, int64_t K, OUT* __restrict__ y) {
+                  int64_t M, int64_t N, int64_t K,
+                  std::conditional_t<TILED, float, uint16_t>* __restrict__ y) {
+  static_assert(TN == 256 || (TN == 192 && TILED && KM != kAligned8), "192 columns: the tiled form's 16-byte copies");
+  constexpr int kWavesN = TN == 256 ? 4 : 2, kWavesM = kWaves / kWavesN;
+  constexpr int kTileN = TN, kWaveM = kTileM / kWavesM, kWaveN = TN / kWavesN;
+  constexpr int kRB = kWaveM / 16, kCB = kWaveN / 16;
+  constexpr int kWBytes = kTileN * kTileK * 2;
   constexpr int kWStages = 3, kAStages = 2;
   // One LDS block: the W ring, then the A ring; the epilogue reuses all of it.
-  constexpr int kLdsBytes = (kWStages + kAStages) * kTileBytes;
+  constexpr int kLdsBytes = kWStages * kWBytes + kAStages * kTileBytes;
   static_assert(store_lds_bytes<kRB, kCB>(kWaves) <= kLdsBytes, "store staging must fit in the rings");
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   char* const lds_w = lds;
-  char* const lds_a = lds + kWStages * kTileBytes;
+  char* const lds_a = lds + kWStages * kWBytes;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // uniform: scalar addressing
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
   const int64_t tiles_m = (M + kTileM - 1) / kTileM, tiles_n = (N + kTileN - 1) / kTileN;
   int64_t tm, tn;
   tile_coords(tiles_m, tiles_n, tm, tn);
@@ -60,26 +166,35 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(x, M * K * 2);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(w, N * K * 2);
   const WTileOffsets xo = w_tile_offsets<kWaves>(K, m0);
-  const WTileOffsets wo = w_tile_offsets<kWaves>(K, n0);
+  const WTileOffsets wo = TILED ? w_order_offsets(K, n0) : w_tile_offsets<kWaves>(K, n0);
   const uint32_t f0 = frag_lane_offset(0), f1 = frag_lane_offset(1);
   const char* b_base0 = lds_w + wn * kCB * 2048 + f0;
   const char* b_base1 = lds_w + wn * kCB * 2048 + f1;
   const char* a_base0 = lds_a + wm * kRB * 2048 + f0;
   const char* a_base1 = lds_a + wm * kRB * 2048 + f1;
-  constexpr int kTileOps = KM == kAligned8 ? 128 / kWaves : 32 / kWaves;
+  constexpr int kTileOps = KM == kAligned8 ? 128 / kWaves : TN / 64;     // of a W tile
 
   // Both tile copies are issued as inline-asm DMA blocks: no vector-memory
   // operation of the loop is visible to the compiler, so it inserts no
   // vmcnt waits of its own (it cannot always prove that a copy into one
   // stage does not alias the reads of another) and the explicit waits below
   // are exact.  The K % 8 == 4 mode uses the compiler-visible dword copy.
-  auto copy_tile = [&](__amdgpu_buffer_rsrc_t rs, const WTileOffsets& o, int64_t row0, int64_t rows,
-                       int64_t ks, char* dst) {
+  auto copy_w = [&](int64_t ks, char* dst) {
     if constexpr (KM == kAligned8) {
-      dma_w_tile_dword<kWaves>(rs, rows, K, row0, ks * kTileK, dst);
+      if constexpr (TILED) dma_w_ordered_dword(wr, N, K, n0, ks * kTileK, dst);
+      else dma_w_tile_dword<kWaves>(wr, N, K, n0, ks * kTileK, dst);
     } else {
       const uint32_t lds_addr = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)(dst);
-      dma_w_tile_asm<kWaves>(rs, o, K, ks * kTileK, lds_addr, KM == kAligned16);
+      if constexpr (TILED) dma_w_ordered_asm<TN / 64>(wr, wo, K, ks * kTileK, lds_addr, KM == kAligned16);
+      else dma_w_tile_asm<kWaves>(wr, wo, K, ks * kTileK, lds_addr, KM == kAligned16);
+    }
+  };
+  auto copy_a = [&](int64_t ks, char* dst) {
+    if constexpr (KM == kAligned8) {
+      dma_w_tile_dword<kWaves>(xr, M, K, m0, ks * kTileK, dst);
+    } else {
+      const uint32_t lds_addr = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)(dst);
+      dma_w_tile_asm<kWaves>(xr, xo, K, ks * kTileK, lds_addr, KM == kAligned16);
     }
   };
 
@@ -94,11 +209,11 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     barrier_no_fence();
     const int64_t ka = ks + 1 < ksteps ? ks + 1 : ksteps - 1;
     const int64_t kw = ks + 2 < ksteps ? ks + 2 : ksteps - 1;
-    copy_tile(xr, xo, m0, M, ka, lds_a + (1 - ba) * kTileBytes);
-    copy_tile(wr, wo, n0, N, kw, lds_w + (bw + 2) % kWStages * kTileBytes);
+    copy_a(ka, lds_a + (1 - ba) * kTileBytes);
+    copy_w(kw, lds_w + (bw + 2) % kWStages * kWBytes);
     __builtin_amdgcn_sched_barrier(0);
-    const char* bs0 = b_base0 + bw * kTileBytes;
-    const char* bs1 = b_base1 + bw * kTileBytes;
+    const char* bs0 = b_base0 + bw * kWBytes;
+    const char* bs1 = b_base1 + bw * kWBytes;
     const char* as0 = a_base0 + ba * kTileBytes;
     const char* as1 = a_base1 + ba * kTileBytes;
     bf16x8 af[2][kRB];
@@ -118,16 +233,18 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
       }
 #pragma unroll
       for (int rb = 0; rb < kRB; ++rb)
-        acc[rb][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[0][rb], b0, acc[rb][cb], 0, 0, 0);
+        acc[rb][cb] = TILED ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0, af[0][rb], acc[rb][cb], 0, 0, 0)
+                            : __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[0][rb], b0, acc[rb][cb], 0, 0, 0);
 #pragma unroll
       for (int rb = 0; rb < kRB; ++rb)
-        acc[rb][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[1][rb], b1, acc[rb][cb], 0, 0, 0);
+        acc[rb][cb] = TILED ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1, af[1][rb], acc[rb][cb], 0, 0, 0)
+                            : __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[1][rb], b1, acc[rb][cb], 0, 0, 0);
     }
   };
 
-  copy_tile(wr, wo, n0, N, 0, lds_w);
-  copy_tile(xr, xo, m0, M, 0, lds_a);
-  copy_tile(wr, wo, n0, N, ksteps > 1 ? 1 : 0, lds_w + kTileBytes);
+  copy_w(0, lds_w);
+  copy_a(0, lds_a);
+  copy_w(ksteps > 1 ? 1 : 0, lds_w + kWBytes);
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
@@ -150,48 +267,51 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   wait_vm<0>();
   barrier_no_fence();                     // every wave is done with the rings
 
-  if constexpr (std::is_same_v<OUT, float>) {
-    const int lane = threadIdx.x & 63;
+  if constexpr (TILED) {
+    const int64_t tn16 = (N + 63) / 64 * 4;
+    const int64_t mb = (m0 + wm * kWaveM) / 16, nb = (n0 + wn * kWaveN) / 16;
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb)
 #pragma unroll
-      for (int cb = 0; cb < kCB; ++cb) {
-        const int64_t n = n0 + wn * kWaveN + 16 * cb + (lane & 15);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t m = m0 + wm * kWaveM + 16 * rb + 4 * (lane >> 4) + i;
-          if (m < M && n < N) y[m * N + n] = acc[rb][cb][i];
-        }
-      }
+      for (int cb = 0; cb < kCB; ++cb)
+        if (16 * (mb + rb) < M && nb + cb < tn16)
+          *reinterpret_cast<f32x4*>(y + (((mb + rb) * tn16 + nb + cb) * 64 + (threadIdx.x & 63)) * 4) = acc[rb][cb];
+  } else if (N % 8 == 0) {
+    store_tile_via_lds<kRB, kCB>(acc, lds, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
+  } else {
+    store_acc_bf16<kRB, kCB>(acc, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
   }
-  else if (N % 8 == 0) store_tile_via_lds<kRB, kCB>(acc, lds, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
-  else store_acc_bf16<kRB, kCB>(acc, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
-}
-
-template <typename OUT>
-hipError_t launch_dense(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K, OUT* y,
-                        hipStream_t stream) {
-  const int64_t tiles = ((M + kTileM - 1) / kTileM) * ((N + kTileN - 1) / kTileN);
-  const dim3 grid((unsigned)tiles), block(kThreads);
-  // 16 x 16 blocks: a form of the same loop on v_mfma_f32_32x32x16_bf16
-  // (4 x 2 blocks of 32 x 32 per wavefront) measured 8 % slower (253
-  // against 235 us at M = 4096, K = 3072, N = 12288).
-  auto* k = K % kTileK == 0 ? &dense_gemm_kernel<kFullK, OUT>
-            : K % 8 == 0   ? &dense_gemm_kernel<kAligned16, OUT>
-                           : &dense_gemm_kernel<kAligned8, OUT>;
-  return launch(k, grid, block, stream, x, w, M, N, K, y);
 }
 
 }  // namespace
 
 hipError_t launch_dense_gemm(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
                              int64_t K, uint16_t* y, hipStream_t stream) {
-  return launch_dense(x, w, M, N, K, y, stream);
+  const int64_t tiles = ((M + kTileM - 1) / kTileM) * ((N + kTileN - 1) / kTileN);
+  const dim3 grid((unsigned)tiles), block(kThreads);
+  // 16 x 16 blocks: a form of the same loop on v_mfma_f32_32x32x16_bf16
+  // (4 x 2 blocks of 32 x 32 per wavefront) measured 8 % slower (253
+  // against 235 us at M = 4096, K = 3072, N = 12288).
+  auto* k = K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 256, false>
+            : K % 8 == 0   ? &dense_gemm_kernel<kAligned16, 256, false>
+                           : &dense_gemm_kernel<kAligned8, 256, false>;
+  return launch(k, grid, block, stream, x, w, M, N, K, y);
 }
 
 hipError_t launch_dense_gemm_f32(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
-                                 int64_t K, float* y, hipStream_t stream) {
-  return launch_dense(x, w, M, N, K, y, stream);
+                                 int64_t K, float* y, int compute_units, hipStream_t stream) {
+  // 192-column tiles when they fill the CUs in fewer rounds, weighed by what
+  // a tile takes (0.79 of a 256-column one).
+  const int64_t tiles_m = (M + kTileM - 1) / kTileM;
+  auto rounds = [&](int64_t tn) { return (tiles_m * ((N + tn - 1) / tn) + compute_units - 1) / compute_units; };
+  const bool narrow = K % 8 == 0 && rounds(192) * 79 < rounds(256) * 100;
+  const int64_t tile_n = narrow ? 192 : 256;
+  const dim3 grid((unsigned)(tiles_m * ((N + tile_n - 1) / tile_n))), block(kThreads);
+  auto* k = narrow ? (K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 192, true> : &dense_gemm_kernel<kAligned16, 192, true>)
+            : K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 256, true>
+            : K % 8 == 0      ? &dense_gemm_kernel<kAligned16, 256, true>
+                              : &dense_gemm_kernel<kAligned8, 256, true>;
+  return launch(k, grid, block, stream, x, w, M, N, K, y);
 }
 
 }  // namespace rtl

@@ -11,7 +11,7 @@
 // same 16-byte pair count; see vec below), so the kernel is bound by HBM:
 // each element is read once and written once.
 #include "rtl_common.hpp"
-#include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 
 namespace rtl {
 

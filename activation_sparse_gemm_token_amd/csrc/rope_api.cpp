@@ -1,6 +1,6 @@
 // Host side of include/rtlynx_rope.h: argument checks, then one launch.
 #include "rtl_api.hpp"
-#include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 #include "rtlynx_rope.h"
 
 namespace {

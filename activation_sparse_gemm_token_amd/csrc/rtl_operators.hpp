@@ -1,0 +1,77 @@
+// Launch wrappers of the operators beside the sparse layer: rotary positions,
+// 4-bit linears, the activation checkpoint and the layer's backward pass
+// (internal; the public interfaces are include/rtlynx_*.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace rtl {
+
+// Rotary positions.  One tensor [batch, tokens, heads, dim] and its result
+// (strides in elements); heads == 0 for an absent second tensor.
+struct RopeSide {
+  const void* x;
+  void* y;
+  int64_t xb, xt, xh, yb, yt, yh;
+  int heads;
+  bool in_place;                         // y is x: copied channels need no copy
+};
+struct RopeArgs {
+  RopeSide t[2];
+  const int64_t* positions;
+  const double* inv_freq;
+  int64_t total, tokens;                 // batch * tokens, tokens
+  int64_t pos_b, pos_t;
+  int dim, rot;
+  int axis_end[3];                       // first pair of axes 1, 2 and 3
+  float scale;
+  bool inverse;
+  int group;                             // tokens per workgroup (set by launch_rope)
+};
+hipError_t launch_rope(RopeArgs a, int elem_bytes, bool fp16, bool interleaved, int compute_units,
+                       hipStream_t stream);
+
+// 4-bit weights: tiles of 16 rows x 128 channels (1 KiB of codes each).
+inline int64_t w4_tiles(int64_t N, int64_t K) { return ((N + 15) / 16) * ((K + 127) / 128); }
+hipError_t launch_w4_pack(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t N,
+                          int64_t K, int group, void* packed, hipStream_t stream);
+hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, int64_t N, int64_t K,
+                            int group, bool zeros, uint16_t* y, hipStream_t stream);
+
+// 8-bit activation checkpoint (include/rtlynx_train.h).
+struct Ckpt {
+  const int8_t* codes;
+  const uint8_t* exps;
+  const uint8_t* idx;
+  const float* stats;
+};
+hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
+                                  uint8_t* idx, float* stats, int compute_units, hipStream_t stream);
+hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K,
+                                    uint16_t* y, hipStream_t stream);
+
+// x [M, K] w [N, K]^T with an fp32 result in 16 x 16 blocks:
+// [ceil(M / 16)][4 ceil(N / 64)][lane][4], lane l of block t of every four holding
+// row l % 16, columns 16 (l / 16) + 4 t + [0, 4) of the 64 (dense_gemm.hip).
+hipError_t launch_dense_gemm_f32(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
+                                 float* y, int compute_units, hipStream_t stream);
+
+// Sizes, splits and workspace regions of the layer's backward pass.  Rank is
+// padded to 32, 64 or 128, channels and tokens to 64 (zeros).  Operands of the
+// matrix cores are kept in fragments of 1 KiB: [lane][8] bf16, lane l holding
+// row l % 16 and contraction indices 8 (l / 16) + [0, 8) of a 16 x 32 block.
+struct BackwardLayout {
+  int64_t M, N, K, r;
+  int64_t rp, np, kp, mp;
+  int64_t chunk_g, chunk_x;                        // channels per workgroup of the token-by-rank products
+  int64_t splits_g, splits_x;
+  int64_t chunk_t, splits_t;                       // tokens per workgroup of the products over tokens
+  size_t off_a_down, off_a_up, off_b, off_u, off_uc, off_tc, off_d, off_part, off_p, total;
+};
+BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t r);
+hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
+                           const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx,
+                           uint16_t* da, uint16_t* db, char* workspace, int compute_units, hipStream_t stream);
+
+}  // namespace rtl

@@ -2,7 +2,7 @@
 // sizes, launches.
 #include "rtl_api.hpp"
 #include "rtl_common.hpp"
-#include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 #include "rtlynx_train.h"
 
 namespace {
@@ -22,37 +22,43 @@ bool back_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
 
 }  // namespace
 
-// Splits: about 768 workgroups for the token-by-rank products and 512 for
-// those over tokens (two to three per CU), no finer than two steps each.
+// Splits by sizes alone (a workspace must fit whatever device it is used on):
+// about two workgroups per CU of the card for the products over G's channels
+// and over tokens, one for those over the checkpoint's channels, no workgroup
+// with less than one step of each of its four wavefronts.
 rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
+  constexpr int64_t kCus = 256;
   BackwardLayout L{};
   L.M = M; L.N = N; L.K = K; L.r = r;
   L.rp = r == 0 ? 0 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
   L.np = round_up(N, 64);
   L.kp = round_up(K, 64);
   L.mp = round_up(M, 64);
-  const int64_t row_blocks = (M + 127) / 128;
-  int64_t chunk = row_blocks * (L.np + L.kp) / 768;
-  L.row_chunk = chunk < 128 ? 128 : round_up(chunk, 64);
-  L.row_splits_g = (L.np + L.row_chunk - 1) / L.row_chunk;
-  L.row_splits_x = (L.kp + L.row_chunk - 1) / L.row_chunk;
-  const int64_t col_blocks = (N + 127) / 128 + (K + 127) / 128;
-  chunk = col_blocks * L.mp / 512;
-  L.col_chunk = chunk < 128 ? 128 : round_up(chunk, 64);
-  L.col_splits = (L.mp + L.col_chunk - 1) / L.col_chunk;
+  auto chunk = [](int64_t work, int64_t groups, int64_t step) {
+    const int64_t c = (work + groups - 1) / groups;
+    return round_up(c < step ? step : c, step);
+  };
+  const int64_t rows_g = L.rp == 128 ? 32 : 64, rows_x = rows_g / 2;    // tokens per workgroup
+  L.chunk_g = chunk((M + rows_g - 1) / rows_g * L.np, 2 * kCus, 256);
+  L.splits_g = (L.np + L.chunk_g - 1) / L.chunk_g;
+  L.chunk_x = chunk((M + rows_x - 1) / rows_x * L.kp, kCus, 256);
+  L.splits_x = (L.kp + L.chunk_x - 1) / L.chunk_x;
+  const int64_t cols_g = L.rp == 128 ? 64 : 128, cols_x = cols_g / 2;   // channels per workgroup
+  L.chunk_t = chunk(((N + cols_g - 1) / cols_g + (K + cols_x - 1) / cols_x) * L.mp, 2 * kCus, 128);
+  L.splits_t = (L.mp + L.chunk_t - 1) / L.chunk_t;
   size_t o = 0;
-  auto take = [&](size_t bytes) { const size_t at = o; o += (bytes + 255) / 256 * 256; return at; };
-  L.off_ap = take((size_t)(L.rp * L.kp) * 2);
-  L.off_at = take((size_t)(L.rp * L.kp) * 2);
-  L.off_bt = take((size_t)(L.rp * L.np) * 2);
-  L.off_u_rows = take((size_t)(2 * L.rp * M) * 2);
-  L.off_u_cols = take((size_t)(4 * L.rp * L.mp) * 2);
-  L.off_t_cols = take((size_t)(2 * L.rp * L.mp) * 2);
-  L.off_d = take((size_t)M * 4);
-  const size_t rows = (size_t)((L.row_splits_g + 2 * L.row_splits_x) * M * L.rp) * 4;
-  const size_t cols = (size_t)(L.col_splits * (N + L.kp) * L.rp) * 4;
-  L.off_part = take(rows > cols ? rows : cols);
-  L.off_p = take((size_t)(M * K) * 4);
+  auto take = [&](int64_t bytes) { const size_t at = o; o += ((size_t)bytes + 255) / 256 * 256; return at; };
+  L.off_a_down = take(L.rp * L.kp * 2);
+  L.off_a_up = take(L.rp * L.kp * 2);
+  L.off_b = take(L.rp * L.np * 2);
+  L.off_u = take(2 * L.rp * L.mp * 2);
+  L.off_uc = take(4 * L.rp * L.mp * 2);
+  L.off_tc = take(2 * L.rp * L.mp * 2);
+  L.off_d = take(L.mp * 4);
+  const int64_t rows = (L.splits_g + 2 * L.splits_x) * M * L.rp * 4;
+  const int64_t over_t = L.splits_t * (N + L.kp) * L.rp * 4;
+  L.off_part = take(rows > over_t ? rows : over_t);
+  L.off_p = take(round_up(M, 16) * L.kp * 4);
   L.total = o;
   return L;
 }
@@ -114,9 +120,10 @@ RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* c
     if (workspace == nullptr || workspace_bytes < rtl::backward_layout(M, N, K, r).total) return RTL_ERR_WORKSPACE;
     if (!rtl::aligned(workspace, 16)) return RTL_ERR_MISALIGNED;
   }
-  const rtl_status d = rtl::check_device(stream);
+  int cus = 0;
+  const rtl_status d = rtl::check_device(stream, &cus);
   if (d != RTL_OK) return d;
   const rtl::Ckpt ck{codes, exps, idx, stats};
   return rtl::from_hip(rtl::launch_backward(g, ck, w_t, lora_a, lora_b, rtl::backward_layout(M, N, K, r), lora_scale,
-                                            dx, da, db, static_cast<char*>(workspace), stream));
+                                            dx, da, db, static_cast<char*>(workspace), cus > 0 ? cus : 1, stream));
 }

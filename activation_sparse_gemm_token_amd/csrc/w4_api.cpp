@@ -1,6 +1,6 @@
 // Host side of include/rtlynx_w4.h: argument checks, then one launch.
 #include "rtl_api.hpp"
-#include "rtl_kernels.hpp"
+#include "rtl_operators.hpp"
 #include "rtlynx_w4.h"
 
 namespace {
