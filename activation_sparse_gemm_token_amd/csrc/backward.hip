@@ -18,7 +18,8 @@
 //                           rows in memory: the tile goes through LDS and is read
 //                           transposed (ds_read_b64_tr_b16).
 //   5. join_columns_kernel  sums the token ranges in order into dA and dB.
-//   6. the dense GEMM       P = G W, in 16 x 16 blocks of fp32.
+//   6. the dense GEMM       P = G W, in 16 x 16 blocks of fp32, and of each tile
+//                           its share of D.
 //   7. finish_kernel        D per token, then dX; U A is formed again, a 16-token
 //                           strip at a time, on the matrix cores (r is small), so it
 //                           never goes to memory.
@@ -106,6 +107,9 @@ __device__ __forceinline__ void ckpt_split(const CkptRaw& r, u32x4& pruned, u32x
     pruned[i] = v[i] & ~m[i];
   }
 }
+__device__ __forceinline__ void ckpt_split(const Ckpt16& r, int half, u32x4& pruned, u32x4& kept) {
+  ckpt_split(CkptRaw{{r.codes[2 * half], r.codes[2 * half + 1]}, r.exp, r.idx >> (8 * half)}, pruned, kept);
+}
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -134,7 +138,8 @@ __device__ __forceinline__ void join_waves(f32x4* acc, f32x4* lds, int wave, int
 
 // --- 1. factors ------------------------------------------------------------
 // One thread per lane of a fragment.  a_down [kp / 32][rp / 16]: rows ranks,
-// contraction channels; a_up [kp / 16][rp / 32]: rows channels in the order of
+// contraction channels (in step h of every two, lanes l / 16 hold channels
+// 16 (l / 16) + 8 h + [0, 8) of the 64); a_up [kp / 16][rp / 32]: rows channels in the order of
 // P's blocks (row 4 q + e of block t of four: channel 16 q + 4 t + e of the 64),
 // contraction ranks; b [np / 32][rp / 16]: rows ranks, contraction output channels.
 __global__ void __launch_bounds__(256)
@@ -146,7 +151,8 @@ factors_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, B
     const int lane = (int)(i & 63), row = lane & 15, at = 8 * (lane >> 4);
     uint32_t v[8];
     if (i < na) {
-      const int64_t f = i >> 6, j = 16 * (f % jt) + row, k = 32 * (f / jt) + at;
+      const int64_t f = i >> 6, j = 16 * (f % jt) + row, step = f / jt;
+      const int64_t k = 64 * (step >> 1) + 2 * at + 8 * (step & 1);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = j < L.r && k + e < L.K ? a[j * L.K + k + e] : 0;
     } else if (i < 2 * na) {
@@ -228,29 +234,37 @@ __device__ __forceinline__ void g_rows(const uint16_t* __restrict__ g, const u32
       }
 }
 
-template <int MT, int JT, bool WIDE>
+// A lane reads 16 channels of its token: its 8 of both steps of 64 channels
+// (a_down has the same order).
+template <int MT, int JT>
 __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__ a, const BackwardLayout& L,
                                        int64_t m0, int64_t lo, int64_t hi, f32x4* lds, float* __restrict__ out) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   struct Stage {
-    CkptRaw x[MT][2];
+    Ckpt16 x[MT];
     u32x4 w[2][JT];
   };
   f32x4 acc[2 * MT * JT];                               // pruned, kept
 #pragma unroll
   for (int i = 0; i < 2 * MT * JT; ++i) acc[i] = kZero4;
+  // Tokens past M read the last one's; their products are not stored.
+  const int8_t* codes[MT];
+  const uint8_t *exps[MT], *idx[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + 16 * i + col, row = m < L.M ? m : L.M - 1;
+    codes[i] = ck.codes + row * L.K;
+    exps[i] = ck.exps + row * ((L.K + 31) / 32);
+    idx[i] = ck.idx + row * ((L.K + 7) / 8);
+  }
   auto load = [&](Stage& s, int64_t c) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < MT; ++i) s.x[i] = ckpt_load16(codes[i], exps[i], idx[i], c + 16 * quad, L.K);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + col;
-        s.x[i][h] = ckpt_load<WIDE>(ck, m, c + 32 * h + 8 * quad, L.K, m < L.M);
-      }
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < JT; ++j) s.w[h][j] = a[((c / 32 + h) * JT + j) * 64 + lane];
-    }
   };
   auto use = [&](const Stage& s) {
 #pragma unroll
@@ -258,7 +272,7 @@ __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         u32x4 pruned, kept;
-        ckpt_split(s.x[i][h], pruned, kept);
+        ckpt_split(s.x[i], h, pruned, kept);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
           acc[i * JT + j] = mfma(pruned, s.w[h][j], acc[i * JT + j]);
@@ -290,7 +304,7 @@ __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__
         }
 }
 
-template <int JT, bool WIDE_G, bool WIDE_X>
+template <int JT, bool WIDE_G>
 __global__ void __launch_bounds__(256)
 rows_kernel(const uint16_t* __restrict__ g, const u32x4* __restrict__ b, const u32x4* __restrict__ a, Ckpt ck,
             BackwardLayout L, float* __restrict__ part) {
@@ -305,7 +319,7 @@ rows_kernel(const uint16_t* __restrict__ g, const u32x4* __restrict__ b, const u
   } else {
     id -= groups_g;
     const int64_t s = id % L.splits_x, lo = s * L.chunk_x, hi = lo + L.chunk_x < L.kp ? lo + L.chunk_x : L.kp;
-    x_rows<kX, JT, WIDE_X>(ck, a, L, id / L.splits_x * (16 * kX), lo, hi, lds, part + (L.splits_g + 2 * s) * slab);
+    x_rows<kX, JT>(ck, a, L, id / L.splits_x * (16 * kX), lo, hi, lds, part + (L.splits_g + 2 * s) * slab);
   }
 }
 
@@ -583,157 +597,135 @@ join_columns_kernel(const float* __restrict__ part, BackwardLayout L, uint16_t* 
 }
 
 // --- 7. dX -----------------------------------------------------------------------
-// 16 tokens per workgroup, 8 wavefronts along the channels, 64 channels (four of
-// P's blocks) at a time: lane l has token l % 16, channels 16 (l / 16) + [0, 16),
-// i.e. 16 bytes of codes, one exponent, two position bytes and 32 bytes of dX.
-// dX needs D first, a sum over the whole token.  With HOLD > 0 a wavefront keeps
-// what it read (HOLD times 64 channels: tokens of up to 512 HOLD channels) in
-// registers over that sum; otherwise it reads P and the checkpoint again.
-constexpr int kFinWaves = 8;
-
-struct FinUnit {
-  f32x4 p[4];                                           // P of channels 4 t + [0, 4)
-  u32x4 codes;
-  uint32_t exp, idx;
-};
-
-template <int RT, int HOLD>                             // RT: rp / 32, 0 without LoRA
-__global__ void __launch_bounds__(64 * kFinWaves)
-finish_kernel(const float* __restrict__ p, Ckpt ck, const u32x4* __restrict__ u, const u32x4* __restrict__ a_up,
-              const float* __restrict__ d_lora, BackwardLayout L, uint16_t* __restrict__ dx) {
-  __shared__ float red[kFinWaves][16];
+// 32 tokens (two of P's block rows) and a range of channels per workgroup, its 4
+// wavefronts 64 channels (four of P's blocks) in turn: lane l has token l % 16,
+// channels 16 (l / 16) + [0, 16), i.e. 16 bytes of codes, one exponent, two
+// position bytes and 32 bytes of dX.
+template <int RT>                                       // rp / 32, 0 without LoRA
+__global__ void __launch_bounds__(256)
+finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckpt ck, const u32x4* __restrict__ u,
+              const u32x4* __restrict__ a_up, const float* __restrict__ d_lora, BackwardLayout L, int64_t chunk,
+              uint16_t* __restrict__ dx) {
+  __shared__ float red[256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const int64_t m = (int64_t)blockIdx.x * 16 + col;
-  const bool ok = m < L.M;
-  const int64_t row = ok ? m : L.M - 1;
-  const float s = ck.stats[2 * row], lk = ck.stats[2 * row + 1];
-  const int8_t* codes = ck.codes + row * L.K;
-  const uint8_t* exps = ck.exps + row * ((L.K + 31) / 32);
-  const uint8_t* idx = ck.idx + row * ((L.K + 7) / 8);
-  const int64_t steps = L.kp / 64;
-  const f32x4* pr = reinterpret_cast<const f32x4*>(p) + (int64_t)blockIdx.x * steps * 256 + lane;
-
-  // Channels past K have code 0 and count as pruned; nothing past a row is read.
-  auto load = [&](FinUnit& f, int64_t t) {
-    const int64_t k = 64 * t + 16 * quad;
+  const int64_t steps = L.kp / 64, rows16 = (L.M + 15) / 16, slab = rows16 * steps * 256;
+  const int64_t groups = (rows16 + 1) / 2;
+  const int64_t b0 = 2 * (blockIdx.x % groups);
+  const int64_t lo = blockIdx.x / groups * chunk, hi = lo + chunk < steps ? lo + chunk : steps;
+  float s[2], lk[2];
+  const int8_t* codes[2];
+  const uint8_t *exps[2], *idx[2];
+  const f32x4* pr[2];
+  bool ok[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f.p[i] = pr[(4 * t + i) * 64];
-    f.codes = (u32x4){0, 0, 0, 0};
-    f.exp = f.idx = 0;
-    if (k + 16 <= L.K) {
-      __builtin_memcpy(&f.codes, codes + k, 16);
-      f.exp = exps[k / 32];
-      uint16_t two;
-      __builtin_memcpy(&two, idx + k / 8, 2);
-      f.idx = two;
-    } else if (k < L.K) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (k + 4 * i < L.K) f.codes[i] = *reinterpret_cast<const uint32_t*>(codes + k + 4 * i);
-      f.exp = exps[k / 32];
-      f.idx = idx[k / 8];
-      if (k + 8 < L.K) f.idx |= (uint32_t)idx[k / 8 + 1] << 8;
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int64_t b = b0 + i < rows16 ? b0 + i : rows16 - 1, m = 16 * (b0 + i) + col;
+    ok[i] = m < L.M;
+    const int64_t row = ok[i] ? m : L.M - 1;
+    s[i] = ck.stats[2 * row];
+    lk[i] = ck.stats[2 * row + 1];
+    codes[i] = ck.codes + row * L.K;
+    exps[i] = ck.exps + row * ((L.K + 31) / 32);
+    idx[i] = ck.idx + row * ((L.K + 7) / 8);
+    pr[i] = reinterpret_cast<const f32x4*>(p) + b * steps * 256 + lane;
+  }
+  struct Stage {
+    f32x4 p[2][4];
+    Ckpt16 x[2];
   };
-  auto partial = [&](const FinUnit& f) {
+  auto load = [&](Stage& f, int64_t t) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) f.p[i][n] = pr[i][(4 * t + n) * 64];
+      f.x[i] = ckpt_load16(codes[i], exps[i], idx[i], 64 * t + 16 * quad, L.K);
+    }
+    for (int64_t q = 1; q < L.p_splits; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) f.p[i][n] += pr[i][q * slab + (4 * t + n) * 64];
+  };
+  Stage s0, s1;
+  if (lo + wave < hi) load(s0, lo + wave);
+
+  // D: the tiles' and ranges' shares, 8 at a time, then those 8 in order.
+  {
+    const int64_t m = 16 * b0 + (threadIdx.x & 31), row = m < L.M ? m : L.M - 1;
+    float d = 0.f;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x >> 5; i < L.p_splits * L.p_tiles; i += 8) d += d_part[i * L.M + row];
+    red[threadIdx.x] = d;
+  }
+  u32x4 uh[2][RT > 0 ? RT : 1], ul[2][RT > 0 ? RT : 1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      uh[i][r] = u[(((b0 + i) * RT + r) * 2) * 64 + lane];
+      ul[i][r] = u[(((b0 + i) * RT + r) * 2 + 1) * 64 + lane];
+    }
+  __syncthreads();
+  float per[2], per_kept[2];                            // D / Lk of a pruned channel; times 1 - s of a kept one
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
     float d = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = kept_bits(f.idx >> (4 * i)), q = f.codes[i];
-      d += (b & 1u) ? (float)((int)(q << 24) >> 24) * f.p[i][0] : 0.f;
-      d += (b & 2u) ? (float)((int)(q << 16) >> 24) * f.p[i][1] : 0.f;
-      d += (b & 4u) ? (float)((int)(q << 8) >> 24) * f.p[i][2] : 0.f;
-      d += (b & 8u) ? (float)((int)q >> 24) * f.p[i][3] : 0.f;
-    }
-    return __builtin_amdgcn_ldexpf(d, (int)f.exp - 133);
-  };
-
-  FinUnit held[HOLD > 0 ? HOLD : 1];
-  float d = 0.f;
-  if constexpr (HOLD > 0) {
-#pragma unroll
-    for (int h = 0; h < HOLD; ++h)
-      if (wave + kFinWaves * h < steps) load(held[h], wave + kFinWaves * h);
-#pragma unroll
-    for (int h = 0; h < HOLD; ++h)
-      if (wave + kFinWaves * h < steps) d += partial(held[h]);
-  } else {
-#pragma unroll 2
-    for (int64_t t = wave; t < steps; t += kFinWaves) {
-      load(held[0], t);
-      d += partial(held[0]);
-    }
+    for (int n = 0; n < 8; ++n) d += red[32 * n + 16 * i + col];
+    if constexpr (RT > 0) d -= d_lora[16 * (b0 + i) + col];
+    per[i] = lk[i] > 0.f ? d / lk[i] : 0.f;
+    per_kept[i] = per[i] * (1.f - s[i]);
   }
-  d += __shfl_xor(d, 16, 64);
-  d += __shfl_xor(d, 32, 64);
-  if (quad == 0) red[wave][col] = d;
-  __syncthreads();
-  d = 0.f;
-#pragma unroll
-  for (int w = 0; w < kFinWaves; ++w) d += red[w][col];
-  if constexpr (RT > 0) d -= d_lora[row];
-  const float per = lk > 0.f ? d / lk : 0.f;            // of a pruned channel; times 1 - s of a kept one
-  const float per_kept = per * (1.f - s);
 
-  u32x4 uh[RT > 0 ? RT : 1], ul[RT > 0 ? RT : 1];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    uh[i] = u[(((int64_t)blockIdx.x * RT + i) * 2) * 64 + lane];
-    ul[i] = u[(((int64_t)blockIdx.x * RT + i) * 2 + 1) * 64 + lane];
-  }
-  auto finish = [&](const FinUnit& f, int64_t t) {
-    uint32_t out[8];
+  auto finish = [&](const Stage& f, int64_t t) {
+    uint32_t out[2][8];
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      f32x4 v = kZero4;
+      f32x4 v[2] = {kZero4, kZero4};
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const u32x4 a = a_up[((4 * t + n) * RT + i) * 64 + lane];
-        v = mfma(a, uh[i], v);
-        v = mfma(a, ul[i], v);
-      }
-      const uint32_t b = kept_bits(f.idx >> (4 * n)), q = f.codes[n];
-      float o[4];
+      for (int r = 0; r < RT; ++r) {
+        const u32x4 a = a_up[((4 * t + n) * RT + r) * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (int)(q << (24 - 8 * i)) >> 24;
-        const float sign = c > 0 ? 1.f : c < 0 ? -1.f : 0.f;
-        o[i] = (b >> i) & 1u ? v[i] + s * (f.p[n][i] - v[i]) + sign * per_kept : v[i] + sign * per;
+        for (int i = 0; i < 2; ++i) {
+          v[i] = mfma(a, uh[i][r], v[i]);
+          v[i] = mfma(a, ul[i][r], v[i]);
+        }
       }
-      out[2 * n] = cvt_pk_bf16(o[0], o[1]);
-      out[2 * n + 1] = cvt_pk_bf16(o[2], o[3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t b = kept_bits(f.x[i].idx >> (4 * n)), q = f.x[i].codes[n];
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = (int)(q << (24 - 8 * e)) >> 24;
+          const float sign = c > 0 ? 1.f : c < 0 ? -1.f : 0.f;
+          o[e] = (b >> e) & 1u ? v[i][e] + s[i] * (f.p[i][n][e] - v[i][e]) + sign * per_kept[i]
+                               : v[i][e] + sign * per[i];
+        }
+        out[i][2 * n] = cvt_pk_bf16(o[0], o[1]);
+        out[i][2 * n + 1] = cvt_pk_bf16(o[2], o[3]);
+      }
     }
     const int64_t k = 64 * t + 16 * quad;
-    uint16_t* y = dx + row * L.K + k;
-    if (ok && k + 16 <= L.K) {
-      __builtin_memcpy(__builtin_assume_aligned(y, 8), out, 32);
-    } else if (ok) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (k + 4 * i < L.K) *reinterpret_cast<u32x2*>(y + 4 * i) = (u32x2){out[2 * i], out[2 * i + 1]};
+    for (int i = 0; i < 2; ++i) {
+      uint16_t* y = dx + (16 * (b0 + i) + col) * L.K + k;
+      if (ok[i] && k + 16 <= L.K) {
+        __builtin_memcpy(__builtin_assume_aligned(y, 8), out[i], 32);
+      } else if (ok[i]) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (k + 4 * n < L.K) *reinterpret_cast<u32x2*>(y + 4 * n) = (u32x2){out[i][2 * n], out[i][2 * n + 1]};
+      }
     }
   };
-  if constexpr (HOLD > 0) {
-#pragma unroll
-    for (int h = 0; h < HOLD; ++h)
-      if (wave + kFinWaves * h < steps) finish(held[h], wave + kFinWaves * h);
-  } else {
-    for (int64_t t = wave; t < steps; t += kFinWaves) {
-      load(held[0], t);
-      finish(held[0], t);
-    }
+  for (int64_t t = lo + wave; t < hi; t += 8) {
+    if (t + 4 < hi) load(s1, t + 4);
+    finish(s0, t);
+    if (t + 8 < hi) load(s0, t + 8);
+    if (t + 4 < hi) finish(s1, t + 4);
   }
-}
-
-template <int RT>
-hipError_t launch_finish(const float* p, const Ckpt& ck, const BackwardLayout& L, const char* ws, uint16_t* dx,
-                         hipStream_t stream) {
-  const int64_t held = (L.kp / 64 + kFinWaves - 1) / kFinWaves;
-  auto* k = held <= 2 ? &finish_kernel<RT, 2> : held <= 6 ? &finish_kernel<RT, 6> : &finish_kernel<RT, 0>;
-  return launch(k, dim3((unsigned)((L.M + 15) / 16)), dim3(64 * kFinWaves), stream, p, ck,
-                reinterpret_cast<const u32x4*>(ws + L.off_u), reinterpret_cast<const u32x4*>(ws + L.off_a_up),
-                reinterpret_cast<const float*>(ws + L.off_d), L, dx);
 }
 
 template <int JT>
@@ -748,8 +740,7 @@ hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a
                         frag(L.off_a_down), frag(L.off_a_up), frag(L.off_b));
   if (e != hipSuccess) return e;
   const bool wg = L.N % 8 == 0, wx = L.K % 8 == 0;
-  auto* rk = wg ? (wx ? &rows_kernel<JT, true, true> : &rows_kernel<JT, true, false>)
-                : (wx ? &rows_kernel<JT, false, true> : &rows_kernel<JT, false, false>);
+  auto* rk = wg ? &rows_kernel<JT, true> : &rows_kernel<JT, false>;
   const int64_t row_groups = (L.M + 16 * kG - 1) / (16 * kG) * L.splits_g + (L.M + 16 * kX - 1) / (16 * kX) * L.splits_x;
   e = launch(rk, dim3((unsigned)row_groups), dim3(256), stream, g, frag(L.off_b), frag(L.off_a_down), ck, L, part);
   if (e != hipSuccess) return e;
@@ -769,7 +760,7 @@ hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a
 
 hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
                            const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx, uint16_t* da,
-                           uint16_t* db, char* ws, int compute_units, hipStream_t stream) {
+                           uint16_t* db, char* ws, hipStream_t stream) {
   if (L.M == 0) {                                       // no tokens: no ranges to sum, zeros
     const int64_t b = (L.r * (L.N + L.K) + 255) / 256;
     return launch(&join_columns_kernel, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), stream,
@@ -783,12 +774,20 @@ hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_
   }
   if (dx == nullptr) return hipSuccess;
   float* p = reinterpret_cast<float*>(ws + L.off_p);
-  const hipError_t e = launch_dense_gemm_f32(g, w_t, L.M, L.K, L.N, p, compute_units, stream);
+  float* d_part = reinterpret_cast<float*>(ws + L.off_d_part);
+  const hipError_t e = launch_grad_gemm(g, w_t, ck, L, p, d_part, stream);
   if (e != hipSuccess) return e;
-  return L.r == 0     ? launch_finish<0>(p, ck, L, ws, dx, stream)
-         : L.rp == 32 ? launch_finish<1>(p, ck, L, ws, dx, stream)
-         : L.rp == 64 ? launch_finish<2>(p, ck, L, ws, dx, stream)
-                      : launch_finish<4>(p, ck, L, ws, dx, stream);
+  auto* k = L.r == 0     ? &finish_kernel<0>
+            : L.rp == 32 ? &finish_kernel<1>
+            : L.rp == 64 ? &finish_kernel<2>
+                         : &finish_kernel<4>;
+  // About 4096 wavefronts (four per SIMD), each with at least one 64-channel step.
+  const int64_t groups = (L.M + 31) / 32, steps = L.kp / 64;
+  const int64_t chunk = 4 * ((groups * steps + 4095) / 4096);
+  const int64_t blocks = groups * ((steps + chunk - 1) / chunk);
+  return launch(k, dim3((unsigned)blocks), dim3(256), stream, p, d_part, ck,
+                reinterpret_cast<const u32x4*>(ws + L.off_u), reinterpret_cast<const u32x4*>(ws + L.off_a_up),
+                reinterpret_cast<const float*>(ws + L.off_d), L, chunk, dx);
 }
 
 }  // namespace rtl

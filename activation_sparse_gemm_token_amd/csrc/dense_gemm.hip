@@ -10,16 +10,19 @@
 // the same swizzled row-major layout as W, copied by the same DMA routine,
 // in a 2-stage ring next to the 3-stage W ring (96 + 64 KiB of LDS).
 //
-// A second form serves the layer's backward pass (G W, launch_dense_gemm_f32):
+// A second form serves the layer's backward pass (G W, launch_grad_gemm):
 // an fp32 result in blocks of 16 x 16, 1 KiB each, in the order in which the
 // matrix core leaves them with its operands swapped, so the stores, and the
 // loads of the kernel that follows, are contiguous.  Every 64 rows of W enter
 // LDS in the order that gives a lane 16 consecutive columns over four blocks
 // (lane l, block t of 4: row l % 16 of X, columns 16 (l / 16) + 4 t + [0, 4)).
-// It also has 192-column tiles.
+// While the result is in registers its share of D, the sum over a token's kept
+// channels of x G W, is taken too.  192-column tiles, and ranges of the
+// contraction where the tiles alone leave CUs idle.
 #include <type_traits>
 
 #include "gemm_common.hpp"
+#include "rtl_checkpoint.hpp"
 #include "rtl_kernels.hpp"
 #include "rtl_operators.hpp"
 
@@ -124,6 +127,15 @@ __device__ __forceinline__ void dma_w_ordered_dword(__amdgpu_buffer_rsrc_t wr, i
   }
 }
 
+// The tiled form's result and what it needs to form D.
+struct GradOut {
+  float* p;
+  float* d_part;
+  Ckpt ck;
+  int64_t blocks_n;                      // 16-column blocks of a row of p
+  int64_t splits;                        // ranges of the contraction
+};
+
 // KM: how channel tails are handled.  TN: tile columns, 256 or 192.  TILED: fp32
 // result in 16 x 16 blocks [M / 16][4 (N / 64)][lane][4] instead of a bf16
 // row-major one.  256 columns: 2 x 4 wavefronts of 128 x 64; 192: 4 x 2 of
@@ -132,8 +144,7 @@ __device__ __forceinline__ void dma_w_ordered_dword(__amdgpu_buffer_rsrc_t wr, i
 template <int KM, int TN, bool TILED>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
-                  int64_t M, int64_t N, int64_t K,
-                  std::conditional_t<TILED, float, uint16_t>* __restrict__ y) {
+                  int64_t M, int64_t N, int64_t K, std::conditional_t<TILED, GradOut, uint16_t* __restrict__> y) {
   static_assert(TN == 256 || (TN == 192 && TILED && KM != kAligned8), "192 columns: the tiled form's 16-byte copies");
   constexpr int kWavesN = TN == 256 ? 4 : 2, kWavesM = kWaves / kWavesN;
   constexpr int kTileN = TN, kWaveM = kTileM / kWavesM, kWaveN = TN / kWavesN;
@@ -150,10 +161,19 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   const int wm = wave / kWavesN, wn = wave % kWavesN;
   const int64_t tiles_m = (M + kTileM - 1) / kTileM, tiles_n = (N + kTileN - 1) / kTileN;
   int64_t tm, tn;
-  tile_coords(tiles_m, tiles_n, tm, tn);
+  // Tiled form: [k_lo, k_lo + ksteps) is this workgroup's range of the steps.
+  int64_t k_lo = 0, ksteps = (K + kTileK - 1) / kTileK, split = 0;
+  if constexpr (TILED) {
+    const int64_t tiles = tiles_m * tiles_n, per = (ksteps + y.splits - 1) / y.splits;
+    split = blockIdx.x / tiles;
+    tile_coords_of(blockIdx.x - split * tiles, tiles_m, tiles_n, tm, tn);
+    k_lo = split * per;
+    ksteps = ksteps - k_lo < per ? ksteps - k_lo : per;
+  } else {
+    tile_coords(tiles_m, tiles_n, tm, tn);
+  }
   const int64_t n0 = tn * kTileN;
   const int64_t m0 = tm * kTileM;
-  const int64_t ksteps = (K + kTileK - 1) / kTileK;
 
   f32x4 acc[kRB][kCB];
 #pragma unroll
@@ -179,7 +199,8 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   // vmcnt waits of its own (it cannot always prove that a copy into one
   // stage does not alias the reads of another) and the explicit waits below
   // are exact.  The K % 8 == 4 mode uses the compiler-visible dword copy.
-  auto copy_w = [&](int64_t ks, char* dst) {
+  auto copy_w = [&](int64_t step, char* dst) {
+    const int64_t ks = TILED ? k_lo + step : step;
     if constexpr (KM == kAligned8) {
       if constexpr (TILED) dma_w_ordered_dword(wr, N, K, n0, ks * kTileK, dst);
       else dma_w_tile_dword<kWaves>(wr, N, K, n0, ks * kTileK, dst);
@@ -189,7 +210,8 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
       else dma_w_tile_asm<kWaves>(wr, wo, K, ks * kTileK, lds_addr, KM == kAligned16);
     }
   };
-  auto copy_a = [&](int64_t ks, char* dst) {
+  auto copy_a = [&](int64_t step, char* dst) {
+    const int64_t ks = TILED ? k_lo + step : step;
     if constexpr (KM == kAligned8) {
       dma_w_tile_dword<kWaves>(xr, M, K, m0, ks * kTileK, dst);
     } else {
@@ -268,14 +290,58 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   barrier_no_fence();                     // every wave is done with the rings
 
   if constexpr (TILED) {
-    const int64_t tn16 = (N + 63) / 64 * 4;
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const int64_t mb = (m0 + wm * kWaveM) / 16, nb = (n0 + wn * kWaveN) / 16;
+    f32x4* const out = reinterpret_cast<f32x4*>(y.p) + (split * ((M + 15) / 16) + mb) * y.blocks_n * 64 + lane;
+    float* const red = reinterpret_cast<float*>(lds);                     // [wavefront column][256 tokens]
+    // Blocks of 64 columns that this wavefront's columns lie in (whole or part).
+    constexpr int kGroups = kCB / 4 + (kCB % 4 != 0);
+    // All of the checkpoint's loads go out first, then P's stores, so the sums
+    // wait for neither.
+    Ckpt16 f[kRB][kGroups];
+#pragma unroll
+    for (int rb = 0; rb < kRB; ++rb) {
+      const int64_t m = 16 * (mb + rb) + col, row = m < M ? m : M - 1;
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q)
+        f[rb][q] = ckpt_load16(y.ck.codes + row * N, y.ck.exps + row * ((N + 31) / 32),
+                               y.ck.idx + row * ((N + 7) / 8), 64 * ((nb >> 2) + q) + 16 * quad, N);
+    }
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb)
 #pragma unroll
       for (int cb = 0; cb < kCB; ++cb)
-        if (16 * (mb + rb) < M && nb + cb < tn16)
-          *reinterpret_cast<f32x4*>(y + (((mb + rb) * tn16 + nb + cb) * 64 + (threadIdx.x & 63)) * 4) = acc[rb][cb];
+        if (16 * (mb + rb) < M && nb + cb < y.blocks_n) out[(rb * y.blocks_n + nb + cb) * 64] = acc[rb][cb];
+    // nb % 4 is 0, or 2 for the second wavefront column of a 192-column tile.
+    const bool whole = kCB % 4 == 0 || (nb & 3) == 0;
+#pragma unroll
+    for (int rb = 0; rb < kRB; ++rb) {
+      float part[kGroups];
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) part[q] = 0.f;
+      if (whole) {
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb) part[cb / 4] += ckpt_kept_dot(f[rb][cb / 4], cb % 4, acc[rb][cb]);
+      } else {
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb)
+          part[(cb + 2) / 4 % kGroups] += ckpt_kept_dot(f[rb][(cb + 2) / 4 % kGroups], (cb + 2) % 4, acc[rb][cb]);
+      }
+      float d = 0.f;
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) d += __builtin_amdgcn_ldexpf(part[q], (int)f[rb][q].exp - 133);
+      d += __shfl_xor(d, 16, 64);
+      d += __shfl_xor(d, 32, 64);
+      if (quad == 0) red[wn * kTileM + wm * kWaveM + 16 * rb + col] = d;
+    }
+    __syncthreads();
+    const int64_t m = m0 + threadIdx.x;
+    if (threadIdx.x < kTileM && m < M) {
+      float d = 0.f;
+#pragma unroll
+      for (int v = 0; v < kWavesN; ++v) d += red[v * kTileM + threadIdx.x];
+      y.d_part[(split * tiles_n + tn) * M + m] = d;
+    }
   } else if (N % 8 == 0) {
     store_tile_via_lds<kRB, kCB>(acc, lds, y, M, N, m0 + wm * kWaveM, n0 + wn * kWaveN);
   } else {
@@ -298,20 +364,17 @@ hipError_t launch_dense_gemm(const uint16_t* x, const uint16_t* w, int64_t M, in
   return launch(k, grid, block, stream, x, w, M, N, K, y);
 }
 
-hipError_t launch_dense_gemm_f32(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N,
-                                 int64_t K, float* y, int compute_units, hipStream_t stream) {
-  // 192-column tiles when they fill the CUs in fewer rounds, weighed by what
-  // a tile takes (0.79 of a 256-column one).
-  const int64_t tiles_m = (M + kTileM - 1) / kTileM;
-  auto rounds = [&](int64_t tn) { return (tiles_m * ((N + tn - 1) / tn) + compute_units - 1) / compute_units; };
-  const bool narrow = K % 8 == 0 && rounds(192) * 79 < rounds(256) * 100;
-  const int64_t tile_n = narrow ? 192 : 256;
-  const dim3 grid((unsigned)(tiles_m * ((N + tile_n - 1) / tile_n))), block(kThreads);
-  auto* k = narrow ? (K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 192, true> : &dense_gemm_kernel<kAligned16, 192, true>)
+hipError_t launch_grad_gemm(const uint16_t* g, const uint16_t* w_t, const Ckpt& ck, const BackwardLayout& L, float* p,
+                            float* d_part, hipStream_t stream) {
+  const int64_t M = L.M, N = L.K, K = L.N;              // result columns N, contraction K
+  const GradOut out{p, d_part, ck, L.kp / 16, L.p_splits};
+  const dim3 grid((unsigned)((M + kTileM - 1) / kTileM * L.p_tiles * L.p_splits)), block(kThreads);
+  auto* k = L.p_tile == 192 ? (K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 192, true>
+                                               : &dense_gemm_kernel<kAligned16, 192, true>)
             : K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 256, true>
             : K % 8 == 0      ? &dense_gemm_kernel<kAligned16, 256, true>
                               : &dense_gemm_kernel<kAligned8, 256, true>;
-  return launch(k, grid, block, stream, x, w, M, N, K, y);
+  return launch(k, grid, block, stream, g, w_t, M, N, K, out);
 }
 
 }  // namespace rtl

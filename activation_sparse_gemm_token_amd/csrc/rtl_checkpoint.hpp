@@ -44,4 +44,41 @@ __device__ __forceinline__ u32x4 kept_masks(uint32_t byte) {
   return m;
 }
 
+// 16 channels of a token at channel k (k % 16 == 0), as the backward pass reads
+// them: one lane's share of 64.  Channels past K have code 0 and count as
+// pruned; nothing past a row is read.
+struct Ckpt16 {
+  u32x4 codes;
+  uint32_t exp, idx;                      // idx: 4 bits per group
+};
+__device__ __forceinline__ Ckpt16 ckpt_load16(const int8_t* codes, const uint8_t* exps, const uint8_t* idx,
+                                              int64_t k, int64_t K) {
+  Ckpt16 f = {{0, 0, 0, 0}, 0, 0};
+  if (k + 16 <= K) {
+    __builtin_memcpy(&f.codes, __builtin_assume_aligned(codes + k, 4), 16);
+    f.exp = exps[k / 32];
+    uint16_t two;
+    __builtin_memcpy(&two, idx + k / 8, 2);
+    f.idx = two;
+  } else if (k < K) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k + 4 * i < K) f.codes[i] = *reinterpret_cast<const uint32_t*>(codes + k + 4 * i);
+    f.exp = exps[k / 32];
+    f.idx = idx[k / 8];
+    if (k + 8 < K) f.idx |= (uint32_t)idx[k / 8 + 1] << 8;
+  }
+  return f;
+}
+
+// Sum over the kept ones of group i's 4 channels of code * p.
+__device__ __forceinline__ float ckpt_kept_dot(const Ckpt16& f, int i, f32x4 p) {
+  const uint32_t b = kept_bits(f.idx >> (4 * i)), q = f.codes[i];
+  float d = (b & 1u) ? (float)((int)(q << 24) >> 24) * p[0] : 0.f;
+  d += (b & 2u) ? (float)((int)(q << 16) >> 24) * p[1] : 0.f;
+  d += (b & 4u) ? (float)((int)(q << 8) >> 24) * p[2] : 0.f;
+  d += (b & 8u) ? (float)((int)q >> 24) * p[3] : 0.f;
+  return d;
+}
+
 }  // namespace rtl

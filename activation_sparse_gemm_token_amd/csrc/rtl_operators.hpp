@@ -51,12 +51,6 @@ hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_
 hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K,
                                     uint16_t* y, hipStream_t stream);
 
-// x [M, K] w [N, K]^T with an fp32 result in 16 x 16 blocks:
-// [ceil(M / 16)][4 ceil(N / 64)][lane][4], lane l of block t of every four holding
-// row l % 16, columns 16 (l / 16) + 4 t + [0, 4) of the 64 (dense_gemm.hip).
-hipError_t launch_dense_gemm_f32(const uint16_t* x, const uint16_t* w, int64_t M, int64_t N, int64_t K,
-                                 float* y, int compute_units, hipStream_t stream);
-
 // Sizes, splits and workspace regions of the layer's backward pass.  Rank is
 // padded to 32, 64 or 128, channels and tokens to 64 (zeros).  Operands of the
 // matrix cores are kept in fragments of 1 KiB: [lane][8] bf16, lane l holding
@@ -67,11 +61,20 @@ struct BackwardLayout {
   int64_t chunk_g, chunk_x;                        // channels per workgroup of the token-by-rank products
   int64_t splits_g, splits_x;
   int64_t chunk_t, splits_t;                       // tokens per workgroup of the products over tokens
-  size_t off_a_down, off_a_up, off_b, off_u, off_uc, off_tc, off_d, off_part, off_p, total;
+  int64_t p_tile, p_tiles, p_splits;               // G W: tile columns, their number, contraction ranges
+  size_t off_a_down, off_a_up, off_b, off_u, off_uc, off_tc, off_d, off_part, off_p, off_d_part, total;
 };
 BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t r);
+// The backward pass's P = G W on the dense GEMM's ring (dense_gemm.hip): the
+// contraction over N in L.p_splits ranges, each an fp32 result in 16 x 16
+// blocks, [range][ceil(M / 16)][kp / 16][lane][4], lane l of block t of every
+// four holding token l % 16, channels 16 (l / 16) + 4 t + [0, 4) of the 64; and of
+// each tile and range the sums of kept x * P over the tile's channels, d_part
+// [range][tile][M].
+hipError_t launch_grad_gemm(const uint16_t* g, const uint16_t* w_t, const Ckpt& ck, const BackwardLayout& L,
+                            float* p, float* d_part, hipStream_t stream);
 hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
                            const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx,
-                           uint16_t* da, uint16_t* db, char* workspace, int compute_units, hipStream_t stream);
+                           uint16_t* da, uint16_t* db, char* workspace, hipStream_t stream);
 
 }  // namespace rtl

@@ -22,10 +22,11 @@ bool back_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
 
 }  // namespace
 
-// Splits by sizes alone (a workspace must fit whatever device it is used on):
-// about two workgroups per CU of the card for the products over G's channels
-// and over tokens, one for those over the checkpoint's channels, no workgroup
-// with less than one step of each of its four wavefronts.
+// Splits by sizes alone (a workspace must fit whatever device it is used on).
+// Two workgroups of these kernels fit a CU, so the split sizes aim at all of
+// them running at once: 384 workgroups over G's channels (and, short ones, 512
+// over the checkpoint's), 512 over tokens; a range is a whole number of steps of
+// the workgroup's four wavefronts.
 rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
   constexpr int64_t kCus = 256;
   BackwardLayout L{};
@@ -34,18 +35,40 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   L.np = round_up(N, 64);
   L.kp = round_up(K, 64);
   L.mp = round_up(M, 64);
-  auto chunk = [](int64_t work, int64_t groups, int64_t step) {
-    const int64_t c = (work + groups - 1) / groups;
-    return round_up(c < step ? step : c, step);
+  // `length` in as many ranges as `groups` workgroups make of `blocks` blocks.
+  auto chunk = [](int64_t length, int64_t groups, int64_t blocks, int64_t step) {
+    const int64_t splits = blocks > 0 && groups > blocks ? groups / blocks : 1;
+    return length > 0 ? round_up((length + splits - 1) / splits, step) : step;
   };
   const int64_t rows_g = L.rp == 128 ? 32 : 64, rows_x = rows_g / 2;    // tokens per workgroup
-  L.chunk_g = chunk((M + rows_g - 1) / rows_g * L.np, 2 * kCus, 256);
+  L.chunk_g = chunk(L.np, 3 * kCus / 2, (M + rows_g - 1) / rows_g, 256);
   L.splits_g = (L.np + L.chunk_g - 1) / L.chunk_g;
-  L.chunk_x = chunk((M + rows_x - 1) / rows_x * L.kp, kCus, 256);
+  L.chunk_x = chunk(L.kp, 2 * kCus, (M + rows_x - 1) / rows_x, 256);
   L.splits_x = (L.kp + L.chunk_x - 1) / L.chunk_x;
   const int64_t cols_g = L.rp == 128 ? 64 : 128, cols_x = cols_g / 2;   // channels per workgroup
-  L.chunk_t = chunk(((N + cols_g - 1) / cols_g + (K + cols_x - 1) / cols_x) * L.mp, 2 * kCus, 128);
+  L.chunk_t = chunk(L.mp, 2 * kCus, (N + cols_g - 1) / cols_g + (K + cols_x - 1) / cols_x, 128);
   L.splits_t = (L.mp + L.chunk_t - 1) / L.chunk_t;
+  // G W: tile columns and contraction ranges by the time they should take, in
+  // us: a k-step of 64 measured 1.65 (256 columns) and 1.25 (192) with the chip
+  // full, plus 8 per tile, plus writing and reading the ranges' results.
+  const int64_t tiles_m = (M + 255) / 256, steps = (N + 63) / 64;
+  double best = 0;
+  for (int64_t tn : {256, 192}) {
+    if (tn == 192 && N % 8 != 0) continue;
+    const int64_t tiles = (K + tn - 1) / tn;
+    for (int64_t s = 1; s <= 16 && (s == 1 || steps / s >= 4); ++s) {
+      const int64_t rounds = (tiles_m * tiles * s + kCus - 1) / kCus, per = (steps + s - 1) / s;
+      if (s > 1 && (s - 1) * per >= steps) continue;                    // the last range would be empty
+      const double t = (double)rounds * ((double)per * (tn == 256 ? 1.65 : 1.25) + 8) +
+                       (double)s * (double)M * (double)L.kp * 8 / 5e6;
+      if (best == 0 || t < best) {
+        best = t;
+        L.p_tile = tn;
+        L.p_tiles = tiles;
+        L.p_splits = s;
+      }
+    }
+  }
   size_t o = 0;
   auto take = [&](int64_t bytes) { const size_t at = o; o += ((size_t)bytes + 255) / 256 * 256; return at; };
   L.off_a_down = take(L.rp * L.kp * 2);
@@ -58,7 +81,8 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   const int64_t rows = (L.splits_g + 2 * L.splits_x) * M * L.rp * 4;
   const int64_t over_t = L.splits_t * (N + L.kp) * L.rp * 4;
   L.off_part = take(rows > over_t ? rows : over_t);
-  L.off_p = take(round_up(M, 16) * L.kp * 4);
+  L.off_p = take(L.p_splits * round_up(M, 16) * L.kp * 4);
+  L.off_d_part = take(L.p_splits * L.p_tiles * M * 4);
   L.total = o;
   return L;
 }
@@ -120,10 +144,9 @@ RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* c
     if (workspace == nullptr || workspace_bytes < rtl::backward_layout(M, N, K, r).total) return RTL_ERR_WORKSPACE;
     if (!rtl::aligned(workspace, 16)) return RTL_ERR_MISALIGNED;
   }
-  int cus = 0;
-  const rtl_status d = rtl::check_device(stream, &cus);
+  const rtl_status d = rtl::check_device(stream);
   if (d != RTL_OK) return d;
   const rtl::Ckpt ck{codes, exps, idx, stats};
   return rtl::from_hip(rtl::launch_backward(g, ck, w_t, lora_a, lora_b, rtl::backward_layout(M, N, K, r), lora_scale,
-                                            dx, da, db, static_cast<char*>(workspace), cus > 0 ? cus : 1, stream));
+                                            dx, da, db, static_cast<char*>(workspace), stream));
 }
