@@ -21,6 +21,7 @@ Entry points (same names as the C ABI in include/rtlynx.h, without the
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -128,7 +129,12 @@ def _as_2d(t, name: str):
 
 
 def _stream():
-    return _torch().cuda.current_stream().cuda_stream
+    """The current device's current stream (inside ``_on``: the tensors')."""
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+_HERE_CONTEXT = contextlib.nullcontext()                # the device is current already
 
 
 def _on(device, **tensors):
@@ -138,7 +144,8 @@ def _on(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, the inputs on {device}")
-    return _torch().cuda.device(device)
+    cuda = _torch().cuda
+    return _HERE_CONTEXT if cuda.current_device() == device.index else cuda.device(device)
 
 
 def _out(out, m: int, n: int, lead, device):

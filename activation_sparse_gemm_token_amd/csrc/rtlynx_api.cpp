@@ -83,15 +83,19 @@ void* scratch_address(int dev) {
 }  // namespace
 
 rtl_status rtl::check_device(hipStream_t stream, int* cus) {
-  int count = 0;
-  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
-    (void)hipGetLastError();
-    return RTL_ERR_NO_DEVICE;
-  }
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) {
     (void)hipGetLastError();
     return RTL_ERR_NO_DEVICE;
+  }
+  // A device whose architecture is known exists: only the first call on it
+  // asks for the number of devices.
+  if (dev < 0 || dev >= kMaxDevices || g_arch_ok[dev].load(std::memory_order_relaxed) == 0) {
+    int count = 0;
+    if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
+      (void)hipGetLastError();
+      return RTL_ERR_NO_DEVICE;
+    }
   }
   if (stream != nullptr) {
     // The kernels run on the stream's device with the current device's

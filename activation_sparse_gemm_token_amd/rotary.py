@@ -22,11 +22,12 @@ _c_i64, _c_vp = ctypes.c_int64, ctypes.c_void_p
 
 
 class _Tensor(ctypes.Structure):
+    """rtl_rope_tensor."""
     _fields_ = [("x", _c_vp), ("y", _c_vp), ("heads", _c_i64)] + [
         (f"{t}_{d}_stride", _c_i64) for t in "xy" for d in ("batch", "token", "head")]
 
 
-_SIG = (ctypes.c_int, [ctypes.POINTER(_Tensor), ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
+_SIG = (ctypes.c_int, [_c_vp, ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
                        ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), _c_vp, ctypes.c_float, ctypes.c_uint32, _c_vp])
 
 
@@ -125,79 +126,99 @@ def _apart(a, b):
     return nested and off >= first and off + second <= room
 
 
-def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, inverse):
-    torch = _torch()
-    if layout not in LAYOUTS:
-        raise ValueError(f"layout must be one of {LAYOUTS}, got {layout!r}")
-    if x.dtype not in (torch.bfloat16, torch.float16, torch.float32):
-        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    if x.dim() not in (3, 4):
-        raise ValueError("x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim]")
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    ins = [("x", x, out)] + ([("k", k, k_out)] if k is not None else [])
-    lead, dim, outs = tuple(x.shape[:-2]), x.shape[-1], []
-    for name, t, o in ins:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
-        if t.dtype != x.dtype:
-            raise TypeError(f"{name} must be {x.dtype} like x, got {t.dtype}")
-        if t.dim() != x.dim() or tuple(t.shape[:-2]) != lead or t.shape[-1] != dim:
-            raise ValueError(f"{name} must have shape {lead + ('heads', dim)}, got {tuple(t.shape)}")
-        if dim > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name}: the channel stride must be 1")
-        if o is None:
-            o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        else:
-            if o.dtype != t.dtype:
-                raise TypeError(f"out of {name} must be {t.dtype}, got {o.dtype}")
-            if o.device != t.device or o.shape != t.shape:
-                raise ValueError(f"out of {name} must be on {t.device} with shape {tuple(t.shape)}")
-            if (dim > 1 and o.stride(-1) != 1) or not _distinct(o):
-                raise ValueError(f"out of {name} must have a channel stride of 1 and no overlapping elements")
-        outs.append(o)
-    given = out is not None or k_out is not None
-    for i, o in enumerate(outs if given else ()):
+def _check_out(name, t, o):
+    if o.dtype != t.dtype:
+        raise TypeError(f"out of {name} must be {t.dtype}, got {o.dtype}")
+    if o.device != t.device or o.shape != t.shape:
+        raise ValueError(f"out of {name} must be on {t.device} with shape {tuple(t.shape)}")
+    if (t.shape[-1] > 1 and o.stride(-1) != 1) or not _distinct(o):
+        raise ValueError(f"out of {name} must have a channel stride of 1 and no overlapping elements")
+
+
+def _check_overlap(ins, outs):
+    """An output may be its own input and shares no element with any other tensor."""
+    for i, o in enumerate(outs):
         for j, (name, t, _) in enumerate(ins):
             if o.numel() and t.numel() and not (i == j and _same(o, t)) and not _apart(o, t):
                 raise ValueError(f"an output overlaps {name} (it may be its own input, or share no element with any)")
-    if given and len(outs) == 2 and outs[0].numel() and outs[1].numel() and not _apart(outs[0], outs[1]):
+    if len(outs) == 2 and outs[0].numel() and outs[1].numel() and not _apart(outs[0], outs[1]):
         raise ValueError("the two outputs overlap")
 
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+
+def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, inverse):
+    torch = _torch()
+    dtype, shape = x.dtype, x.shape
+    if dtype is torch.bfloat16:
+        flags = 0
+    elif dtype is torch.float16:
+        flags = 1
+    elif dtype is torch.float32:
+        flags = 2
+    else:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {dtype}")
+    if layout == "interleaved":
+        flags |= _INTERLEAVED
+    elif layout != "half":
+        raise ValueError(f"layout must be one of {LAYOUTS}, got {layout!r}")
+    if inverse:
+        flags |= _INVERSE
+    if len(shape) not in (3, 4):
+        raise ValueError("x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim]")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    lead, dim = shape[:-2], shape[-1]
+    batched = len(lead) == 2
+    ins = (("x", x, out),) if k is None else (("x", x, out), ("k", k, k_out))
+    outs, words = [], []
+    for name, t, o in ins:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        ts, st = t.shape, t.stride()
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype} like x, got {t.dtype}")
+        if ts[:-2] != lead or ts[-1] != dim:
+            raise ValueError(f"{name} must have shape {(*lead, 'heads', dim)}, got {tuple(ts)}")
+        if dim > 1 and st[-1] != 1:
+            raise ValueError(f"{name}: the channel stride must be 1")
+        if o is None:
+            o = t.new_empty(ts)
+        else:
+            _check_out(name, t, o)
+        so = o.stride()
+        words += (t.data_ptr(), o.data_ptr(), ts[-2])
+        words += (*st[:3], *so[:3]) if batched else (0, *st[:2], 0, *so[:2])
+        outs.append(o)
+    if out is not None or k_out is not None:
+        _check_overlap(ins, outs)
+
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous float64 vector")
     rot = 2 * inv_freq.shape[0]
     if rot > dim:
         raise ValueError(f"inv_freq has {rot // 2} pairs, a head {dim} channels")
-    axes = 1 if sections is None else len(sections)
-    if sections is not None and (any(int(s) < 0 for s in sections) or sum(int(s) for s in sections) != rot // 2):
-        raise ValueError(f"sections must be counts that sum to {rot // 2} pairs, got {list(sections)}")
-    if positions.dtype != torch.int64:
+    axes, pairs, tail = 1, None, ()
+    if sections is not None:
+        counts = [int(s) for s in sections]
+        if any(s < 0 for s in counts) or sum(counts) != rot // 2:
+            raise ValueError(f"sections must be counts that sum to {rot // 2} pairs, got {counts}")
+        axes, tail = len(counts), (len(counts),)
+        pairs = (ctypes.c_int32 * axes)(*counts)
+    if positions.dtype is not torch.int64:
         raise TypeError(f"positions must be int64, got {positions.dtype}")
-    tail = () if sections is None else (axes,)
-    if tuple(positions.shape) == lead + tail:
-        pos = positions
-    elif len(lead) == 2 and tuple(positions.shape) == lead[1:] + tail:
-        pos = positions.unsqueeze(0).expand(lead + tail)
+    ps, pos = positions.shape, positions.stride()
+    if ps == lead + tail:
+        pos_b, pos_t = pos[:2] if batched else (0, pos[0])
+    elif batched and ps == lead[1:] + tail:                       # one row of positions for every sequence
+        pos_b, pos_t = 0, pos[0]
     else:
-        raise ValueError(f"positions must have shape {lead + tail}" +
-                         (f" or {lead[1:] + tail}" if len(lead) == 2 else "") + f", got {tuple(positions.shape)}")
-    if sections is not None and axes > 1 and pos.stride(-1) != 1:
+        raise ValueError(f"positions must have shape {(*lead, *tail)}" +
+                         (f" or {(*lead[1:], *tail)}" if batched else "") + f", got {tuple(ps)}")
+    if axes > 1 and pos[-1] != 1:
         raise ValueError("positions: the axis stride must be 1")
-    batch, tokens = (1, lead[0]) if len(lead) == 1 else lead
-    pos_b, pos_t = (0, pos.stride(0)) if len(lead) == 1 else (pos.stride(0), pos.stride(1))
-
-    def strides(t):
-        return (0, t.stride(0), t.stride(1)) if len(lead) == 1 else (t.stride(0), t.stride(1), t.stride(2))
-
-    arr = (_Tensor * len(ins))(*[_Tensor(t.data_ptr(), o.data_ptr(), t.shape[-2], *strides(t), *strides(o))
-                                 for (_, t, _), o in zip(ins, outs)])
-    pairs = (ctypes.c_int32 * axes)(*[int(s) for s in sections]) if sections is not None else None
-    flags = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[x.dtype]
-    flags |= (_INTERLEAVED if layout == "interleaved" else 0) | (_INVERSE if inverse else 0)
+    batch, tokens = lead if batched else (1, lead[0])
     with _on(x.device, k=k, positions=positions, inv_freq=inv_freq):
-        st = _fn()(arr, len(ins), batch, tokens, dim, rot, pos.data_ptr(), pos_b, pos_t, axes, pairs,
-                   inv_freq.data_ptr(), float(scale), flags, _stream())
+        st = _fn()((ctypes.c_int64 * len(words))(*words), len(ins), batch, tokens, dim, rot, positions.data_ptr(),
+                   pos_b, pos_t, axes, pairs, inv_freq.data_ptr(), float(scale), flags, _stream())
     _check(st, "rtl_rope")
     return outs[0] if k is None else tuple(outs)
 

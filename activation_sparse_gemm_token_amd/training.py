@@ -58,13 +58,22 @@ class Checkpoint:
                 raise ValueError(f"{name} must be a contiguous device tensor")
             if t.device != codes.device:
                 raise ValueError(f"{name} is on {t.device}, codes on {codes.device}")
-        self.codes, self.exps, self.idx, self.stats = codes, exps, idx, stats
-        self.m, self.k, self.lead = m, k, (m,) if lead is None else tuple(lead)
+        self._set(codes, exps, idx, stats, (m,) if lead is None else tuple(lead))
+
+    def _set(self, codes, exps, idx, stats, lead):
+        self.codes, self.exps, self.idx, self.stats, self.lead = codes, exps, idx, stats, lead
+        self.m, self.k = codes.shape
+
+    @classmethod
+    def _made(cls, codes, exps, idx, stats, lead):
+        """A checkpoint of tensors that ``checkpoint`` made: nothing to check."""
+        kept = cls.__new__(cls)
+        kept._set(codes, exps, idx, stats, tuple(lead))
+        return kept
 
     def unpack(self, out=None):
         """The stored values [*lead, k] in bf16 (exact)."""
-        y = unpack(self.codes, self.exps, out=out)
-        return y.reshape(*self.lead, self.k)
+        return unpack(self.codes, self.exps, out=out).view(*self.lead, self.k)
 
 
 def checkpoint(x) -> Checkpoint:
@@ -72,15 +81,15 @@ def checkpoint(x) -> Checkpoint:
     torch = _torch()
     x2 = _as_2d(x, "x")
     m, k = x2.shape
-    codes = torch.empty((m, k), dtype=torch.int8, device=x2.device)
-    exps = torch.empty((m, (k + 31) // 32), dtype=torch.uint8, device=x2.device)
-    idx = torch.empty((m, (k + 7) // 8), dtype=torch.uint8, device=x2.device)
-    stats = torch.empty((m, 2), dtype=torch.float32, device=x2.device)
+    codes = x2.new_empty((m, k), dtype=torch.int8)
+    exps = x2.new_empty((m, (k + 31) // 32), dtype=torch.uint8)
+    idx = x2.new_empty((m, (k + 7) // 8), dtype=torch.uint8)
+    stats = x2.new_empty((m, 2), dtype=torch.float32)
     with _on(x2.device):
         st = _fn("rtl_checkpoint_pack")(x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), idx.data_ptr(),
                                         stats.data_ptr(), _stream())
     _check(st, "rtl_checkpoint_pack")
-    return Checkpoint(codes, exps, idx, stats, x.shape[:-1])
+    return Checkpoint._made(codes, exps, idx, stats, x.shape[:-1])
 
 
 def unpack(codes, exps, out=None):
@@ -112,7 +121,6 @@ def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, l
 
     ``w_t`` [k, n] is the frozen weight transposed, laid out once
     (``w.t().contiguous()``); it may be None when ``need_dx`` is False."""
-    torch = _torch()
     g2 = _as_2d(g, "g")
     m, n = g2.shape
     k = kept.k
@@ -133,10 +141,11 @@ def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, l
         if lora_a.shape[1] != k or tuple(lora_b.shape) != (n, r):
             raise ValueError(f"LoRA shapes {tuple(lora_a.shape)}, {tuple(lora_b.shape)} do not match K={k}, N={n}")
     dev = g2.device
-    dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev) if need_dx else None
+    lead = g.shape[:-1]
+    dx = g2.new_empty((*lead, k)) if need_dx else None
     lora = need_lora and r > 0
-    da = torch.empty((r, k), dtype=torch.bfloat16, device=dev) if lora else None
-    db = torch.empty((n, r), dtype=torch.bfloat16, device=dev) if lora else None
+    da = g2.new_empty((r, k)) if lora else None
+    db = g2.new_empty((n, r)) if lora else None
     workspace = _workspace(workspace, backward_workspace_bytes(m, n, k, r), dev)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     with _on(dev, kept=kept.codes, w_t=w_t, lora_a=lora_a, lora_b=lora_b):
@@ -145,4 +154,4 @@ def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, l
             ptr(w_t), ptr(lora_a) if r else None, ptr(lora_b) if r else None, m, n, k, r, float(lora_scale), ptr(dx),
             ptr(da), ptr(db), workspace.data_ptr(), workspace.numel(), _stream())
     _check(st, "rtl_sparse_linear_backward")
-    return None if dx is None else dx.reshape(*g.shape[:-1], k), da, db
+    return dx, da, db

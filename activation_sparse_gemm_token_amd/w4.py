@@ -77,9 +77,9 @@ def linear(x, weight: Weight, out=None):
     m, k = x2.shape
     if k != weight.k:
         raise ValueError(f"the weight has {weight.k} input channels, x has {k}")
-    y = _out(out, m, weight.n, x.shape[:-1], x2.device)
+    y = x2.new_empty((*x.shape[:-1], weight.n)) if out is None else _out(out, m, weight.n, x.shape[:-1], x2.device)
     with _on(x2.device, weight=weight.packed):
         st = _fn("rtl_w4_linear")(x2.data_ptr(), weight.packed.data_ptr(), weight.packed.numel(), m, weight.n, k,
                                   weight.group, _ZEROS if weight.zeros else 0, y.data_ptr(), _stream())
     _check(st, "rtl_w4_linear")
-    return y.reshape(*x.shape[:-1], weight.n)
+    return y if out is None else y.view(*x.shape[:-1], weight.n)
