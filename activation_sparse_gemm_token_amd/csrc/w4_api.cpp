@@ -5,10 +5,12 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxN = (int64_t)1 << 31;
+// 64 rows of x are addressed with 32-bit offsets.
+constexpr int64_t kMaxK = RTL_W4_MAX_CHANNELS;
 
 bool weight_ok(int64_t N, int64_t K, int64_t group) {
-  return N >= 1 && N < kMaxDim && K >= 1 && K < kMaxDim && (group == 32 || group == 64 || group == 128) &&
+  return N >= 1 && N < kMaxN && K >= 1 && K <= kMaxK && (group == 32 || group == 64 || group == 128) &&
          K % group == 0;
 }
 

@@ -31,13 +31,14 @@ extern "C" {
 /* flags: the weight has zero points. */
 #define RTL_W4_ZEROS 0x1u
 
-/* Most rows of one call. */
+/* Most rows of one call, and channels of a weight. */
 #define RTL_W4_MAX_ROWS (1 << 20)
+#define RTL_W4_MAX_CHANNELS (1 << 22)
 
 /*
  * rtl_w4_packed_bytes - size of the packed form of a weight [N, K].  Returns 0
- * for invalid sizes (N < 1, K < 1, group not 32, 64 or 128, K % group != 0) or
- * unknown flags.
+ * for invalid sizes (N < 1, K < 1, K > RTL_W4_MAX_CHANNELS, group not 32, 64 or
+ * 128, K % group != 0) or unknown flags.
  */
 size_t rtl_w4_packed_bytes(int64_t N, int64_t K, int64_t group, uint32_t flags);
 

@@ -34,7 +34,8 @@ def test_packed_bytes():
 
 @pytest.mark.parametrize("call", [_pack, _linear])
 def test_refusals(call):
-    for bad in (dict(n=0), dict(n=-1), dict(k=0), dict(k=100), dict(group=16), dict(group=0), dict(n=1 << 31)):
+    for bad in (dict(n=0), dict(n=-1), dict(k=0), dict(k=100), dict(group=16), dict(group=0), dict(n=1 << 31),
+                dict(k=(1 << 22) + 128)):
         assert call(**bad) == SHAPE, bad
     assert call(flags=2) == FLAGS
     assert call(p=None) == NULLP and call(p=P2 + 8) == MISAL

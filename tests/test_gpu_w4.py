@@ -66,7 +66,9 @@ def check(got, ref, tol):
 @pytest.mark.parametrize("group", w4.GROUPS)
 @pytest.mark.parametrize("m,k,n", [(1, 128, 16), (1, 256, 1), (2, 384, 15), (3, 640, 17), (15, 1152, 333), (16, 2048, 64),
                                    (17, 128, 48), (31, 1280, 65), (32, 896, 160), (33, 1024, 100), (64, 1408, 257),
-                                   (65, 256, 130), (200, 512, 70), (1, 12288, 40)])
+                                   (65, 256, 130), (200, 512, 70), (1, 12288, 40), (8, 1152, 4100),
+                                   (3, 1088 * 2, 4112), (9, 1280, 4097), (16, 1152, 8200), (17, 1152, 8208), (32, 640, 8209),
+                                   (33, 1152, 8200), (100, 384, 8193), (16, 1024, 33), (7, 896, 4096)])
 def test_sizes(m, k, n, group, zeros):
     say(m, k, n, group, zeros)
     t = make(m, k, n, group, zeros)
