@@ -56,48 +56,32 @@ __device__ __forceinline__ Split split8(const float (&v)[8]) {
   return r;
 }
 
-// 8 channels of a row at channel c of C (C % 4 == 0): rows are 16-byte aligned
-// when WIDE (C % 8 == 0), else 8-byte, with half a unit at the end.
+// 8 channels at channel c of a row of C (C % 4 == 0) of a bf16 tensor, `row` its
+// byte offset; zeros past C and past the tensor.  Rows are 16-byte aligned when
+// WIDE (C % 8 == 0), else 8-byte, with half a unit at the end.
 template <bool WIDE>
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t c, int64_t C, bool ok) {
-  u32x4 v = {0, 0, 0, 0};
+__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t t, uint32_t row, int c, int C) {
   if constexpr (WIDE) {
-    if (ok && c < C) v = *reinterpret_cast<const u32x4*>(row + c);
+    return buf_load16(t, c < C ? row + 2u * c : kOobOffset);
   } else {
-    if (ok && c < C) {
-      const u32x2 a = *reinterpret_cast<const u32x2*>(row + c);
-      v[0] = a[0];
-      v[1] = a[1];
-      if (c + 8 <= C) {
-        const u32x2 b = *reinterpret_cast<const u32x2*>(row + c + 4);
-        v[2] = b[0];
-        v[3] = b[1];
-      }
-    }
+    const u32x2 a = buf_load8(t, c < C ? row + 2u * c : kOobOffset);
+    const u32x2 b = buf_load8(t, c + 4 < C ? row + 2u * c + 8u : kOobOffset);
+    return (u32x4){a[0], a[1], b[0], b[1]};
   }
-  return v;
 }
 
-// The checkpoint's 8 channels at channel c, raw, then pruned and kept values.
+// 8 channels of the checkpoint at channel c, raw, then pruned and kept values.
 struct CkptRaw {
   u32x2 q;
   uint32_t e, idx;
 };
 template <bool WIDE>
-__device__ __forceinline__ CkptRaw ckpt_load(const Ckpt& k, int64_t row, int64_t c, int64_t K, bool ok) {
-  CkptRaw r = {{0, 0}, 0, 0};
-  if (ok && c < K) {
-    const int8_t* p = k.codes + row * K + c;
-    if constexpr (WIDE) {
-      r.q = *reinterpret_cast<const u32x2*>(p);
-    } else {
-      r.q[0] = *reinterpret_cast<const uint32_t*>(p);
-      if (c + 8 <= K) r.q[1] = *reinterpret_cast<const uint32_t*>(p + 4);
-    }
-    r.e = k.exps[row * ((K + 31) / 32) + c / 32];
-    r.idx = k.idx[row * ((K + 7) / 8) + c / 8];
-  }
-  return r;
+__device__ __forceinline__ CkptRaw ckpt_load8(const CkptRsrc& k, const CkptRow& r, int c, int K) {
+  CkptRaw f;
+  f.q = buf_load8(k.codes, c < K ? r.codes + c : kOobOffset);
+  f.e = __builtin_amdgcn_raw_buffer_load_b8(k.exps, c < K ? r.exps + c / 32 : kOobOffset, 0, 0);
+  f.idx = __builtin_amdgcn_raw_buffer_load_b8(k.idx, c < K ? r.idx + c / 8 : kOobOffset, 0, 0);
+  return f;
 }
 __device__ __forceinline__ void ckpt_split(const CkptRaw& r, u32x4& pruned, u32x4& kept) {
   const u32x4 v = ckpt_values(r.q, (int)r.e), m = kept_masks(r.idx);
@@ -108,7 +92,7 @@ __device__ __forceinline__ void ckpt_split(const CkptRaw& r, u32x4& pruned, u32x
   }
 }
 __device__ __forceinline__ void ckpt_split(const Ckpt16& r, int half, u32x4& pruned, u32x4& kept) {
-  ckpt_split(CkptRaw{{r.codes[2 * half], r.codes[2 * half + 1]}, r.exp, r.idx >> (8 * half)}, pruned, kept);
+  ckpt_split(CkptRaw{{r.codes[2 * half], r.codes[2 * half + 1]}, r.exp, half ? r.idx1 : r.idx0}, pruned, kept);
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -187,19 +171,16 @@ __device__ __forceinline__ void g_rows(const uint16_t* __restrict__ g, const u32
   f32x4 acc[MT * JT];
 #pragma unroll
   for (int i = 0; i < MT * JT; ++i) acc[i] = kZero4;
-  const uint16_t* row[MT];
-  bool ok[MT];
+  const __amdgpu_buffer_rsrc_t gr = make_rsrc(g, L.M * L.N * 2);
+  const int N = (int)L.N;
+  uint32_t row[MT];                                     // tokens past M lie past the end: zeros
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + 16 * i + col;
-    ok[i] = m < L.M;
-    row[i] = g + (ok[i] ? m : 0) * L.N;
-  }
+  for (int i = 0; i < MT; ++i) row[i] = (uint32_t)((m0 + 16 * i + col) * L.N * 2);
   auto load = [&](Stage& s, int64_t c) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) s.x[i][h] = load8<WIDE>(row[i], c + 32 * h + 8 * quad, L.N, ok[i]);
+      for (int i = 0; i < MT; ++i) s.x[i][h] = load8<WIDE>(gr, row[i], (int)c + 32 * h + 8 * quad, N);
 #pragma unroll
       for (int j = 0; j < JT; ++j) s.w[h][j] = b[((c / 32 + h) * JT + j) * 64 + lane];
     }
@@ -215,11 +196,18 @@ __device__ __forceinline__ void g_rows(const uint16_t* __restrict__ g, const u32
   Stage s0, s1;
   int64_t c = lo + 64 * wave;
   if (c < hi) load(s0, c);
-  for (; c < hi; c += 512) {
-    if (c + 256 < hi) load(s1, c + 256);
+  for (; c + 512 < hi; c += 512) {
+    load(s1, c + 256);
     use(s0);
-    if (c + 512 < hi) load(s0, c + 512);
-    if (c + 256 < hi) use(s1);
+    load(s0, c + 512);
+    use(s1);
+  }
+  if (c + 256 < hi) {
+    load(s1, c + 256);
+    use(s0);
+    use(s1);
+  } else if (c < hi) {
+    use(s0);
   }
   join_waves<MT * JT>(acc, lds, wave, lane);
   if (wave != 0) return;
@@ -248,25 +236,22 @@ __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__
   f32x4 acc[2 * MT * JT];                               // pruned, kept
 #pragma unroll
   for (int i = 0; i < 2 * MT * JT; ++i) acc[i] = kZero4;
-  // Tokens past M read the last one's; their products are not stored.
-  const int8_t* codes[MT];
-  const uint8_t *exps[MT], *idx[MT];
+  const CkptRsrc kr = ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K);
+  const int K = (int)L.K;
+  CkptRow row[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + 16 * i + col, row = m < L.M ? m : L.M - 1;
-    codes[i] = ck.codes + row * L.K;
-    exps[i] = ck.exps + row * ((L.K + 31) / 32);
-    idx[i] = ck.idx + row * ((L.K + 7) / 8);
-  }
+  for (int i = 0; i < MT; ++i) row[i] = ckpt_row(m0 + 16 * i + col, L.K);
   auto load = [&](Stage& s, int64_t c) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) s.x[i] = ckpt_load16(codes[i], exps[i], idx[i], c + 16 * quad, L.K);
+    for (int i = 0; i < MT; ++i) s.x[i] = ckpt_load16(kr, row[i], (int)c + 16 * quad, K);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < JT; ++j) s.w[h][j] = a[((c / 32 + h) * JT + j) * 64 + lane];
   };
-  auto use = [&](const Stage& s) {
+  auto use = [&](Stage& s, int64_t c) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ckpt_clip16(s.x[i], (int)c + 16 * quad, K);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -283,11 +268,18 @@ __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__
   Stage s0, s1;
   int64_t c = lo + 64 * wave;
   if (c < hi) load(s0, c);
-  for (; c < hi; c += 512) {
-    if (c + 256 < hi) load(s1, c + 256);
-    use(s0);
-    if (c + 512 < hi) load(s0, c + 512);
-    if (c + 256 < hi) use(s1);
+  for (; c + 512 < hi; c += 512) {
+    load(s1, c + 256);
+    use(s0, c);
+    load(s0, c + 512);
+    use(s1, c + 256);
+  }
+  if (c + 256 < hi) {
+    load(s1, c + 256);
+    use(s0, c);
+    use(s1, c + 256);
+  } else if (c < hi) {
+    use(s0, c);
   }
   join_waves<2 * MT * JT>(acc, lds, wave, lane);
   if (wave != 0) return;
@@ -305,7 +297,7 @@ __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__
 }
 
 template <int JT, bool WIDE_G>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 rows_kernel(const uint16_t* __restrict__ g, const u32x4* __restrict__ b, const u32x4* __restrict__ a, Ckpt ck,
             BackwardLayout L, float* __restrict__ part) {
   constexpr int kG = JT == 8 ? 2 : 4, kX = kG / 2;      // 16-token tiles per workgroup
@@ -469,21 +461,22 @@ __device__ __forceinline__ void g_columns(const uint16_t* __restrict__ g, const 
 #pragma unroll
   for (int i = 0; i < CT * JT; ++i) acc[i] = kZero4;
   u32x4 v[T::kLoads], w[2 * JT];
-  auto load = [&](int64_t t) {
+  const __amdgpu_buffer_rsrc_t gr = make_rsrc(g, L.M * L.N * 2);
+  // Past the range: its last tokens again, unused.  Tokens past M: zeros.
+  auto load = [&](int64_t at) {
+    const int64_t t = at < hi ? at : hi - 32;
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) {
-      const int64_t m = t + lr + T::kRows * i;
-      v[i] = load8<WIDE>(g + (m < L.M ? m : 0) * L.N, c0 + lc, L.N, m < L.M);
-    }
+    for (int i = 0; i < T::kLoads; ++i)
+      v[i] = load8<WIDE>(gr, (uint32_t)((t + lr + T::kRows * i) * L.N * 2), (int)c0 + lc, (int)L.N);
   };
   int64_t t = lo + 32 * wave;
-  if (t < hi) load(t);
+  load(t);
   for (; t < hi; t += 128) {
 #pragma unroll
     for (int i = 0; i < 2 * JT; ++i) w[i] = tc[(t / 32 * 2 * JT + i) * 64 + lane];
 #pragma unroll
     for (int i = 0; i < T::kLoads; ++i) *reinterpret_cast<u32x4*>(dst + T::kRows * i * col_pitch<CT>()) = v[i];
-    if (t + 128 < hi) load(t + 128);
+    load(t + 128);
     __builtin_amdgcn_wave_barrier();
     col_step<CT, JT>(tile, w, acc);
     __builtin_amdgcn_wave_barrier();
@@ -515,15 +508,15 @@ __device__ __forceinline__ void x_columns(const Ckpt& ck, const u32x4* __restric
   for (int i = 0; i < CT * JT; ++i) acc[i] = kZero4;
   CkptRaw v[T::kLoads];
   u32x4 w[2 * JT];
-  auto load = [&](int64_t t) {
+  const CkptRsrc kr = ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K);
+  auto load = [&](int64_t at) {
+    const int64_t t = at < hi ? at : hi - 32;
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) {
-      const int64_t m = t + lr + T::kRows * i;
-      v[i] = ckpt_load<WIDE>(ck, m, c0 + lc, L.K, m < L.M);
-    }
+    for (int i = 0; i < T::kLoads; ++i)
+      v[i] = ckpt_load8<WIDE>(kr, ckpt_row(t + lr + T::kRows * i, L.K), (int)c0 + lc, (int)L.K);
   };
   int64_t t = lo + 32 * wave;
-  if (t < hi) load(t);
+  load(t);
   for (; t < hi; t += 128) {
     u32x4 kept[T::kLoads];
 #pragma unroll
@@ -531,10 +524,11 @@ __device__ __forceinline__ void x_columns(const Ckpt& ck, const u32x4* __restric
 #pragma unroll
     for (int i = 0; i < T::kLoads; ++i) {
       u32x4 pruned;
+      if (!WIDE) v[i].q[1] = c0 + lc + 4 < L.K ? v[i].q[1] : 0u;   // past the row: the next one's
       ckpt_split(v[i], pruned, kept[i]);
       *reinterpret_cast<u32x4*>(dst + T::kRows * i * col_pitch<CT>()) = pruned;
     }
-    if (t + 128 < hi) load(t + 128);
+    load(t + 128);
     __builtin_amdgcn_wave_barrier();
     col_step<CT, JT>(tile, w, acc);                     // pruned with U
     __builtin_amdgcn_wave_barrier();
@@ -601,7 +595,7 @@ join_columns_kernel(const float* __restrict__ part, BackwardLayout L, uint16_t* 
 // wavefronts 64 channels (four of P's blocks) in turn: lane l has token l % 16,
 // channels 16 (l / 16) + [0, 16), i.e. 16 bytes of codes, one exponent, two
 // position bytes and 32 bytes of dX.
-template <int RT>                                       // rp / 32, 0 without LoRA
+template <int RT, bool SPLIT>                           // RT: rp / 32, 0 without LoRA; SPLIT: P in ranges
 __global__ void __launch_bounds__(256)
 finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckpt ck, const u32x4* __restrict__ u,
               const u32x4* __restrict__ a_up, const float* __restrict__ d_lora, BackwardLayout L, int64_t chunk,
@@ -614,8 +608,9 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
   const int64_t b0 = 2 * (blockIdx.x % groups);
   const int64_t lo = blockIdx.x / groups * chunk, hi = lo + chunk < steps ? lo + chunk : steps;
   float s[2], lk[2];
-  const int8_t* codes[2];
-  const uint8_t *exps[2], *idx[2];
+  const CkptRsrc kr = ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K);
+  const int K = (int)L.K;
+  CkptRow rows[2];
   const f32x4* pr[2];
   bool ok[2];
 #pragma unroll
@@ -625,9 +620,7 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
     const int64_t row = ok[i] ? m : L.M - 1;
     s[i] = ck.stats[2 * row];
     lk[i] = ck.stats[2 * row + 1];
-    codes[i] = ck.codes + row * L.K;
-    exps[i] = ck.exps + row * ((L.K + 31) / 32);
-    idx[i] = ck.idx + row * ((L.K + 7) / 8);
+    rows[i] = ckpt_row(row, L.K);
     pr[i] = reinterpret_cast<const f32x4*>(p) + b * steps * 256 + lane;
   }
   struct Stage {
@@ -639,13 +632,15 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) f.p[i][n] = pr[i][(4 * t + n) * 64];
-      f.x[i] = ckpt_load16(codes[i], exps[i], idx[i], 64 * t + 16 * quad, L.K);
+      f.x[i] = ckpt_load16(kr, rows[i], (int)(64 * t + 16 * quad), K);
     }
-    for (int64_t q = 1; q < L.p_splits; ++q)
+    if constexpr (SPLIT) {
+      for (int64_t q = 1; q < L.p_splits; ++q)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) f.p[i][n] += pr[i][q * slab + (4 * t + n) * 64];
+          for (int n = 0; n < 4; ++n) f.p[i][n] += pr[i][q * slab + (4 * t + n) * 64];
+    }
   };
   Stage s0, s1;
   if (lo + wave < hi) load(s0, lo + wave);
@@ -678,8 +673,10 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
     per_kept[i] = per[i] * (1.f - s[i]);
   }
 
-  auto finish = [&](const Stage& f, int64_t t) {
+  auto finish = [&](Stage& f, int64_t t) {
     uint32_t out[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ckpt_clip16(f.x[i], (int)(64 * t + 16 * quad), K);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       f32x4 v[2] = {kZero4, kZero4};
@@ -694,7 +691,7 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t b = kept_bits(f.x[i].idx >> (4 * n)), q = f.x[i].codes[n];
+        const uint32_t b = ckpt_kept16(f.x[i], n), q = f.x[i].codes[n];
         float o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -720,11 +717,19 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
       }
     }
   };
-  for (int64_t t = lo + wave; t < hi; t += 8) {
-    if (t + 4 < hi) load(s1, t + 4);
+  int64_t t = lo + wave;
+  for (; t + 8 < hi; t += 8) {
+    load(s1, t + 4);
     finish(s0, t);
-    if (t + 8 < hi) load(s0, t + 8);
-    if (t + 4 < hi) finish(s1, t + 4);
+    load(s0, t + 8);
+    finish(s1, t + 4);
+  }
+  if (t + 4 < hi) {
+    load(s1, t + 4);
+    finish(s0, t);
+    finish(s1, t + 4);
+  } else if (t < hi) {
+    finish(s0, t);
   }
 }
 
@@ -777,10 +782,11 @@ hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_
   float* d_part = reinterpret_cast<float*>(ws + L.off_d_part);
   const hipError_t e = launch_grad_gemm(g, w_t, ck, L, p, d_part, stream);
   if (e != hipSuccess) return e;
-  auto* k = L.r == 0     ? &finish_kernel<0>
-            : L.rp == 32 ? &finish_kernel<1>
-            : L.rp == 64 ? &finish_kernel<2>
-                         : &finish_kernel<4>;
+  const bool split = L.p_splits > 1;
+  auto* k = L.r == 0     ? (split ? &finish_kernel<0, true> : &finish_kernel<0, false>)
+            : L.rp == 32 ? (split ? &finish_kernel<1, true> : &finish_kernel<1, false>)
+            : L.rp == 64 ? (split ? &finish_kernel<2, true> : &finish_kernel<2, false>)
+                         : (split ? &finish_kernel<4, true> : &finish_kernel<4, false>);
   // About 4096 wavefronts (four per SIMD), each with at least one 64-channel step.
   const int64_t groups = (L.M + 31) / 32, steps = L.kp / 64;
   const int64_t chunk = 4 * ((groups * steps + 4095) / 4096);

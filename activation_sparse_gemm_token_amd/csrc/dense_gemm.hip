@@ -298,14 +298,14 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     constexpr int kGroups = kCB / 4 + (kCB % 4 != 0);
     // All of the checkpoint's loads go out first, then P's stores, so the sums
     // wait for neither.
+    const CkptRsrc ck = ckpt_rsrc(y.ck.codes, y.ck.exps, y.ck.idx, M, N);
     Ckpt16 f[kRB][kGroups];
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb) {
-      const int64_t m = 16 * (mb + rb) + col, row = m < M ? m : M - 1;
+      const CkptRow row = ckpt_row(16 * (mb + rb) + col, N);
 #pragma unroll
       for (int q = 0; q < kGroups; ++q)
-        f[rb][q] = ckpt_load16(y.ck.codes + row * N, y.ck.exps + row * ((N + 31) / 32),
-                               y.ck.idx + row * ((N + 7) / 8), 64 * ((nb >> 2) + q) + 16 * quad, N);
+        f[rb][q] = ckpt_load16(ck, row, (int)(64 * ((nb >> 2) + q) + 16 * quad), (int)N);
     }
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb)
@@ -318,7 +318,10 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     for (int rb = 0; rb < kRB; ++rb) {
       float part[kGroups];
 #pragma unroll
-      for (int q = 0; q < kGroups; ++q) part[q] = 0.f;
+      for (int q = 0; q < kGroups; ++q) {
+        part[q] = 0.f;
+        ckpt_clip16(f[rb][q], (int)(64 * ((nb >> 2) + q) + 16 * quad), (int)N);
+      }
       if (whole) {
 #pragma unroll
         for (int cb = 0; cb < kCB; ++cb) part[cb / 4] += ckpt_kept_dot(f[rb][cb / 4], cb % 4, acc[rb][cb]);

@@ -44,36 +44,53 @@ __device__ __forceinline__ u32x4 kept_masks(uint32_t byte) {
   return m;
 }
 
-// 16 channels of a token at channel k (k % 16 == 0), as the backward pass reads
-// them: one lane's share of 64.  Channels past K have code 0 and count as
-// pruned; nothing past a row is read.
+// The checkpoint through buffer resources: a load past the tensors or at
+// kOobOffset gives zeros and needs no branch, so none is ever under a condition
+// (a conditional load makes the compiler wait for every load in flight where it
+// waits for one).  All of it is below 2 GiB: 32-bit offsets.
+struct CkptRsrc {
+  __amdgpu_buffer_rsrc_t codes, exps, idx;
+};
+__device__ __forceinline__ CkptRsrc ckpt_rsrc(const int8_t* codes, const uint8_t* exps, const uint8_t* idx, int64_t M,
+                                              int64_t K) {
+  return {make_rsrc(codes, M * K), make_rsrc(exps, M * ((K + 31) / 32)), make_rsrc(idx, M * ((K + 7) / 8))};
+}
+// A token's offsets in the three; a token past M gives zeros.
+struct CkptRow {
+  uint32_t codes, exps, idx;
+};
+__device__ __forceinline__ CkptRow ckpt_row(int64_t row, int64_t K) {
+  return {(uint32_t)(row * K), (uint32_t)(row * ((K + 31) / 32)), (uint32_t)(row * ((K + 7) / 8))};
+}
+
+// 16 channels of a token at channel k (k % 16 == 0): one lane's share of 64.
+// Channels past K have code 0.
 struct Ckpt16 {
   u32x4 codes;
-  uint32_t exp, idx;                      // idx: 4 bits per group
+  uint32_t exp, idx0, idx1;               // idx: 4 bits per group, two groups each
 };
-__device__ __forceinline__ Ckpt16 ckpt_load16(const int8_t* codes, const uint8_t* exps, const uint8_t* idx,
-                                              int64_t k, int64_t K) {
-  Ckpt16 f = {{0, 0, 0, 0}, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&f.codes, __builtin_assume_aligned(codes + k, 4), 16);
-    f.exp = exps[k / 32];
-    uint16_t two;
-    __builtin_memcpy(&two, idx + k / 8, 2);
-    f.idx = two;
-  } else if (k < K) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (k + 4 * i < K) f.codes[i] = *reinterpret_cast<const uint32_t*>(codes + k + 4 * i);
-    f.exp = exps[k / 32];
-    f.idx = idx[k / 8];
-    if (k + 8 < K) f.idx |= (uint32_t)idx[k / 8 + 1] << 8;
-  }
+__device__ __forceinline__ Ckpt16 ckpt_load16(const CkptRsrc& c, const CkptRow& r, int k, int K) {
+  Ckpt16 f;
+  f.codes = buf_load16(c.codes, k < K ? r.codes + k : kOobOffset);
+  f.exp = __builtin_amdgcn_raw_buffer_load_b8(c.exps, k < K ? r.exps + k / 32 : kOobOffset, 0, 0);
+  f.idx0 = __builtin_amdgcn_raw_buffer_load_b8(c.idx, k < K ? r.idx + k / 8 : kOobOffset, 0, 0);
+  f.idx1 = __builtin_amdgcn_raw_buffer_load_b8(c.idx, k + 8 < K ? r.idx + k / 8 + 1 : kOobOffset, 0, 0);
   return f;
+}
+// What such a load brings past the end of a row is the next row's: made zeros
+// when it is used.
+__device__ __forceinline__ void ckpt_clip16(Ckpt16& f, int k, int K) {
+#pragma unroll
+  for (int i = 1; i < 4; ++i) f.codes[i] = k + 4 * i < K ? f.codes[i] : 0u;
+}
+// Kept channels of group i (0 to 3) as bits 0..3.
+__device__ __forceinline__ uint32_t ckpt_kept16(const Ckpt16& f, int i) {
+  return kept_bits((i < 2 ? f.idx0 : f.idx1) >> (4 * (i & 1)));
 }
 
 // Sum over the kept ones of group i's 4 channels of code * p.
 __device__ __forceinline__ float ckpt_kept_dot(const Ckpt16& f, int i, f32x4 p) {
-  const uint32_t b = kept_bits(f.idx >> (4 * i)), q = f.codes[i];
+  const uint32_t b = ckpt_kept16(f, i), q = f.codes[i];
   float d = (b & 1u) ? (float)((int)(q << 24) >> 24) * p[0] : 0.f;
   d += (b & 2u) ? (float)((int)(q << 16) >> 24) * p[1] : 0.f;
   d += (b & 4u) ? (float)((int)(q << 8) >> 24) * p[2] : 0.f;
