@@ -60,59 +60,47 @@ __device__ __forceinline__ void angle(int64_t pos, double inv_freq, float& s, fl
 // V elements per access.  Units of one head: rot / (2 V) pairs of V-element
 // pieces in the half layout, rot / V pieces in the interleaved one (rot / 2
 // pairs of single elements when V is 1), then the (dim - rot) / V pieces
-// that are copied.
+// that are copied.  A row is (token, head); blockIdx.y takes every gridDim.y-th
+// block of rows.  A thread keeps its unit and walks rows, kUnroll at a time; the
+// first of them are requested before the angles are formed.
 template <typename E, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads)
 rope_kernel(RopeArgs a) {
   using raw = typename E::raw;
   using P = Pack<raw, V>;
-  extern __shared__ int64_t lds[];
-  // Per token of this group: element offsets of x and y of both tensors.
-  int64_t* const base = lds;
-  float* const table = reinterpret_cast<float*>(lds + 4 * a.group);   // [token][cos pairs, sin pairs]
+  extern __shared__ float table[];                 // [token][cos pairs, sin pairs]
   const int pairs = a.rot / 2;
   const int64_t tok0 = (int64_t)blockIdx.x * a.group;
   const int ntok = (int)(a.total - tok0 < a.group ? a.total - tok0 : a.group);
-  for (int t = threadIdx.x; t < ntok; t += kThreads) {
-    const int64_t b = (tok0 + t) / a.tokens, tt = (tok0 + t) - b * a.tokens;
-    base[4 * t + 0] = b * a.t[0].xb + tt * a.t[0].xt;
-    base[4 * t + 1] = b * a.t[0].yb + tt * a.t[0].yt;
-    base[4 * t + 2] = b * a.t[1].xb + tt * a.t[1].xt;
-    base[4 * t + 3] = b * a.t[1].yb + tt * a.t[1].yt;
-  }
-  // The group's tokens are consecutive: a token's batch is the group's first
-  // one's or follows it.
-  const int64_t b0 = tok0 / a.tokens;
-  const int64_t t0 = tok0 - b0 * a.tokens;
-  for (int i = threadIdx.x; i < ntok * pairs; i += kThreads) {
-    const int t = i / pairs, p = i - t * pairs;
-    int64_t b = b0, tt = t0 + t;
+  const int64_t b0 = tok0 / a.tokens, t0 = tok0 - b0 * a.tokens;
+  // Batch and position of local token t: the group's tokens are consecutive.
+  auto place = [&](int t, int64_t& b, int64_t& tt) {
+    b = b0;
+    tt = t0 + t;
     while (tt >= a.tokens) { tt -= a.tokens; ++b; }
-    const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
-    float s, c;
-    angle(a.positions[b * a.pos_b + tt * a.pos_t + axis], a.inv_freq[p], s, c);
-    table[2 * pairs * t + p] = c * a.scale;
-    table[2 * pairs * t + pairs + p] = (a.inverse ? -s : s) * a.scale;
-  }
-  __syncthreads();
+  };
 
   constexpr int kPer = INTER ? (V == 1 ? 2 : V) : 2 * V;     // rotated elements per unit
   const int rot_units = a.rot / kPer;
   const int units = rot_units + (a.dim - a.rot) / V;
   const int heads = a.t[0].heads + a.t[1].heads;
-  // blockIdx.y takes every gridDim.y-th block of rows: a row is (token, head).
   const int lanes = units < kThreads ? units : kThreads;     // threads along a head
   const int rows_at_once = kThreads / lanes;
   const int sub = threadIdx.x / lanes;
-  if (sub >= rows_at_once) return;
-  const int rows = ntok * heads;
   const int step = rows_at_once * (int)gridDim.y;
   const int first = sub * (int)gridDim.y + (int)blockIdx.y;
   const int step_t = step / heads, step_h = step - step_t * heads;
-  for (int u = threadIdx.x - sub * lanes; u < units; u += lanes) {
-    const bool turn = u < rot_units;
-    // Element offsets of the unit's first and second piece in its head.
-    int o0, o1;
+  const int first_t = first / heads, first_h = first - first_t * heads;
+
+  // A batch of rows of unit u: what was read, where it goes, its token's table.
+  P x0[kUnroll], x1[kUnroll];
+  raw* dst[kUnroll];
+  int tk[kUnroll];
+  int u = threadIdx.x - sub * lanes, t = first_t, h = first_h;
+  bool turn = false, two = false;
+  int o0 = 0, o1 = 0;                              // element offsets of the unit's pieces in its head
+  auto unit = [&]() {
+    turn = u < rot_units;
     if (turn) {
       o0 = INTER ? (V == 1 ? 2 * u : V * u) : V * u;
       o1 = INTER ? o0 + 1 : o0 + pairs;
@@ -120,65 +108,92 @@ rope_kernel(RopeArgs a) {
       o0 = a.rot + (u - rot_units) * V;
       o1 = o0;
     }
-    const bool two = turn && (!INTER || V == 1);
-    int t = first / heads, h = first - t * heads;
-    for (int row0 = first; row0 < rows; row0 += step * kUnroll) {
-      P x0[kUnroll], x1[kUnroll];
-      raw* dst[kUnroll];
-      int tk[kUnroll];
+    two = turn && (!INTER || V == 1);
+  };
+  auto load = [&]() {
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        dst[j] = nullptr;
-        if (t < ntok) {
-          const int w = h >= a.t[0].heads;
-          const RopeSide& z = a.t[w];
-          if (turn || !z.in_place) {
-            const int64_t hh = h - (w ? a.t[0].heads : 0);
-            const raw* src = static_cast<const raw*>(z.x) + base[4 * t + 2 * w] + hh * z.xh;
-            dst[j] = static_cast<raw*>(z.y) + base[4 * t + 2 * w + 1] + hh * z.yh;
-            tk[j] = t;
-            x0[j] = *reinterpret_cast<const P*>(src + o0);
-            if (two) x1[j] = *reinterpret_cast<const P*>(src + o1);
-          }
+    for (int j = 0; j < kUnroll; ++j) {
+      dst[j] = nullptr;
+      if (t < ntok) {
+        const int w = h >= a.t[0].heads;
+        const RopeSide& z = a.t[w];
+        if (turn || !z.in_place) {
+          const int64_t hh = h - (w ? a.t[0].heads : 0);
+          int64_t b, tt;
+          place(t, b, tt);
+          const raw* src = static_cast<const raw*>(z.x) + b * z.xb + tt * z.xt + hh * z.xh;
+          dst[j] = static_cast<raw*>(z.y) + b * z.yb + tt * z.yt + hh * z.yh;
+          tk[j] = t;
+          x0[j] = *reinterpret_cast<const P*>(src + o0);
+          if (two) x1[j] = *reinterpret_cast<const P*>(src + o1);
         }
-        t += step_t;
-        h += step_h;
-        if (h >= heads) { h -= heads; ++t; }
       }
+      t += step_t;
+      h += step_h;
+      if (h >= heads) { h -= heads; ++t; }
+    }
+  };
+  const bool active = sub < rows_at_once && u < units;
+  if (active) {
+    unit();
+    load();
+  }
+
+  for (int i = threadIdx.x; i < ntok * pairs; i += kThreads) {
+    const int n = i / pairs, p = i - n * pairs;
+    int64_t b, tt;
+    place(n, b, tt);
+    const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
+    float s, c;
+    angle(a.positions[b * a.pos_b + tt * a.pos_t + axis], a.inv_freq[p], s, c);
+    table[2 * pairs * n + p] = c * a.scale;
+    table[2 * pairs * n + pairs + p] = (a.inverse ? -s : s) * a.scale;
+  }
+  __syncthreads();
+  if (!active) return;
+
+  for (;;) {
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        if (dst[j] == nullptr) continue;
-        if (!turn) {
-          *reinterpret_cast<P*>(dst[j] + o0) = x0[j];
-          continue;
+    for (int j = 0; j < kUnroll; ++j) {
+      if (dst[j] == nullptr) continue;
+      if (!turn) {
+        *reinterpret_cast<P*>(dst[j] + o0) = x0[j];
+        continue;
+      }
+      const float* tc = table + 2 * pairs * tk[j];
+      if constexpr (INTER && V > 1) {
+        const float* c = tc + (V / 2) * u;
+        P y;
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          const float p = E::up(x0[j].v[2 * e]), q = E::up(x0[j].v[2 * e + 1]);
+          const float cc = c[e], ss = c[pairs + e];
+          y.v[2 * e] = E::down(p * cc - q * ss);
+          y.v[2 * e + 1] = E::down(q * cc + p * ss);
         }
-        const float* tc = table + 2 * pairs * tk[j];
-        if constexpr (INTER && V > 1) {
-          const float* c = tc + (V / 2) * u;
-          P y;
+        *reinterpret_cast<P*>(dst[j] + o0) = y;
+      } else {
+        const float* c = tc + V * u;
+        P y0, y1;
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            const float p = E::up(x0[j].v[2 * e]), q = E::up(x0[j].v[2 * e + 1]);
-            const float cc = c[e], ss = c[pairs + e];
-            y.v[2 * e] = E::down(p * cc - q * ss);
-            y.v[2 * e + 1] = E::down(q * cc + p * ss);
-          }
-          *reinterpret_cast<P*>(dst[j] + o0) = y;
-        } else {
-          const float* c = tc + V * u;
-          P y0, y1;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float p = E::up(x0[j].v[e]), q = E::up(x1[j].v[e]);
-            const float cc = c[e], ss = c[pairs + e];
-            y0.v[e] = E::down(p * cc - q * ss);
-            y1.v[e] = E::down(q * cc + p * ss);
-          }
-          *reinterpret_cast<P*>(dst[j] + o0) = y0;
-          *reinterpret_cast<P*>(dst[j] + o1) = y1;
+        for (int e = 0; e < V; ++e) {
+          const float p = E::up(x0[j].v[e]), q = E::up(x1[j].v[e]);
+          const float cc = c[e], ss = c[pairs + e];
+          y0.v[e] = E::down(p * cc - q * ss);
+          y1.v[e] = E::down(q * cc + p * ss);
         }
+        *reinterpret_cast<P*>(dst[j] + o0) = y0;
+        *reinterpret_cast<P*>(dst[j] + o1) = y1;
       }
     }
+    if (t >= ntok) {                               // this unit's rows are done
+      u += lanes;
+      if (u >= units) return;
+      unit();
+      t = first_t;
+      h = first_h;
+    }
+    load();
   }
 }
 
@@ -229,7 +244,7 @@ hipError_t launch_rope(RopeArgs a, int elem_bytes, bool fp16, bool inter, int co
   }
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks, (unsigned)split);
-  const size_t lds = (size_t)group * (4 * sizeof(int64_t) + 2 * pairs * sizeof(float));
+  const size_t lds = (size_t)group * 2 * pairs * sizeof(float);
   if (elem_bytes == 4) {
     if (vec >= 4) return launch_v<Fp32, 4>(a, inter, grid, lds, stream);
     if (vec >= 2) return launch_v<Fp32, 2>(a, inter, grid, lds, stream);
