@@ -73,7 +73,15 @@ class Checkpoint:
 
     def unpack(self, out=None):
         """The stored values [*lead, k] in bf16 (exact)."""
-        return unpack(self.codes, self.exps, out=out).view(*self.lead, self.k)
+        codes = self.codes
+        if out is not None:
+            return unpack(codes, self.exps, out=out).view(*self.lead, self.k)
+        y = codes.new_empty((*self.lead, self.k), dtype=_torch().bfloat16)
+        with _on(codes.device):
+            st = _fn("rtl_checkpoint_unpack")(codes.data_ptr(), self.exps.data_ptr(), self.m, self.k, y.data_ptr(),
+                                              _stream())
+        _check(st, "rtl_checkpoint_unpack")
+        return y
 
 
 def checkpoint(x) -> Checkpoint:

@@ -211,3 +211,46 @@ def test_offsets_past_32_bits():
     check(rotary.rope(x, pos, f), want, pos, f)
     rotary.rope(x, pos, f, out=x)
     check(x, want, pos, f)
+
+
+def test_outputs_that_overlap_are_refused():
+    f, pos = freq(16), torch.arange(4, device=DEV)
+    x, k = make((4, 3, 16), torch.bfloat16, 18), make((4, 3, 16), torch.bfloat16, 19)
+    fused = make((4, 8, 16), torch.bfloat16, 21)
+    for kw in (dict(k=k, out=k), dict(k=x, out=x, k_out=x), dict(k=k, out=torch.empty_like(x), k_out=x),
+               dict(out=torch.empty(4, 1, 16, dtype=x.dtype, device=DEV).expand(4, 3, 16))):
+        with pytest.raises(ValueError):
+            rotary.rope(x, pos, f, **kw)
+    with pytest.raises(ValueError):
+        rotary.rope(fused[:, :4], pos, f, k=fused[:, 3:5], out=fused[:, :4], k_out=fused[:, 3:5])
+    with pytest.raises(ValueError):
+        rotary.rope(fused[:, :4], pos, f, out=fused[:, 2:6])
+    with pytest.raises(ValueError):
+        rotary.rope(x, pos.cpu(), f)
+    with pytest.raises(TypeError):
+        rotary.rope(x, pos.int(), f)
+    with pytest.raises(TypeError):
+        rotary.rope(x, pos, f.float())
+    # next to each other is fine
+    want = rotary.rope(fused[:, :4].clone(), pos, f)
+    got = rotary.rope(fused[:, :4], pos, f, out=fused[:, 4:])
+    assert torch.equal(got, want)
+
+
+def test_seeded_sweep():
+    rng = np.random.default_rng(22)
+    for i in range(30):
+        d = int(rng.integers(1, 300))
+        rot = 2 * int(rng.integers(0, d // 2 + 1))
+        b, t, h, hk = int(rng.integers(1, 4)), int(rng.integers(1, 200)), int(rng.integers(1, 20)), int(rng.integers(1, 6))
+        dtype, layout = DTYPES[int(rng.integers(3))], rotary.LAYOUTS[int(rng.integers(2))]
+        pad = int(rng.integers(0, 9))
+        say("sweep", i, b, t, h, hk, d, rot, dtype, layout, pad)
+        x = make((b, t, h, d + pad), dtype, 50 + i)[..., :d]
+        k = make((b, t, hk + 2, d), dtype, 90 + i)[:, :, 1:1 + hk]
+        pos = torch.randint(-1000, 100000, (b, t), generator=torch.Generator().manual_seed(i)).to(DEV)
+        f = freq(rot, linear=2.0, ntk=3.0)
+        inverse = bool(rng.integers(2))
+        y, ky = (rotary.rope_backward if inverse else rotary.rope)(x, pos, f, k=k, layout=layout, scale=0.7)
+        check(y, x, pos, f, layout, None, 0.7, inverse)
+        check(ky, k, pos, f, layout, None, 0.7, inverse)

@@ -317,3 +317,53 @@ def test_forward_and_backward_meet():
     kept = training.checkpoint(x)
     _, _, s_ref, _, _ = oracle.sparsify(bits)
     assert np.allclose(kept.stats[:, 0].cpu().numpy(), s_ref, rtol=1e-5, atol=0)
+
+
+def test_seeded_sweep():
+    rng = np.random.default_rng(8)
+    for i in range(16):
+        m, n, k = int(2 ** rng.uniform(0, 9.5)), 4 * int(2 ** rng.uniform(0, 8.5)), 4 * int(2 ** rng.uniform(0, 8.5))
+        r, alpha = int(rng.integers(0, 129)), float(rng.uniform(-2, 2))
+        say("sweep", i, m, n, k, r, alpha)
+        t = layer(m, n, k, r, seed=100 * i, law=["mixture", "gelu", "ties"][i % 3])
+        ws = torch.full((training.backward_workspace_bytes(m, n, k, r),), 0xff, dtype=torch.uint8, device=DEV)
+        check(run(t, alpha, workspace=ws), *reference(t, alpha))
+
+
+def test_a_gradient_row_that_is_not_finite_stays_alone():
+    t = layer(70, 136, 260, 16)
+    want = run(t)[0]
+    t["g"][33, 5] = float("nan")
+    dx = run(t)[0]
+    rows = [i for i in range(70) if i != 33]
+    assert torch.equal(dx[rows], want[rows]) and torch.isnan(dx[33].float()).all()
+
+
+def test_large_tiles_and_ranges():
+    """More than one round of tiles (256 columns), and a long contraction in
+    many ranges; sampled rows against fp64."""
+    for m, n, k, r in ((4100, 192, 4100, 16), (40, 12000, 200, 8), (1030, 320, 9000, 64)):
+        say("large", m, n, k, r)
+        t = layer(m, n, k, r)
+        got = run(t, 0.5)
+        rows = torch.tensor(sorted({0, 1, 255, 256, m // 2, m - 1} & set(range(m))), device=DEV)
+        kept = t["kept"]
+        part = dict(t, g=t["g"][rows], kept=training.Checkpoint(kept.codes[rows].contiguous(), kept.exps[rows].contiguous(),
+                                                                kept.idx[rows].contiguous(), kept.stats[rows].contiguous()))
+        ref, tol = reference(part, 0.5)
+        d = np.abs(plain.bf16(got[0][rows]) - ref[0])
+        assert (d <= tol[0]).all()
+        # sums over all tokens: in fp64 on the device
+        x = kept.unpack().double()
+        mk = torch.from_numpy(plain.mask(kept.idx.cpu().numpy(), k)).to(DEV)
+        s = kept.stats[:, :1].double()
+        rest = x * (1 - s * mk)
+        g, a, b = t["g"].double(), t["a"].double(), t["b"].double()
+        u, tt = 0.5 * g @ b, 0.5 * rest @ a.t().contiguous()
+        for got_i, want, size, lost in ((got[1], u.t().contiguous() @ rest, u.abs().t().contiguous() @ rest.abs(),
+                                         plain.depth(n) * plain.U24 * (0.5 * g.abs() @ b.abs()).t().contiguous() @ rest.abs()),
+                                        (got[2], g.t().contiguous() @ tt, g.abs().t().contiguous() @ tt.abs(),
+                                         g.abs().t().contiguous() @ (plain.depth(k) * plain.U24 * 0.5 *
+                                                                     (rest.abs() @ a.abs().t().contiguous())))):
+            tol_i = plain.HALF_BF16 * want.abs() + (plain.depth(m) * plain.U24 + plain.U16 + 4 * plain.U24) * size + lost
+            assert ((got_i.double() - want).abs() <= tol_i).all()

@@ -201,3 +201,23 @@ def test_refusals():
     with pytest.raises(rtl.RtlError) as e:
         w4.linear(x, w4.Weight(weight.packed[:-16], 32, 256, 64, True))
     assert e.value.status == 4
+
+
+def test_seeded_sweep():
+    rng = np.random.default_rng(3)
+    for i in range(30):
+        group = int(rng.choice(w4.GROUPS))
+        m = int(2 ** rng.uniform(0, 8))
+        k = group * int(rng.integers(1, max(2, 3000 // group)))
+        n = int(2 ** rng.uniform(0, 13.3))
+        zeros = bool(rng.integers(2))
+        say("sweep", i, m, k, n, group, zeros)
+        t = make(m, k, n, group, zeros, seed=i)
+        check(run(*t, group), *plain(*t, group))
+
+
+def test_many_rows_reread_the_weight():
+    """More rows than one pass over the weight serves, and more tiles of rows
+    than a chip has units."""
+    t = make(3000, 256, 72, 64, True)
+    check(run(*t, 64), *plain(*t, 64))
