@@ -338,10 +338,11 @@ join_rows_kernel(const float* __restrict__ part, const float* __restrict__ stats
     float keep = 0.f;
     if (m < L.M) {
       const float* p = part + m * RP + j;
-#pragma unroll 4
+      // Few tokens have many ranges: their loads go out 16 at a time.
+#pragma unroll 16
       for (int64_t q = 0; q < L.splits_g; ++q) u += *reinterpret_cast<const f32x4*>(p + q * slab);
       p += L.splits_g * slab;
-#pragma unroll 2
+#pragma unroll 8
       for (int64_t q = 0; q < L.splits_x; ++q) {
         pr += *reinterpret_cast<const f32x4*>(p + 2 * q * slab);
         ke += *reinterpret_cast<const f32x4*>(p + (2 * q + 1) * slab);

@@ -56,7 +56,7 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   for (int64_t tn : {256, 192}) {
     if (tn == 192 && N % 8 != 0) continue;
     const int64_t tiles = (K + tn - 1) / tn;
-    for (int64_t s = 1; s <= 16 && (s == 1 || steps / s >= 4); ++s) {
+    for (int64_t s = 1; s <= 16 && (s == 1 || steps / s >= 2); ++s) {
       const int64_t rounds = (tiles_m * tiles * s + kCus - 1) / kCus, per = (steps + s - 1) / s;
       if (s > 1 && (s - 1) * per >= steps) continue;                    // the last range would be empty
       const double t = (double)rounds * ((double)per * (tn == 256 ? 1.65 : 1.25) + 8) +
