@@ -139,8 +139,8 @@ struct GradOut {
 // KM: how channel tails are handled.  TN: tile columns, 256 or 192.  TILED: fp32
 // result in 16 x 16 blocks [M / 16][4 (N / 64)][lane][4] instead of a bf16
 // row-major one.  256 columns: 2 x 4 wavefronts of 128 x 64; 192: 4 x 2 of
-// 64 x 96, which read 160 rows of operands from LDS per step instead of the
-// 176 of 2 x 4.
+// 64 x 96 (160 rows of operands read from LDS per step instead of the 176 of
+// 2 x 4; measured alike).
 template <int KM, int TN, bool TILED>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
