@@ -134,6 +134,18 @@ def _stream():
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _here(t, *others):
+    """The current stream if t and the others (None left out) are all on the
+    current device, else None: the caller then goes through ``_on``, which
+    makes that device current or raises."""
+    c = _torch()._C
+    device = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != device:
+            return None
+    return c._cuda_getCurrentRawStream(device) if c._cuda_getDevice() == device else None
+
+
 _HERE_CONTEXT = contextlib.nullcontext()                # the device is current already
 
 

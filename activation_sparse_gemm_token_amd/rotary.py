@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from . import _check, _on, _stream, _torch, lib
+from . import _check, _here, _on, _stream, _torch, lib
 
 __all__ = ["rope", "rope_backward", "frequencies", "frequencies_by_parts", "LAYOUTS"]
 
@@ -181,7 +181,7 @@ def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, invers
         if dim > 1 and st[-1] != 1:
             raise ValueError(f"{name}: the channel stride must be 1")
         if o is None:
-            o = t.new_empty(ts)
+            o = torch.empty_like(t, memory_format=torch.contiguous_format)
         else:
             _check_out(name, t, o)
         so = o.stride()
@@ -216,9 +216,14 @@ def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, invers
     if axes > 1 and pos[-1] != 1:
         raise ValueError("positions: the axis stride must be 1")
     batch, tokens = lead if batched else (1, lead[0])
-    with _on(x.device, k=k, positions=positions, inv_freq=inv_freq):
-        st = _fn()((ctypes.c_int64 * len(words))(*words), len(ins), batch, tokens, dim, rot, positions.data_ptr(),
-                   pos_b, pos_t, axes, pairs, inv_freq.data_ptr(), float(scale), flags, _stream())
+    args = ((ctypes.c_int64 * len(words))(*words), len(ins), batch, tokens, dim, rot, positions.data_ptr(), pos_b, pos_t,
+            axes, pairs, inv_freq.data_ptr(), float(scale), flags)
+    stream = _here(x, k, positions, inv_freq)
+    if stream is None:
+        with _on(x.device, k=k, positions=positions, inv_freq=inv_freq):
+            st = _fn()(*args, _stream())
+    else:
+        st = _fn()(*args, stream)
     _check(st, "rtl_rope")
     return outs[0] if k is None else tuple(outs)
 

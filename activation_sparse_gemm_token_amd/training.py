@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _as_2d, _check, _on, _out, _stream, _torch, _workspace, lib
+from . import _as_2d, _check, _here, _on, _out, _stream, _torch, _workspace, lib
 
 __all__ = ["Checkpoint", "checkpoint", "unpack", "sparse_linear_backward", "backward_workspace_bytes"]
 
@@ -30,6 +30,18 @@ def _fn(name):
     if fn.argtypes is None:
         fn.restype, fn.argtypes = _SIGNATURES[name]
     return fn
+
+
+def _run(name, args, t, **tensors):
+    """Entry point ``name`` on t's device, which the named tensors share, and
+    its current stream."""
+    stream = _here(t, *tensors.values())
+    if stream is None:
+        with _on(t.device, **tensors):
+            st = _fn(name)(*args, _stream())
+    else:
+        st = _fn(name)(*args, stream)
+    _check(st, name)
 
 
 class Checkpoint:
@@ -77,10 +89,7 @@ class Checkpoint:
         if out is not None:
             return unpack(codes, self.exps, out=out).view(*self.lead, self.k)
         y = codes.new_empty((*self.lead, self.k), dtype=_torch().bfloat16)
-        with _on(codes.device):
-            st = _fn("rtl_checkpoint_unpack")(codes.data_ptr(), self.exps.data_ptr(), self.m, self.k, y.data_ptr(),
-                                              _stream())
-        _check(st, "rtl_checkpoint_unpack")
+        _run("rtl_checkpoint_unpack", (codes.data_ptr(), self.exps.data_ptr(), self.m, self.k, y.data_ptr()), codes)
         return y
 
 
@@ -93,10 +102,8 @@ def checkpoint(x) -> Checkpoint:
     exps = x2.new_empty((m, (k + 31) // 32), dtype=torch.uint8)
     idx = x2.new_empty((m, (k + 7) // 8), dtype=torch.uint8)
     stats = x2.new_empty((m, 2), dtype=torch.float32)
-    with _on(x2.device):
-        st = _fn("rtl_checkpoint_pack")(x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), idx.data_ptr(),
-                                        stats.data_ptr(), _stream())
-    _check(st, "rtl_checkpoint_pack")
+    _run("rtl_checkpoint_pack", (x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), idx.data_ptr(),
+                                 stats.data_ptr()), x2)
     return Checkpoint._made(codes, exps, idx, stats, x.shape[:-1])
 
 
@@ -111,9 +118,7 @@ def unpack(codes, exps, out=None):
         raise ValueError("codes and exps must be contiguous device tensors")
     m, k = codes.shape
     y = _out(out, m, k, (m,), codes.device)
-    with _on(codes.device, exps=exps):
-        st = _fn("rtl_checkpoint_unpack")(codes.data_ptr(), exps.data_ptr(), m, k, y.data_ptr(), _stream())
-    _check(st, "rtl_checkpoint_unpack")
+    _run("rtl_checkpoint_unpack", (codes.data_ptr(), exps.data_ptr(), m, k, y.data_ptr()), codes, exps=exps)
     return y
 
 
@@ -156,10 +161,9 @@ def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, l
     db = g2.new_empty((n, r)) if lora else None
     workspace = _workspace(workspace, backward_workspace_bytes(m, n, k, r), dev)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    with _on(dev, kept=kept.codes, w_t=w_t, lora_a=lora_a, lora_b=lora_b):
-        st = _fn("rtl_sparse_linear_backward")(
-            g2.data_ptr(), kept.codes.data_ptr(), kept.exps.data_ptr(), kept.idx.data_ptr(), kept.stats.data_ptr(),
-            ptr(w_t), ptr(lora_a) if r else None, ptr(lora_b) if r else None, m, n, k, r, float(lora_scale), ptr(dx),
-            ptr(da), ptr(db), workspace.data_ptr(), workspace.numel(), _stream())
-    _check(st, "rtl_sparse_linear_backward")
+    _run("rtl_sparse_linear_backward",
+         (g2.data_ptr(), kept.codes.data_ptr(), kept.exps.data_ptr(), kept.idx.data_ptr(), kept.stats.data_ptr(),
+          ptr(w_t), ptr(lora_a) if r else None, ptr(lora_b) if r else None, m, n, k, r, float(lora_scale), ptr(dx),
+          ptr(da), ptr(db), workspace.data_ptr(), workspace.numel()),
+         g2, kept=kept.codes, w_t=w_t, lora_a=lora_a, lora_b=lora_b)
     return dx, da, db

@@ -6,7 +6,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _as_2d, _check, _on, _out, _stream, _torch, lib
+from . import _as_2d, _check, _here, _on, _out, _stream, _torch, lib
 
 __all__ = ["Weight", "pack", "linear", "packed_bytes", "GROUPS", "MAX_ROWS"]
 
@@ -78,8 +78,14 @@ def linear(x, weight: Weight, out=None):
     if k != weight.k:
         raise ValueError(f"the weight has {weight.k} input channels, x has {k}")
     y = x2.new_empty((*x.shape[:-1], weight.n)) if out is None else _out(out, m, weight.n, x.shape[:-1], x2.device)
-    with _on(x2.device, weight=weight.packed):
-        st = _fn("rtl_w4_linear")(x2.data_ptr(), weight.packed.data_ptr(), weight.packed.numel(), m, weight.n, k,
-                                  weight.group, _ZEROS if weight.zeros else 0, y.data_ptr(), _stream())
+    packed = weight.packed
+    args = (x2.data_ptr(), packed.data_ptr(), packed.numel(), m, weight.n, k, weight.group,
+            _ZEROS if weight.zeros else 0, y.data_ptr())
+    stream = _here(x2, packed)
+    if stream is None:
+        with _on(x2.device, weight=packed):
+            st = _fn("rtl_w4_linear")(*args, _stream())
+    else:
+        st = _fn("rtl_w4_linear")(*args, stream)
     _check(st, "rtl_w4_linear")
     return y if out is None else y.view(*x.shape[:-1], weight.n)
