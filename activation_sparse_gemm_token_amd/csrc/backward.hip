@@ -27,7 +27,7 @@
 // A kept value's residual (1 - s) x is not a bf16 number; multiplying U (or the
 // joined sum) by 1 - s instead keeps the checkpoint's values exact operands.
 //
-// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 41, join 8, columns 38, join
+// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 38, join 7, columns 38, join
 // 8, G W 250 to 280 as the clock drops, dX 27.  Rows and columns read G (100 MB)
 // and the checkpoint (14 MB), 22 us at the card's copy rate.
 //

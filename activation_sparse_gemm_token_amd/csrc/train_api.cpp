@@ -24,9 +24,11 @@ bool back_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
 
 // Splits by sizes alone (a workspace must fit whatever device it is used on).
 // Two workgroups of these kernels fit a CU, so the split sizes aim at all of
-// them running at once: 384 workgroups over G's channels (and, short ones, 512
-// over the checkpoint's), 512 over tokens; a range is a whole number of steps of
-// the workgroup's four wavefronts.
+// them running at once: 256 over G's channels and 256 over the checkpoint's, in
+// one launch, and 512 over tokens; a range is a whole number of steps of the
+// workgroup's four wavefronts.  (4096 x 3072 x 12288 and 4096 x 12288 x 3072,
+// r = 64: 38 and 47 us; 384 and 512 workgroups took 41 and 51, 512 and 512 the
+// same, 256 and 192 44 and 73.)
 rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_t r) {
   constexpr int64_t kCus = 256;
   BackwardLayout L{};
@@ -41,12 +43,15 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
     return length > 0 ? round_up((length + splits - 1) / splits, step) : step;
   };
   const int64_t rows_g = L.rp == 128 ? 32 : 64, rows_x = rows_g / 2;    // tokens per workgroup
-  L.chunk_g = chunk(L.np, 3 * kCus / 2, (M + rows_g - 1) / rows_g, 256);
+  L.chunk_g = chunk(L.np, kCus, (M + rows_g - 1) / rows_g, 256);
   L.splits_g = (L.np + L.chunk_g - 1) / L.chunk_g;
-  L.chunk_x = chunk(L.kp, 2 * kCus, (M + rows_x - 1) / rows_x, 256);
+  L.chunk_x = chunk(L.kp, kCus, (M + rows_x - 1) / rows_x, 256);
   L.splits_x = (L.kp + L.chunk_x - 1) / L.chunk_x;
   const int64_t cols_g = L.rp == 128 ? 64 : 128, cols_x = cols_g / 2;   // channels per workgroup
-  L.chunk_t = chunk(L.mp, 2 * kCus, (N + cols_g - 1) / cols_g + (K + cols_x - 1) / cols_x, 128);
+  // Tiles of 64 channels (ranks above 64) are more uneven a load per CU than those
+  // of 128, and gain from more and shorter ranges: 864 workgroups instead of 288
+  // took 63 us instead of 83 (r = 128); at r = 64 512 were best.
+  L.chunk_t = chunk(L.mp, L.rp == 128 ? 7 * kCus / 2 : 2 * kCus, (N + cols_g - 1) / cols_g + (K + cols_x - 1) / cols_x, 128);
   L.splits_t = (L.mp + L.chunk_t - 1) / L.chunk_t;
   // G W: tile columns and contraction ranges by the time they should take, in
   // us: a k-step of 64 measured 1.65 (256 columns) and 1.25 (192) with the chip
