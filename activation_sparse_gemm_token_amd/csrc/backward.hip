@@ -17,7 +17,8 @@
 //                           the tokens.  Both operands run along tokens, which are
 //                           rows in memory: the tile goes through LDS and is read
 //                           transposed (ds_read_b64_tr_b16).
-//   5. join_columns_kernel  sums the token ranges in order into dA and dB.
+//   5. join_columns         sums the token ranges in order into dA and dB (a kernel
+//                           of its own where dX is not asked for, else part of 7).
 //   6. the dense GEMM       P = G W, in 16 x 16 blocks of fp32, and of each tile
 //                           its share of D.
 //   7. finish_kernel        D per token, then dX; U A is formed again, a 16-token
@@ -27,9 +28,10 @@
 // A kept value's residual (1 - s) x is not a bf16 number; multiplying U (or the
 // joined sum) by 1 - s instead keeps the checkpoint's values exact operands.
 //
-// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 38, join 7, columns 38, join
-// 8, G W 250 to 280 as the clock drops, dX 27.  Rows and columns read G (100 MB)
-// and the checkpoint (14 MB), 22 us at the card's copy rate.
+// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 38, join 7, columns 38, G W
+// 250 to 280 as the clock drops, dX with the sums of dA and dB 30 (27 and, in a
+// launch of their own, 7.6).  Rows and columns read G (100 MB) and the checkpoint
+// (14 MB), 22 us at the card's copy rate.
 //
 // Fragments instead of transposed matrices: a matrix whose rows are N channels
 // apart puts the 16 rows of an operand load on one memory channel; as 1 KiB
@@ -574,38 +576,58 @@ columns_kernel(const uint16_t* __restrict__ g, Ckpt ck, const u32x4* __restrict_
 }
 
 // --- 5. dA and dB -------------------------------------------------------------
-__global__ void __launch_bounds__(256)
-join_columns_kernel(const float* __restrict__ part, BackwardLayout L, uint16_t* __restrict__ da,
-                    uint16_t* __restrict__ db) {
-  const int64_t nb = L.N * L.r, na = L.r * L.K;
-  const float* pa = part + L.splits_t * L.N * L.rp;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nb + na; i += (int64_t)gridDim.x * 256) {
-    float v = 0.f;
-    if (i < nb) {
-      const int64_t n = i / L.r, j = i - n * L.r;
+// The token ranges' sums, four elements of the padded products at a time, from
+// item i on.
+struct Factors {
+  const float* part;
+  uint16_t *da, *db;                                    // null: not asked for
+};
+__host__ __device__ inline int64_t join_items(const BackwardLayout& L) { return (L.N * L.rp + L.r * L.kp) / 4; }
+
+__device__ __forceinline__ void join_columns(const Factors& f, const BackwardLayout& L, int64_t i, int64_t stride) {
+  const int64_t nb = L.N * L.rp, slab_a = L.rp * L.kp, all = join_items(L);
+  for (; i < all; i += stride) {
+    const bool b = 4 * i < nb;
+    const int64_t at = b ? 4 * i : 4 * i - nb, slab = b ? nb : slab_a;
+    const float* p = f.part + (b ? 0 : L.splits_t * nb) + at;
+    f32x4 v = kZero4;
 #pragma unroll 4
-      for (int64_t s = 0; s < L.splits_t; ++s) v += part[(s * L.N + n) * L.rp + j];
-      db[i] = (uint16_t)f32_to_bf16_rne(v);
+    for (int64_t s = 0; s < L.splits_t; ++s) v += *reinterpret_cast<const f32x4*>(p + s * slab);
+    const u32x2 o = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+    const int64_t row = at / (b ? L.rp : L.kp), c = at - row * (b ? L.rp : L.kp), len = b ? L.r : L.K;
+    uint16_t* y = (b ? f.db : f.da) + row * len + c;
+    if (len % 4 == 0) {                                 // K always is
+      if (c < len) *reinterpret_cast<u32x2*>(y) = o;
     } else {
-      const int64_t q = i - nb, j = q / L.K, k = q - j * L.K;
-#pragma unroll 4
-      for (int64_t s = 0; s < L.splits_t; ++s) v += pa[(s * L.rp + j) * L.kp + k];
-      da[q] = (uint16_t)f32_to_bf16_rne(v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < len) y[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
     }
   }
+}
+
+__global__ void __launch_bounds__(256) join_columns_kernel(Factors f, BackwardLayout L) {
+  join_columns(f, L, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // --- 7. dX -----------------------------------------------------------------------
 // 32 tokens (two of P's block rows) and a range of channels per workgroup, its 4
 // wavefronts 64 channels (four of P's blocks) in turn: lane l has token l % 16,
 // channels 16 (l / 16) + [0, 16), i.e. 16 bytes of codes, one exponent, two
-// position bytes and 32 bytes of dX.
+// position bytes and 32 bytes of dX.  Workgroups past `blocks` sum dA and dB, which
+// saves a launch where both are asked for.
 template <int RT, bool SPLIT>                           // RT: rp / 32, 0 without LoRA; SPLIT: P in ranges
 __global__ void __launch_bounds__(256)
 finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckpt ck, const u32x4* __restrict__ u,
               const u32x4* __restrict__ a_up, const float* __restrict__ d_lora, BackwardLayout L, int64_t chunk,
-              uint16_t* __restrict__ dx) {
+              uint16_t* __restrict__ dx, int64_t blocks, Factors factors) {
   __shared__ float red[256];
+  if constexpr (RT > 0) {
+    if (blockIdx.x >= blocks) {
+      join_columns(factors, L, (blockIdx.x - blocks) * 256 + threadIdx.x, (gridDim.x - blocks) * 256);
+      return;
+    }
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int64_t steps = L.kp / 64, rows16 = (L.M + 15) / 16, slab = rows16 * steps * 256;
@@ -738,15 +760,20 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
   }
 }
 
+// Workgroups of 256 over this many items, at most 4096 of them.
+inline int64_t blocks_of(int64_t items) {
+  const int64_t b = (items + 255) / 256;
+  return b < 4096 ? b : 4096;
+}
+
 template <int JT>
 hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a, const uint16_t* lora_b,
-                       const BackwardLayout& L, float alpha, uint16_t* da, uint16_t* db, char* ws, hipStream_t stream) {
+                       const BackwardLayout& L, float alpha, bool factors, char* ws, hipStream_t stream) {
   constexpr int kCT = JT == 8 ? 4 : 8, kG = JT == 8 ? 2 : 4, kX = kG / 2;
   auto frag = [&](size_t off) { return reinterpret_cast<u32x4*>(ws + off); };
   float* d_lora = reinterpret_cast<float*>(ws + L.off_d);
   float* part = reinterpret_cast<float*>(ws + L.off_part);
-  auto blocks = [](int64_t items) { const int64_t b = (items + 255) / 256; return dim3((unsigned)(b < 4096 ? b : 4096)); };
-  hipError_t e = launch(&factors_kernel, blocks(L.rp * (2 * L.kp + L.np) / 8), dim3(256), stream, lora_a, lora_b, L,
+  hipError_t e = launch(&factors_kernel, dim3((unsigned)blocks_of(L.rp * (2 * L.kp + L.np) / 8)), dim3(256), stream, lora_a, lora_b, L,
                         frag(L.off_a_down), frag(L.off_a_up), frag(L.off_b));
   if (e != hipSuccess) return e;
   const bool wg = L.N % 8 == 0, wx = L.K % 8 == 0;
@@ -756,14 +783,12 @@ hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a
   if (e != hipSuccess) return e;
   e = launch(&join_rows_kernel<16 * JT>, dim3((unsigned)(L.mp / 32)), dim3(kJoinThreads), stream, part, ck.stats, L,
              alpha, frag(L.off_u), frag(L.off_uc), frag(L.off_tc), d_lora);
-  if (e != hipSuccess || da == nullptr) return e;
+  if (e != hipSuccess || !factors) return e;
   auto* cn = wg ? (wx ? &columns_kernel<kCT, JT, true, true> : &columns_kernel<kCT, JT, true, false>)
                 : (wx ? &columns_kernel<kCT, JT, false, true> : &columns_kernel<kCT, JT, false, false>);
   const int64_t col_groups = (L.N + 16 * kCT - 1) / (16 * kCT) + (L.K + 8 * kCT - 1) / (8 * kCT);
-  e = launch(cn, dim3((unsigned)col_groups, (unsigned)L.splits_t), dim3(256), stream, g, ck, frag(L.off_uc),
-             frag(L.off_tc), L, part);
-  if (e != hipSuccess) return e;
-  return launch(&join_columns_kernel, blocks(L.r * (L.N + L.K)), dim3(256), stream, part, L, da, db);
+  return launch(cn, dim3((unsigned)col_groups, (unsigned)L.splits_t), dim3(256), stream, g, ck, frag(L.off_uc),
+                frag(L.off_tc), L, part);
 }
 
 }  // namespace
@@ -771,18 +796,19 @@ hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a
 hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
                            const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx, uint16_t* da,
                            uint16_t* db, char* ws, hipStream_t stream) {
-  if (L.M == 0) {                                       // no tokens: no ranges to sum, zeros
-    const int64_t b = (L.r * (L.N + L.K) + 255) / 256;
-    return launch(&join_columns_kernel, dim3((unsigned)(b < 4096 ? b : 4096)), dim3(256), stream,
-                  reinterpret_cast<float*>(ws), L, da, db);
-  }
-  if (L.r > 0) {
-    const hipError_t e = L.rp == 32   ? launch_lora<2>(g, ck, lora_a, lora_b, L, alpha, da, db, ws, stream)
-                         : L.rp == 64 ? launch_lora<4>(g, ck, lora_a, lora_b, L, alpha, da, db, ws, stream)
-                                      : launch_lora<8>(g, ck, lora_a, lora_b, L, alpha, da, db, ws, stream);
+  // With no tokens there are no ranges to sum: zeros.
+  const Factors factors = {reinterpret_cast<const float*>(ws + L.off_part), da, db};
+  const int64_t join_blocks = da != nullptr ? blocks_of(join_items(L)) : 0;
+  if (L.M > 0 && L.r > 0) {
+    const bool f = da != nullptr;
+    const hipError_t e = L.rp == 32   ? launch_lora<2>(g, ck, lora_a, lora_b, L, alpha, f, ws, stream)
+                         : L.rp == 64 ? launch_lora<4>(g, ck, lora_a, lora_b, L, alpha, f, ws, stream)
+                                      : launch_lora<8>(g, ck, lora_a, lora_b, L, alpha, f, ws, stream);
     if (e != hipSuccess) return e;
   }
-  if (dx == nullptr) return hipSuccess;
+  if (L.M == 0 || dx == nullptr)
+    return join_blocks == 0 ? hipSuccess
+                            : launch(&join_columns_kernel, dim3((unsigned)join_blocks), dim3(256), stream, factors, L);
   float* p = reinterpret_cast<float*>(ws + L.off_p);
   float* d_part = reinterpret_cast<float*>(ws + L.off_d_part);
   const hipError_t e = launch_grad_gemm(g, w_t, ck, L, p, d_part, stream);
@@ -796,9 +822,9 @@ hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_
   const int64_t groups = (L.M + 31) / 32, steps = L.kp / 64;
   const int64_t chunk = 4 * ((groups * steps + 4095) / 4096);
   const int64_t blocks = groups * ((steps + chunk - 1) / chunk);
-  return launch(k, dim3((unsigned)blocks), dim3(256), stream, p, d_part, ck,
+  return launch(k, dim3((unsigned)(blocks + join_blocks)), dim3(256), stream, p, d_part, ck,
                 reinterpret_cast<const u32x4*>(ws + L.off_u), reinterpret_cast<const u32x4*>(ws + L.off_a_up),
-                reinterpret_cast<const float*>(ws + L.off_d), L, chunk, dx);
+                reinterpret_cast<const float*>(ws + L.off_d), L, chunk, dx, blocks, factors);
 }
 
 }  // namespace rtl
