@@ -228,7 +228,9 @@ w4_rows_kernel(const uint16_t* __restrict__ x, const char* __restrict__ packed, 
     sp[t] = reinterpret_cast<const MetaT*>(packed + meta_at) + nt * tiles_k * 16 + col;
   }
   constexpr int kAhead = 4;                             // steps of weights requested ahead,
-  constexpr int kAheadX = XR == 8 ? 4 : 1;              // and of x
+  // and of x; at 16 rows x 64 weight rows two steps took 9.1 us where one took 9.8
+  // (16 x 4096 x 12288), elsewhere two were slower or spilled.
+  constexpr int kAheadX = XR == 8 ? 4 : XR == 16 && NT == 2 ? 2 : 1;
   u32x4 w[kAhead][NT], xv[kAheadX][kLoads];
   MetaT s[kAhead][NT];
   auto load_w = [&](int b, int64_t tile) {
@@ -389,19 +391,23 @@ hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, in
   }
   // Weight rows per workgroup: as few as give each CU one workgroup, with all
   // wavefronts along the channels; more once there are enough, which reads x
-  // less often.  Either way round at the other's sizes (us):
-  //   1 x 12288 x 4096:  16 rows 7.6, 32 rows 10.8;  1 x 4096 x 24576: 15.7, 11.5;
-  //   16 x 4096 x 4096:  16 rows 5.5, 64 rows 7.6;   16 x 4096 x 12288: 11.4, 8.5;
+  // less often, or with few channels, whose steps the loop rounds up to four.
+  // Either way round at the other's sizes (us):
+  //   1 x 12288 x 4096:  16 rows 8.7, 32 rows 12.4;  1 x 12288 x 4099: 14.2, 12.2;
+  //   1 x 4096 x 4096:   16 rows 5.3, 32 rows 6.2;   1 x 4096 x 12288: 11.5, 9.3;
+  //   1 x 1536 x 4096:   16 rows 5.3, 32 rows 4.7;
+  //   16 x 4096 x 8192:  16 rows 8.4, 64 rows 8.9;   16 x 4096 x 12288: 11.3, 9.3;
+  //   16 x 1536 x 4096:  16 rows 5.7, 64 rows 6.1;   16 x 1536 x 4099: 6.8, 6.0;
   //   32 x 4096 x 4096:  32 rows 9.7, 64 rows 12.9;  32 x 4096 x 12288: 13.7, 11.8;
   //   64 x 4096 x 4096:  32 rows of 32 x rows 8.7, 64 of 64 16.2;
   //   64 x 4096 x 12288: 19.2, 17.1.
-  const bool few = tiles_n <= 256;
+  const bool deep = tiles_k > 16;
   if (M <= 8)
-    return few ? launch_rows<8, 1, 1, 8>(x, p, meta_at, M, N, K, group, zeros, y, stream)
-               : launch_rows<8, 1, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
+    return tiles_n <= 256 && deep ? launch_rows<8, 1, 1, 8>(x, p, meta_at, M, N, K, group, zeros, y, stream)
+                                  : launch_rows<8, 1, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
   if (M <= 16)
-    return few ? launch_rows<16, 1, 1, 8>(x, p, meta_at, M, N, K, group, zeros, y, stream)
-               : launch_rows<16, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
+    return tiles_n <= (deep ? 512 : 256) ? launch_rows<16, 1, 1, 8>(x, p, meta_at, M, N, K, group, zeros, y, stream)
+                                         : launch_rows<16, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
   if (tiles_n <= 512) return launch_rows<32, 1, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
   if (M <= 32) return launch_rows<32, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
   return launch_rows<64, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);

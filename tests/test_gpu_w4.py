@@ -75,6 +75,16 @@ def test_sizes(m, k, n, group, zeros):
     check(run(*t, group), *plain(*t, group))
 
 
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("m,k,n", [(1, 2176, 4096), (8, 2176, 33), (8, 2304, 4097), (5, 2048, 130), (9, 2304, 5000),
+                                   (16, 2176, 8192), (13, 2304, 8200), (16, 2048, 4100), (12, 6400, 70)])
+def test_many_channels(m, k, n, group):
+    """Either side of the sizes at which the channels, or the weight rows, are shared out among the wavefronts."""
+    say(m, k, n, group)
+    t = make(m, k, n, group, True)
+    check(run(*t, group), *plain(*t, group))
+
+
 @pytest.mark.parametrize("group,k", [(32, 32), (32, 96), (32, 160), (32, 4128), (64, 64), (64, 192), (64, 1088)])
 @pytest.mark.parametrize("m", [1, 20, 50])
 def test_channels_that_end_inside_a_tile(group, k, m):
