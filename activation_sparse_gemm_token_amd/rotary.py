@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import _check, _here, _on, _stream, _torch, lib
 
@@ -26,6 +27,8 @@ class _Tensor(ctypes.Structure):
     _fields_ = [("x", _c_vp), ("y", _c_vp), ("heads", _c_i64)] + [
         (f"{t}_{d}_stride", _c_i64) for t in "xy" for d in ("batch", "token", "head")]
 
+
+_TENSORS = {n: struct.Struct(f"{9 * n}q") for n in (1, 2)}          # the same as plain words, which pack faster
 
 _SIG = (ctypes.c_int, [_c_vp, ctypes.c_int32, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
                        ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), _c_vp, ctypes.c_float, ctypes.c_uint32, _c_vp])
@@ -174,10 +177,11 @@ def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, invers
         if not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
         ts, st = t.shape, t.stride()
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype} like x, got {t.dtype}")
-        if ts[:-2] != lead or ts[-1] != dim:
-            raise ValueError(f"{name} must have shape {(*lead, 'heads', dim)}, got {tuple(ts)}")
+        if t is not x:
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype} like x, got {t.dtype}")
+            if ts[:-2] != lead or ts[-1] != dim:
+                raise ValueError(f"{name} must have shape {(*lead, 'heads', dim)}, got {tuple(ts)}")
         if dim > 1 and st[-1] != 1:
             raise ValueError(f"{name}: the channel stride must be 1")
         if o is None:
@@ -216,7 +220,7 @@ def _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, invers
     if axes > 1 and pos[-1] != 1:
         raise ValueError("positions: the axis stride must be 1")
     batch, tokens = lead if batched else (1, lead[0])
-    args = ((ctypes.c_int64 * len(words))(*words), len(ins), batch, tokens, dim, rot, positions.data_ptr(), pos_b, pos_t,
+    args = (_TENSORS[len(ins)].pack(*words), len(ins), batch, tokens, dim, rot, positions.data_ptr(), pos_b, pos_t,
             axes, pairs, inv_freq.data_ptr(), float(scale), flags)
     stream = _here(x, k, positions, inv_freq)
     if stream is None:

@@ -98,7 +98,7 @@ def checkpoint(x) -> Checkpoint:
     torch = _torch()
     x2 = _as_2d(x, "x")
     m, k = x2.shape
-    codes = x2.new_empty((m, k), dtype=torch.int8)
+    codes = torch.empty_like(x2, dtype=torch.int8)
     exps = x2.new_empty((m, (k + 31) // 32), dtype=torch.uint8)
     idx = x2.new_empty((m, (k + 7) // 8), dtype=torch.uint8)
     stats = x2.new_empty((m, 2), dtype=torch.float32)
