@@ -14,7 +14,8 @@
  * the matrix cores multiply the bf16 activations with 1 + q / 16, which bf16
  * holds exactly, and each group's share of the ones and of its zero point is
  * taken off with the group's sum of x; sums are fp32 and y is rounded once.
- * x must be finite: a row with an infinity or NaN gives NaN.
+ * x must be finite: a row with an infinity or NaN gives NaN.  So does one whose
+ * magnitudes, summed over a group, or a scale's sixteenfold pass fp32's range.
  *
  * Conventions are those of rtlynx.h; x, y, codes, scales, zeros and the packed
  * weight may pass 2 GiB.
