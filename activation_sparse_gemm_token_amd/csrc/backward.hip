@@ -610,6 +610,101 @@ __global__ void __launch_bounds__(256) join_columns_kernel(Factors f, BackwardLa
   join_columns(f, L, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
+// --- 6. G W of few tokens -------------------------------------------------------
+// The dense GEMM's tiles of 256 tokens leave most of the chip idle then, and a
+// tile's start and end cost more than its products.  Here a workgroup takes 64
+// tokens x 64 channels and a range of the contraction, its 4 wavefronts 64 of it
+// in turn, operands straight from memory; the wavefronts' sums meet in LDS, where
+// each takes 16 tokens.  P and D's shares as in the dense GEMM's form (lane: one
+// token, channel 16 quad + 4 t + e of the 64 in block t).
+template <bool WIDE>
+__global__ void __launch_bounds__(256, 2)
+few_tokens_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ w_t, Ckpt ck, BackwardLayout L,
+                  float* __restrict__ p, float* __restrict__ d_part) {
+  __shared__ f32x4 lds[4 * 16 * 64];
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tiles_m = (L.M + 63) / 64, tiles = tiles_m * L.p_tiles;
+  const int64_t split = blockIdx.x / tiles, id = blockIdx.x - split * tiles;
+  const int64_t tn = id / tiles_m, m0 = 64 * (id - tn * tiles_m);
+  const int64_t steps = (L.N + 63) / 64, per = (steps + L.p_splits - 1) / L.p_splits;
+  const int64_t lo = split * per, hi = lo + per < steps ? lo + per : steps;
+  const __amdgpu_buffer_rsrc_t gr = make_rsrc(g, L.M * L.N * 2), wr = make_rsrc(w_t, L.K * L.N * 2);
+  const int N = (int)L.N;
+  uint32_t xrow[4], wrow[4];                            // past the tensors' ends: zeros
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    xrow[i] = (uint32_t)((m0 + 16 * i + col) * L.N * 2);
+    wrow[i] = (uint32_t)((64 * tn + 16 * (col >> 2) + 4 * i + (col & 3)) * L.N * 2);
+  }
+  struct Stage {
+    u32x4 x[4][2], w[4][2];
+  };
+  f32x4 acc[16];                                        // [16 tokens][block]
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = kZero4;
+  auto load = [&](Stage& s, int64_t t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (int)(64 * t) + 32 * h + 8 * quad;
+        s.x[i][h] = load8<WIDE>(gr, xrow[i], c, N);
+        s.w[i][h] = load8<WIDE>(wr, wrow[i], c, N);
+      }
+  };
+  auto use = [&](const Stage& s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[4 * i + j] = mfma(s.w[j][h], s.x[i][h], acc[4 * i + j]);
+  };
+  Stage s0, s1;
+  int64_t t = lo + wave;
+  if (t < hi) load(s0, t);
+  for (; t + 8 < hi; t += 8) {
+    load(s1, t + 4);
+    use(s0);
+    load(s0, t + 8);
+    use(s1);
+  }
+  if (t + 4 < hi) {
+    load(s1, t + 4);
+    use(s0);
+    use(s1);
+  } else if (t < hi) {
+    use(s0);
+  }
+  const int64_t row = m0 + 16 * wave + col;             // this wavefront's tokens from here on
+  Ckpt16 f = ckpt_load16(ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K), ckpt_row(row, L.K), (int)(64 * tn) + 16 * quad,
+                         (int)L.K);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) lds[(wave * 16 + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  f32x4 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = lds[(4 * wave + j) * 64 + lane];
+#pragma unroll
+    for (int s = 1; s < 4; ++s) v[j] += lds[(16 * s + 4 * wave + j) * 64 + lane];
+  }
+  const int64_t block = m0 / 16 + wave, rows16 = (L.M + 15) / 16;
+  if (block >= rows16) return;
+  f32x4* const out = reinterpret_cast<f32x4*>(p) + ((split * rows16 + block) * (L.kp / 16) + 4 * tn) * 64 + lane;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[64 * j] = v[j];
+  ckpt_clip16(f, (int)(64 * tn) + 16 * quad, (int)L.K);
+  float d = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d += ckpt_kept_dot(f, j, v[j]);
+  d = __builtin_amdgcn_ldexpf(d, (int)f.exp - 133);
+  d += __shfl_xor(d, 16, 64);
+  d += __shfl_xor(d, 32, 64);
+  if (quad == 0 && row < L.M) d_part[(split * L.p_tiles + tn) * L.M + row] = d;
+}
+
 // --- 7. dX -----------------------------------------------------------------------
 // 32 tokens (two of P's block rows) and a range of channels per workgroup, its 4
 // wavefronts 64 channels (four of P's blocks) in turn: lane l has token l % 16,
@@ -662,7 +757,22 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
       f.x[i] = ckpt_load16(kr, rows[i], (int)(64 * t + 16 * quad), K);
     }
     if constexpr (SPLIT) {
-      for (int64_t q = 1; q < L.p_splits; ++q)
+      // Two ranges' loads at a time, added in the ranges' order.
+      int64_t q = 1;
+      for (; q + 1 < L.p_splits; q += 2) {
+        f32x4 v[2][2][4];
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[z][i][n] = pr[i][(q + z) * slab + (4 * t + n) * 64];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) f.p[i][n] = f.p[i][n] + v[0][i][n] + v[1][i][n];
+      }
+      if (q < L.p_splits)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -811,7 +921,11 @@ hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_
                             : launch(&join_columns_kernel, dim3((unsigned)join_blocks), dim3(256), stream, factors, L);
   float* p = reinterpret_cast<float*>(ws + L.off_p);
   float* d_part = reinterpret_cast<float*>(ws + L.off_d_part);
-  const hipError_t e = launch_grad_gemm(g, w_t, ck, L, p, d_part, stream);
+  const hipError_t e =
+      L.p_tile == 64 ? launch(L.N % 8 == 0 ? &few_tokens_kernel<true> : &few_tokens_kernel<false>,
+                              dim3((unsigned)((L.M + 63) / 64 * L.p_tiles * L.p_splits)), dim3(256), stream, g, w_t, ck, L,
+                              p, d_part)
+                     : launch_grad_gemm(g, w_t, ck, L, p, d_part, stream);
   if (e != hipSuccess) return e;
   const bool split = L.p_splits > 1;
   auto* k = L.r == 0     ? (split ? &finish_kernel<0, true> : &finish_kernel<0, false>)

@@ -54,18 +54,25 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   L.chunk_t = chunk(L.mp, L.rp == 128 ? 7 * kCus / 2 : 2 * kCus, (N + cols_g - 1) / cols_g + (K + cols_x - 1) / cols_x, 128);
   L.splits_t = (L.mp + L.chunk_t - 1) / L.chunk_t;
   // G W: tile columns and contraction ranges by the time they should take, in
-  // us: a k-step of 64 measured 1.65 (256 columns) and 1.25 (192) with the chip
-  // full, plus 8 per tile, plus writing and reading the ranges' results.
+  // us.  With 256 and 192 columns a k-step of 64 measured 1.65 and 1.25 with the
+  // chip full, plus 8 per tile.  With 64 (few_tokens_kernel) a workgroup's four
+  // wavefronts take a step each, 1.7 per workgroup on a CU, plus 3 once.  Then
+  // writing and reading the ranges' results, 0.6 each at the least.
+  //   77 x 520 x 264:      5.0 us with 64 columns, 12.4 otherwise;
+  //   16 x 1024 x 4096:    6.2, 13.3;   2000 x 512 x 512: 8.8, 19.4;
+  //   256 x 3072 x 3072:   27.6, 24.4 (with dX 34.0, 33.2);
+  //   512 x 3072 x 12288:  144, 48.
   const int64_t tiles_m = (M + 255) / 256, steps = (N + 63) / 64;
   double best = 0;
-  for (int64_t tn : {256, 192}) {
+  for (int64_t tn : {256, 192, 64}) {
     if (tn == 192 && N % 8 != 0) continue;
-    const int64_t tiles = (K + tn - 1) / tn;
-    for (int64_t s = 1; s <= 16 && (s == 1 || steps / s >= 2); ++s) {
-      const int64_t rounds = (tiles_m * tiles * s + kCus - 1) / kCus, per = (steps + s - 1) / s;
+    const int64_t tiles = (K + tn - 1) / tn, least = tn == 64 ? 4 : 2;
+    for (int64_t s = 1; s <= 16 && (s == 1 || steps / s >= least); ++s) {
+      const int64_t per = (steps + s - 1) / s;
       if (s > 1 && (s - 1) * per >= steps) continue;                    // the last range would be empty
-      const double t = (double)rounds * ((double)per * (tn == 256 ? 1.65 : 1.25) + 8) +
-                       (double)s * (double)M * (double)L.kp * 8 / 5e6;
+      const int64_t groups = (tn == 64 ? (M + 63) / 64 : tiles_m) * tiles * s, rounds = (groups + kCus - 1) / kCus;
+      const double each = tn == 64 ? (double)((per + 3) / 4) * 1.7 : (double)per * (tn == 256 ? 1.65 : 1.25) + 8;
+      const double t = (double)rounds * each + (tn == 64 ? 3 : 0) + 0.6 * (double)(s - 1) + (double)s * (double)M * (double)L.kp * 8 / 5e6;
       if (best == 0 || t < best) {
         best = t;
         L.p_tile = tn;

@@ -367,3 +367,32 @@ def test_large_tiles_and_ranges():
                                                                      (rest.abs() @ a.abs().t().contiguous())))):
             tol_i = plain.HALF_BF16 * want.abs() + (plain.depth(m) * plain.U24 + plain.U16 + 4 * plain.U24) * size + lost
             assert ((got_i.double() - want).abs() <= tol_i).all()
+
+
+@pytest.mark.parametrize("m,n,k,r", [(1, 64, 64, 4), (15, 4, 4, 0), (16, 452, 60, 3), (63, 260, 516, 16), (64, 4096, 128, 0),
+                                     (65, 4100, 68, 32), (130, 1000, 1004, 7), (200, 3000, 132, 64), (333, 516, 64, 128)])
+def test_few_tokens(m, n, k, r):
+    """Tiles of 64 tokens, one contraction range and several, tails in all three sizes."""
+    say("few tokens", m, n, k, r)
+    t = layer(m, n, k, r)
+    ws = torch.full((training.backward_workspace_bytes(m, n, k, r),), 0xff, dtype=torch.uint8, device=DEV)
+    got = run(t, -0.7, workspace=ws)
+    check(got, *reference(t, -0.7))
+    for a, b in zip(got, run(t, -0.7)):
+        assert a is b is None or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,n,k", [(1944, 40, 1612), (640, 64, 6456), (66, 1032, 8248), (216, 960, 8240), (1805, 36, 1784),
+                                   (77, 1580, 9152), (4774, 32, 2904), (524, 1816, 8668), (5383, 320, 4664)])
+def test_wide_tiles(m, n, k):
+    """192 and 256 columns with every channel tail, one contraction range and several; sampled rows against fp64."""
+    say("wide tiles", m, n, k)
+    t = layer(m, n, k, 16)
+    ws = torch.full((training.backward_workspace_bytes(m, n, k, 16),), 0xff, dtype=torch.uint8, device=DEV)
+    got = run(t, 0.5, workspace=ws, need_lora=False)[0]
+    rows = torch.tensor(sorted({0, 1, 15, 16, 63, 64, 255, 256, m // 2, m - 1} & set(range(m))), device=DEV)
+    kept = t["kept"]
+    part = dict(t, g=t["g"][rows], kept=training.Checkpoint(*(getattr(kept, f)[rows].contiguous()
+                                                              for f in ("codes", "exps", "idx", "stats"))))
+    ref, tol = reference(part, 0.5)
+    check((got[rows], None, None), ref, tol)
