@@ -1,7 +1,7 @@
 // rtl_sparse_linear_backward (include/rtlynx_train.h).
 //
 // The work is one large product, G W [M, K] over N channels, which runs on the
-// dense GEMM's ring (dense_gemm.hip), and the LoRA branch, whose products all
+// dense GEMM's ring (dense_gemm.hip) unless the tokens are few, and the LoRA branch, whose products all
 // have one dimension of at most 128 and are bound by reading G and the
 // checkpoint:
 //
@@ -20,7 +20,7 @@
 //   5. join_columns         sums the token ranges in order into dA and dB (a kernel
 //                           of its own where dX is not asked for, else part of 7).
 //   6. the dense GEMM       P = G W, in 16 x 16 blocks of fp32, and of each tile
-//                           its share of D.
+//      or few_tokens_kernel its share of D.
 //   7. finish_kernel        D per token, then dX; U A is formed again, a 16-token
 //                           strip at a time, on the matrix cores (r is small), so it
 //                           never goes to memory.

@@ -145,6 +145,7 @@ RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* c
   if (M == 0 && da == nullptr) return RTL_OK;
   if (!rtl::aligned(dx, 16) || !rtl::aligned(da, 16) || !rtl::aligned(db, 16)) return RTL_ERR_MISALIGNED;
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  const rtl::BackwardLayout L = rtl::backward_layout(M, N, K, r);
   if (M > 0) {
     if (g == nullptr || codes == nullptr || exps == nullptr || idx == nullptr || stats == nullptr ||
         (dx != nullptr && w_t == nullptr) || (r > 0 && (lora_a == nullptr || lora_b == nullptr)))
@@ -153,12 +154,12 @@ RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* c
         !rtl::aligned(stats, 16) || (dx != nullptr && !rtl::aligned(w_t, 16)) ||
         (r > 0 && (!rtl::aligned(lora_a, 16) || !rtl::aligned(lora_b, 16))))
       return RTL_ERR_MISALIGNED;
-    if (workspace == nullptr || workspace_bytes < rtl::backward_layout(M, N, K, r).total) return RTL_ERR_WORKSPACE;
+    if (workspace == nullptr || workspace_bytes < L.total) return RTL_ERR_WORKSPACE;
     if (!rtl::aligned(workspace, 16)) return RTL_ERR_MISALIGNED;
   }
   const rtl_status d = rtl::check_device(stream);
   if (d != RTL_OK) return d;
   const rtl::Ckpt ck{codes, exps, idx, stats};
-  return rtl::from_hip(rtl::launch_backward(g, ck, w_t, lora_a, lora_b, rtl::backward_layout(M, N, K, r), lora_scale,
-                                            dx, da, db, static_cast<char*>(workspace), stream));
+  return rtl::from_hip(rtl::launch_backward(g, ck, w_t, lora_a, lora_b, L, lora_scale, dx, da, db,
+                                            static_cast<char*>(workspace), stream));
 }
