@@ -1,9 +1,9 @@
 // rtl_sparse_linear_backward (include/rtlynx_train.h).
 //
 // The work is one large product, G W [M, K] over N channels, which runs on the
-// dense GEMM's ring (dense_gemm.hip) unless the tokens are few, and the LoRA branch, whose products all
-// have one dimension of at most 128 and are bound by reading G and the
-// checkpoint:
+// dense GEMM's ring (dense_gemm.hip) unless the tokens are few, and the LoRA
+// branch, whose products all have one dimension of at most 128 and are bound by
+// reading G and the checkpoint:
 //
 //   1. factors_kernel       A and B as matrix-core fragments, zero-padded.
 //   2. rows_kernel          G B, and of the checkpoint (pruned A^T) and (kept
@@ -705,6 +705,19 @@ few_tokens_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ w
   if (quad == 0 && row < L.M) d_part[(split * L.p_tiles + tn) * L.M + row] = d;
 }
 
+// Rows of 8-byte units copied to rows half a unit of 16 bytes longer, the last 8
+// bytes zeros: the ring's 16-byte copies then serve N % 8 == 4 too.
+__global__ void __launch_bounds__(256)
+pad_kernel(const u32x2* __restrict__ g, const u32x2* __restrict__ w_t, int64_t rows_g, int64_t rows_w, int64_t units,
+           u32x2* __restrict__ out) {
+  const int64_t all = (rows_g + rows_w) * (units + 1);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / (units + 1), u = i - row * (units + 1);
+    const u32x2* src = row < rows_g ? g + row * units : w_t + (row - rows_g) * units;
+    out[i] = u < units ? src[u] : (u32x2){0, 0};
+  }
+}
+
 // --- 7. dX -----------------------------------------------------------------------
 // 32 tokens (two of P's block rows) and a range of channels per workgroup, its 4
 // wavefronts 64 channels (four of P's blocks) in turn: lane l has token l % 16,
@@ -921,6 +934,15 @@ hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_
                             : launch(&join_columns_kernel, dim3((unsigned)join_blocks), dim3(256), stream, factors, L);
   float* p = reinterpret_cast<float*>(ws + L.off_p);
   float* d_part = reinterpret_cast<float*>(ws + L.off_d_part);
+  if (L.p_length != L.N) {
+    uint16_t* const pad = reinterpret_cast<uint16_t*>(ws + L.off_pad);
+    const hipError_t e = launch(&pad_kernel, dim3((unsigned)blocks_of((L.M + L.K) * L.p_length / 4)), dim3(256), stream,
+                                reinterpret_cast<const u32x2*>(g), reinterpret_cast<const u32x2*>(w_t), L.M, L.K,
+                                L.N / 4, reinterpret_cast<u32x2*>(pad));
+    if (e != hipSuccess) return e;
+    g = pad;
+    w_t = pad + L.M * L.p_length;
+  }
   const hipError_t e =
       L.p_tile == 64 ? launch(L.N % 8 == 0 ? &few_tokens_kernel<true> : &few_tokens_kernel<false>,
                               dim3((unsigned)((L.M + 63) / 64 * L.p_tiles * L.p_splits)), dim3(256), stream, g, w_t, ck, L,

@@ -111,22 +111,6 @@ __device__ __forceinline__ void dma_w_ordered_asm(__amdgpu_buffer_rsrc_t wr, con
   (void)saved;
 }
 
-// The same order for K % 8 == 4 (dma_w_tile_dword's 4-byte copies).
-__device__ __forceinline__ void dma_w_ordered_dword(__amdgpu_buffer_rsrc_t wr, int64_t N, int64_t K, int64_t n0,
-                                                    int64_t k0, char* lds_stage) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-#pragma unroll
-  for (int b = 0; b < 128 / kWaves; ++b) {
-    const int row = (256 / kWaves) * wave + 2 * b + (lane >> 5);
-    const int chunk = ((lane & 31) >> 2) ^ (row & 7);
-    const int64_t n = n0 + (row & ~63) + 16 * ((row >> 2) & 3) + 4 * ((row >> 4) & 3) + (row & 3);
-    const int64_t k = k0 + 8 * chunk + 2 * (lane & 3);
-    const uint32_t voff = (k + 2 <= K && n < N) ? (uint32_t)((n * K + k) * 2) : kOobOffset;
-    char* dst = lds_stage + ((256 / kWaves) * wave + 2 * b) * 128;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (__attribute__((address_space(3))) void*)(dst), 4, voff, 0, 0, 0);
-  }
-}
-
 // The tiled form's result and what it needs to form D.
 struct GradOut {
   float* p;
@@ -145,7 +129,8 @@ template <int KM, int TN, bool TILED>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w,
                   int64_t M, int64_t N, int64_t K, std::conditional_t<TILED, GradOut, uint16_t* __restrict__> y) {
-  static_assert(TN == 256 || (TN == 192 && TILED && KM != kAligned8), "192 columns: the tiled form's 16-byte copies");
+  static_assert(TN == 256 || (TN == 192 && TILED), "192 columns: the tiled form only");
+  static_assert(!TILED || KM != kAligned8, "the tiled form copies 16 bytes");
   constexpr int kWavesN = TN == 256 ? 4 : 2, kWavesM = kWaves / kWavesN;
   constexpr int kTileN = TN, kWaveM = kTileM / kWavesM, kWaveN = TN / kWavesN;
   constexpr int kRB = kWaveM / 16, kCB = kWaveN / 16;
@@ -202,8 +187,7 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
   auto copy_w = [&](int64_t step, char* dst) {
     const int64_t ks = TILED ? k_lo + step : step;
     if constexpr (KM == kAligned8) {
-      if constexpr (TILED) dma_w_ordered_dword(wr, N, K, n0, ks * kTileK, dst);
-      else dma_w_tile_dword<kWaves>(wr, N, K, n0, ks * kTileK, dst);
+      dma_w_tile_dword<kWaves>(wr, N, K, n0, ks * kTileK, dst);
     } else {
       const uint32_t lds_addr = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)(dst);
       if constexpr (TILED) dma_w_ordered_asm<TN / 64>(wr, wo, K, ks * kTileK, lds_addr, KM == kAligned16);
@@ -369,14 +353,13 @@ hipError_t launch_dense_gemm(const uint16_t* x, const uint16_t* w, int64_t M, in
 
 hipError_t launch_grad_gemm(const uint16_t* g, const uint16_t* w_t, const Ckpt& ck, const BackwardLayout& L, float* p,
                             float* d_part, hipStream_t stream) {
-  const int64_t M = L.M, N = L.K, K = L.N;              // result columns N, contraction K
+  const int64_t M = L.M, N = L.K, K = L.p_length;       // result columns N, contraction K
   const GradOut out{p, d_part, ck, L.kp / 16, L.p_splits};
   const dim3 grid((unsigned)((M + kTileM - 1) / kTileM * L.p_tiles * L.p_splits)), block(kThreads);
   auto* k = L.p_tile == 192 ? (K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 192, true>
                                                : &dense_gemm_kernel<kAligned16, 192, true>)
             : K % kTileK == 0 ? &dense_gemm_kernel<kFullK, 256, true>
-            : K % 8 == 0      ? &dense_gemm_kernel<kAligned16, 256, true>
-                              : &dense_gemm_kernel<kAligned8, 256, true>;
+                              : &dense_gemm_kernel<kAligned16, 256, true>;
   return launch(k, grid, block, stream, g, w_t, M, N, K, out);
 }
 

@@ -62,7 +62,8 @@ struct BackwardLayout {
   int64_t splits_g, splits_x;
   int64_t chunk_t, splits_t;                       // tokens per workgroup of the products over tokens
   int64_t p_tile, p_tiles, p_splits;               // G W: tile columns, their number, contraction ranges
-  size_t off_a_down, off_a_up, off_b, off_u, off_uc, off_tc, off_d, off_part, off_p, off_d_part, total;
+  int64_t p_length;                                // and the rows' length there: N, or N + 4 for padded copies
+  size_t off_a_down, off_a_up, off_b, off_u, off_uc, off_tc, off_d, off_part, off_p, off_d_part, off_pad, total;
 };
 BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t r);
 // The backward pass's P = G W on the dense GEMM's ring (dense_gemm.hip): the
@@ -70,7 +71,7 @@ BackwardLayout backward_layout(int64_t M, int64_t N, int64_t K, int64_t r);
 // blocks, [range][ceil(M / 16)][kp / 16][lane][4], lane l of block t of every
 // four holding token l % 16, channels 16 (l / 16) + 4 t + [0, 4) of the 64; and of
 // each tile and range the sums of kept x * P over the tile's channels, d_part
-// [range][tile][M].
+// [range][tile][M].  Rows of g and w_t are L.p_length long, a multiple of 8.
 hipError_t launch_grad_gemm(const uint16_t* g, const uint16_t* w_t, const Ckpt& ck, const BackwardLayout& L,
                             float* p, float* d_part, hipStream_t stream);
 hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,

@@ -56,8 +56,10 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   // G W: tile columns and contraction ranges by the time they should take, in
   // us.  With 256 and 192 columns a k-step of 64 measured 1.65 and 1.25 with the
   // chip full, plus 8 per tile.  With 64 (few_tokens_kernel) a workgroup's four
-  // wavefronts take a step each, 1.7 per workgroup on a CU, plus 3 once.  Then
-  // writing and reading the ranges' results, 0.6 each at the least.
+  // wavefronts take a step each, 1.7 per workgroup on a CU (2.2 with N % 8 == 4,
+  // two loads instead of one), plus 3 once.  Then writing and reading the ranges'
+  // results, 0.6 each at the least, and the wide tiles' padded copies of G and W
+  // where N % 8 == 4.
   //   77 x 520 x 264:      5.0 us with 64 columns, 12.4 otherwise;
   //   16 x 1024 x 4096:    6.2, 13.3;   2000 x 512 x 512: 8.8, 19.4;
   //   256 x 3072 x 3072:   27.6, 24.4 (with dX 34.0, 33.2);
@@ -65,19 +67,22 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   const int64_t tiles_m = (M + 255) / 256, steps = (N + 63) / 64;
   double best = 0;
   for (int64_t tn : {256, 192, 64}) {
-    if (tn == 192 && N % 8 != 0) continue;
+    const bool pad = tn != 64 && N % 8 != 0;
+    if (pad && !(size_ok(M, N + 4) && size_ok(K, N + 4))) continue;
     const int64_t tiles = (K + tn - 1) / tn, least = tn == 64 ? 4 : 2;
     for (int64_t s = 1; s <= 16 && (s == 1 || steps / s >= least); ++s) {
       const int64_t per = (steps + s - 1) / s;
       if (s > 1 && (s - 1) * per >= steps) continue;                    // the last range would be empty
       const int64_t groups = (tn == 64 ? (M + 63) / 64 : tiles_m) * tiles * s, rounds = (groups + kCus - 1) / kCus;
-      const double each = tn == 64 ? (double)((per + 3) / 4) * 1.7 : (double)per * (tn == 256 ? 1.65 : 1.25) + 8;
-      const double t = (double)rounds * each + (tn == 64 ? 3 : 0) + 0.6 * (double)(s - 1) + (double)s * (double)M * (double)L.kp * 8 / 5e6;
+      const double each = tn == 64 ? (double)((per + 3) / 4) * (N % 8 == 0 ? 1.7 : 2.2) : (double)per * (tn == 256 ? 1.65 : 1.25) + 8;
+      const double t = (double)rounds * each + (tn == 64 ? 3 : 0) + (pad ? 3 + (double)((M + K) * N) * 4 / 5e6 : 0) +
+                       0.6 * (double)(s - 1) + (double)s * (double)M * (double)L.kp * 8 / 5e6;
       if (best == 0 || t < best) {
         best = t;
         L.p_tile = tn;
         L.p_tiles = tiles;
         L.p_splits = s;
+        L.p_length = pad ? N + 4 : N;
       }
     }
   }
@@ -95,6 +100,7 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   L.off_part = take(rows > over_t ? rows : over_t);
   L.off_p = take(L.p_splits * round_up(M, 16) * L.kp * 4);
   L.off_d_part = take(L.p_splits * L.p_tiles * M * 4);
+  if (L.p_length != N) L.off_pad = take((M + K) * L.p_length * 2);
   L.total = o;
   return L;
 }

@@ -383,7 +383,8 @@ def test_few_tokens(m, n, k, r):
 
 
 @pytest.mark.parametrize("m,n,k", [(1944, 40, 1612), (640, 64, 6456), (66, 1032, 8248), (216, 960, 8240), (1805, 36, 1784),
-                                   (77, 1580, 9152), (4774, 32, 2904), (524, 1816, 8668), (5383, 320, 4664)])
+                                   (77, 1580, 9152), (4774, 32, 2904), (524, 1816, 8668), (5383, 320, 4664),
+                                   (1314, 3820, 1748), (300, 1084, 8200), (5300, 60, 4600), (1030, 316, 9000)])
 def test_wide_tiles(m, n, k):
     """192 and 256 columns with every channel tail, one contraction range and several; sampled rows against fp64."""
     say("wide tiles", m, n, k)
