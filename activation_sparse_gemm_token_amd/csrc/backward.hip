@@ -896,7 +896,8 @@ hipError_t launch_lora(const uint16_t* g, const Ckpt& ck, const uint16_t* lora_a
   auto frag = [&](size_t off) { return reinterpret_cast<u32x4*>(ws + off); };
   float* d_lora = reinterpret_cast<float*>(ws + L.off_d);
   float* part = reinterpret_cast<float*>(ws + L.off_part);
-  hipError_t e = launch(&factors_kernel, dim3((unsigned)blocks_of(L.rp * (2 * L.kp + L.np) / 8)), dim3(256), stream, lora_a, lora_b, L,
+  const dim3 factor_blocks((unsigned)blocks_of(L.rp * (2 * L.kp + L.np) / 8));
+  hipError_t e = launch(&factors_kernel, factor_blocks, dim3(256), stream, lora_a, lora_b, L,
                         frag(L.off_a_down), frag(L.off_a_up), frag(L.off_b));
   if (e != hipSuccess) return e;
   const bool wg = L.N % 8 == 0, wx = L.K % 8 == 0;

@@ -74,7 +74,8 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
       const int64_t per = (steps + s - 1) / s;
       if (s > 1 && (s - 1) * per >= steps) continue;                    // the last range would be empty
       const int64_t groups = (tn == 64 ? (M + 63) / 64 : tiles_m) * tiles * s, rounds = (groups + kCus - 1) / kCus;
-      const double each = tn == 64 ? (double)((per + 3) / 4) * (N % 8 == 0 ? 1.7 : 2.2) : (double)per * (tn == 256 ? 1.65 : 1.25) + 8;
+      const double each = tn == 64 ? (double)((per + 3) / 4) * (N % 8 == 0 ? 1.7 : 2.2)
+                                   : (double)per * (tn == 256 ? 1.65 : 1.25) + 8;
       const double t = (double)rounds * each + (tn == 64 ? 3 : 0) + (pad ? 3 + (double)((M + K) * N) * 4 / 5e6 : 0) +
                        0.6 * (double)(s - 1) + (double)s * (double)M * (double)L.kp * 8 / 5e6;
       if (best == 0 || t < best) {
