@@ -10,9 +10,8 @@
 //                           A^T): token-by-rank products over the channels.
 //   3. join_rows_kernel     sums the channel ranges in order, forms U = alpha G B,
 //                           T = alpha (pruned A^T + (1 - s) kept A^T) and the part
-//                           of D that needs no G W, and writes U, (1 - s) U and T as
-//                           the fragments of the products that follow, each value as
-//                           two bf16 words (hi + lo: 16 significant bits).
+//                           of D that needs no G W, and writes U, (1 - s) U and T in
+//                           the lane order of the products that follow, in fp32.
 //   4. columns_kernel       G^T T and [pruned; kept]^T [U; (1 - s) U]: products over
 //                           the tokens.  Both operands run along tokens, which are
 //                           rows in memory: the tile goes through LDS and is read
@@ -28,7 +27,7 @@
 // A kept value's residual (1 - s) x is not a bf16 number; multiplying U (or the
 // joined sum) by 1 - s instead keeps the checkpoint's values exact operands.
 //
-// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 38, join 7, columns 38, G W
+// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 38, join 7, columns 48, G W
 // 250 to 280 as the clock drops, dX with the sums of dA and dB 30 (27 and, in a
 // launch of their own, 7.6).  Rows and columns read G (100 MB) and the checkpoint
 // (14 MB), 22 us at the card's copy rate.
@@ -46,20 +45,32 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// fp32 as two bf16 words: hi + lo holds 16 significant bits.
-struct Split {
-  u32x4 hi, lo;
+// 8 fp32 values of a lane as three operands of bf16 whose sum they are: each
+// word takes the value's next 8 of 24 significant bits (cut off, not rounded, so
+// every remainder is exact).  U and T are sums, so they keep fp32's bits between
+// the products; held in two words (16 bits) they turned ten times as many last
+// bits of the results as fp32's own rounding does.  They travel as fp32, no more
+// bytes than two words, and are split where they are used.
+struct Words {
+  u32x4 w[3];
 };
-__device__ __forceinline__ Split split8(const float (&v)[8]) {
-  Split r;
+__device__ __forceinline__ Words split24(u32x4 first, u32x4 last) {
+  Words r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = v[2 * i], b = v[2 * i + 1];
-    const uint32_t h = cvt_pk_bf16(a, b);
-    r.hi[i] = h;
-    r.lo[i] = cvt_pk_bf16(a - bf16_lo_to_f32(h), b - bf16_hi_to_f32(h));
+    uint32_t a = i < 2 ? first[2 * i] : last[2 * i - 4], b = i < 2 ? first[2 * i + 1] : last[2 * i - 3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      r.w[n][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+      a = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) - __builtin_bit_cast(float, a & 0xffff0000u));
+      b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, b) - __builtin_bit_cast(float, b & 0xffff0000u));
+    }
   }
   return r;
+}
+__device__ __forceinline__ u32x4 raw4(const float* v) {
+  return (u32x4){__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                 __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
 }
 
 // 8 channels at channel c of a row of C (C % 4 == 0) of a bf16 tensor, `row` its
@@ -323,9 +334,10 @@ rows_kernel(const uint16_t* __restrict__ g, const u32x4* __restrict__ b, const u
 
 // --- 3. U, T and what follows from them -------------------------------------
 // 32 tokens per workgroup: one contraction step of the products over tokens.
-// Tokens past M are written as zeros.  u [mp / 16][rp / 32][hi, lo]: rows tokens,
-// contraction ranks; uc [mp / 32][U, (1 - s) U][rp / 16][hi, lo] and
-// tc [mp / 32][rp / 16][hi, lo]: rows ranks, contraction tokens.
+// Tokens past M are written as zeros.  u [mp / 16][rp / 32][2]: rows tokens,
+// contraction ranks; uc [mp / 32][U, (1 - s) U][rp / 16][2] and
+// tc [mp / 32][rp / 16][2]: rows ranks, contraction tokens; [2] the halves of a
+// lane's 8 fp32 values.
 constexpr int kJoinThreads = 512;
 
 template <int RP>
@@ -377,13 +389,9 @@ join_rows_kernel(const float* __restrict__ part, const float* __restrict__ stats
   for (int i = threadIdx.x; i < 2 * (RP / 32) * 64; i += kJoinThreads) {      // u
     const int lane = i & 63, f = i >> 6, tile = f / (RP / 32), step = f % (RP / 32);
     const float* p = us + (16 * tile + (lane & 15)) * kPitch + 32 * step + 8 * (lane >> 4);
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[e];
-    const Split s = split8(v);
     u32x4* o = u_out + (((m0 / 16 + tile) * (RP / 32) + step) * 2) * 64 + lane;
-    o[0] = s.hi;
-    o[64] = s.lo;
+    o[0] = raw4(p);
+    o[64] = raw4(p + 4);
   }
   for (int i = threadIdx.x; i < (RP / 16) * 64; i += kJoinThreads) {          // uc, tc
     const int lane = i & 63, jt = i >> 6, j = 16 * jt + (lane & 15), r0 = 8 * (lane >> 4);
@@ -396,17 +404,14 @@ join_rows_kernel(const float* __restrict__ part, const float* __restrict__ stats
       t[e] = ts[(r0 + e) * kPitch + j];
     }
     u32x4* o = uc_out + ((int64_t)blockIdx.x * 2 * (RP / 16) + jt) * 128 + lane;
-    Split s = split8(u);
-    o[0] = s.hi;
-    o[64] = s.lo;
-    s = split8(k);
+    o[0] = raw4(u);
+    o[64] = raw4(u + 4);
     o += (RP / 16) * 128;
-    o[0] = s.hi;
-    o[64] = s.lo;
-    s = split8(t);
+    o[0] = raw4(k);
+    o[64] = raw4(k + 4);
     o = tc_out + ((int64_t)blockIdx.x * (RP / 16) + jt) * 128 + lane;
-    o[0] = s.hi;
-    o[64] = s.lo;
+    o[0] = raw4(t);
+    o[64] = raw4(t + 4);
   }
 }
 
@@ -431,17 +436,19 @@ __device__ __forceinline__ u32x4 transposed_operand(const uint16_t* tile, int c)
   return (u32x4){a2[0], a2[1], b2[0], b2[1]};
 }
 
-// One 32-token step of one staged tile against its fragments (hi, lo).
+// One 32-token step of one staged tile against its factors.
 template <int CT, int JT>
 __device__ __forceinline__ void col_step(const uint16_t* tile, const u32x4 (&w)[2 * JT], f32x4* acc) {
+  u32x4 x[CT];
 #pragma unroll
-  for (int i = 0; i < CT; ++i) {
-    const u32x4 x = transposed_operand<CT>(tile, 16 * i);
+  for (int i = 0; i < CT; ++i) x[i] = transposed_operand<CT>(tile, 16 * i);
 #pragma unroll
-    for (int j = 0; j < JT; ++j) {
-      acc[i * JT + j] = mfma(x, w[2 * j], acc[i * JT + j]);
-      acc[i * JT + j] = mfma(x, w[2 * j + 1], acc[i * JT + j]);
-    }
+  for (int j = 0; j < JT; ++j) {
+    const Words s = split24(w[2 * j], w[2 * j + 1]);
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+#pragma unroll
+      for (int i = 0; i < CT; ++i) acc[i * JT + j] = mfma(x[i], s.w[n], acc[i * JT + j]);
   }
 }
 
@@ -803,13 +810,13 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
     for (int64_t i = threadIdx.x >> 5; i < L.p_splits * L.p_tiles; i += 8) d += d_part[i * L.M + row];
     red[threadIdx.x] = d;
   }
-  u32x4 uh[2][RT > 0 ? RT : 1], ul[2][RT > 0 ? RT : 1];
+  Words us[2][RT > 0 ? RT : 1];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      uh[i][r] = u[(((b0 + i) * RT + r) * 2) * 64 + lane];
-      ul[i][r] = u[(((b0 + i) * RT + r) * 2 + 1) * 64 + lane];
+      const u32x4* const f = u + (((b0 + i) * RT + r) * 2) * 64 + lane;
+      us[i][r] = split24(f[0], f[64]);
     }
   __syncthreads();
   float per[2], per_kept[2];                            // D / Lk of a pruned channel; times 1 - s of a kept one
@@ -834,10 +841,9 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
       for (int r = 0; r < RT; ++r) {
         const u32x4 a = a_up[((4 * t + n) * RT + r) * 64 + lane];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          v[i] = mfma(a, uh[i][r], v[i]);
-          v[i] = mfma(a, ul[i][r], v[i]);
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int w = 0; w < 3; ++w) v[i] = mfma(a, us[i][r].w[w], v[i]);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {

@@ -78,9 +78,9 @@ size_t rtl_sparse_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t 
  *            16-byte aligned, overwritten.
  *
  * N % 4 == 0 (N >= 4), K % 4 == 0, 0 <= r <= RTL_MAX_LORA_RANK.  Products have bf16
- * operands and fp32 sums; U and R A^T are carried between them as two bf16
- * words (16 significant bits), G W and all sums in fp32; each result is rounded
- * once.  M == 0 writes zeros to da and db.  Deterministic: the order of every
+ * operands and fp32 sums; U, R A^T, G W and all sums are carried between them
+ * in fp32 (U and R A^T enter their second product as three bf16 words, 24 bits);
+ * each result is rounded once.  M == 0 writes zeros to da and db.  Deterministic: the order of every
  * sum depends on the sizes only.
  */
 rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* codes, const uint8_t* exps,
