@@ -106,27 +106,44 @@ def _same(a, b):
     return a.data_ptr() == b.data_ptr() and a.stride() == b.stride() and a.shape == b.shape
 
 
+def _meets(off, dims, left):
+    """Whether sum(d * s) == off for some integers lo <= d <= hi per (s, lo, hi)
+    of ``dims`` (s > 0, largest first).  With nested strides a level leaves few
+    candidates; past ``left[0]`` of them in all the answer is yes, unproven."""
+    if not dims:
+        return off == 0
+    s, lo, hi = dims[0]
+    low = sum(t * a for t, a, _ in dims[1:])                       # what the smaller strides reach
+    high = sum(t * b for t, _, b in dims[1:])
+    for d in range(max(lo, -((high - off) // s)), min(hi, (off - low) // s) + 1):
+        left[0] -= 1
+        if left[0] < 0 or _meets(off - d * s, dims[1:], left):
+            return True
+    return False
+
+
 def _apart(a, b):
-    """Whether two tensors share no element: disjoint extents, or slices of
-    one tensor side by side along heads."""
+    """Whether two tensors certainly share no element: disjoint extents, or two
+    slices of one tensor (the same strides, any order of the dimensions, any
+    number of heads each) no element of which is at the same place."""
     (al, ah), (bl, bh) = _span(a), _span(b)
     if ah <= bl or bh <= al:
         return True
-    if a.stride() != b.stride() or a.shape[:-2] != b.shape[:-2]:
+    size = a.element_size()
+    off = b.data_ptr() - a.data_ptr()
+    if off % size or a.dim() != b.dim():
         return False
-    if a.data_ptr() > b.data_ptr():
-        a, b = b, a
-    off, size = b.data_ptr() - a.data_ptr(), a.element_size()
-    room = min((s * size for n, s in zip(a.shape[:-2], a.stride()[:-2]) if n > 1), default=None)
-    head = a.stride(-2) * size
-    if head <= 0 or (room is not None and room <= 0):
-        return False
-    first, second = (a.shape[-2] - 1) * head + a.shape[-1] * size, (b.shape[-2] - 1) * head + b.shape[-1] * size
-    if room is None:
-        return off >= first
-    nested = a.dim() < 4 or a.shape[0] <= 1 or a.shape[1] <= 1 or \
-        a.stride(0) * size >= a.stride(1) * size * a.shape[1] or a.stride(1) * size >= a.stride(0) * size * a.shape[0]
-    return nested and off >= first and off + second <= room
+    dims = []
+    for na, nb, sa, sb in zip(a.shape, b.shape, a.stride(), b.stride()):
+        if na > 1 and nb > 1 and sa != sb:
+            return False
+        s = sa if na > 1 else sb
+        if s < 0:
+            return False
+        if s > 0 and (na > 1 or nb > 1):
+            dims.append((s, 1 - nb, na - 1))                       # index in a less index in b
+    dims.sort(reverse=True)
+    return not _meets(off // size, dims, [1000])
 
 
 def _check_out(name, t, o):
