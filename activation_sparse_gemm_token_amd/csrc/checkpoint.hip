@@ -47,7 +47,7 @@ checkpoint_pack_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K, int
                        uint8_t* __restrict__ exps, uint8_t* __restrict__ idx, float* __restrict__ stats) {
   __shared__ float red[kWaves][2];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, part = wv % P;
-  const int64_t row = (int64_t)blockIdx.x * (kWaves / P) + wv / P;
+  const int64_t row = folded_block() * (kWaves / P) + wv / P;
   const bool live = row < M;
   const int64_t units = (K + 7) / 8;                  // = idx bytes of a row
   const uint16_t* xr = x + row * K;
@@ -155,7 +155,7 @@ hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_
   const int64_t fit = 32 * (int64_t)compute_units;
   const int p = 4 * M <= fit && K > 1024 ? 4 : 2 * M <= fit && K > 512 ? 2 : 1;
   const int64_t rows_per = kWaves / p;
-  const dim3 grid((unsigned)((M + rows_per - 1) / rows_per)), block(64 * kWaves);
+  const dim3 grid = folded_grid((M + rows_per - 1) / rows_per), block(64 * kWaves);
   const bool wide = K % 8 == 0;
   auto* k = p == 4   ? (wide ? &checkpoint_pack_kernel<true, 4> : &checkpoint_pack_kernel<false, 4>)
             : p == 2 ? (wide ? &checkpoint_pack_kernel<true, 2> : &checkpoint_pack_kernel<false, 2>)
