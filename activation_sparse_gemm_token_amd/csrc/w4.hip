@@ -139,7 +139,8 @@ w4_short_kernel(const uint16_t* __restrict__ x, const char* __restrict__ packed,
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int tiles_k = (int)((K + 127) / 128), units = tiles_k * 16, real = (int)(K / 8);   // 16-byte units of a row
-  const int64_t nt = blockIdx.x;
+  const int64_t nt = folded_block();
+  if (nt >= (N + 15) / 16) return;
   const u32x4* wp = reinterpret_cast<const u32x4*>(packed) + nt * tiles_k * 64 + lane;
   const MetaT* sp = reinterpret_cast<const MetaT*>(packed + meta_at) + nt * tiles_k * 16 + col;
   // x is requested first, then the weights, all of them whatever they fetch
@@ -218,7 +219,7 @@ w4_rows_kernel(const uint16_t* __restrict__ x, const char* __restrict__ packed, 
   const int col = lane & 15, quad = lane >> 4;
   const int64_t tiles_n = (N + 15) / 16, tiles_k = (K + 127) / 128;
   const int nw = wave / KW, kg = wave % KW;
-  const int64_t nt0 = ((int64_t)blockIdx.x * NW + nw) * NT, m0 = (int64_t)blockIdx.y * kRows;
+  const int64_t nt0 = (folded_block() * NW + nw) * NT, m0 = (int64_t)blockIdx.y * kRows;
   const u32x4* wp[NT];
   const MetaT* sp[NT];
 #pragma unroll
@@ -369,7 +370,7 @@ template <int XR, int NT, int NW, int KW>
 hipError_t launch_rows(const uint16_t* x, const char* packed, int64_t meta_at, int64_t M, int64_t N, int64_t K,
                        int group, bool zeros, uint16_t* y, hipStream_t stream) {
   constexpr int kN = 16 * NT * NW;
-  const dim3 grid((unsigned)((N + kN - 1) / kN), (unsigned)((M + XR - 1) / XR));
+  const dim3 grid = folded_grid((N + kN - 1) / kN, (unsigned)((M + XR - 1) / XR));
   auto* k = group == 128  ? (zeros ? &w4_rows_kernel<XR, NT, NW, KW, 1, true> : &w4_rows_kernel<XR, NT, NW, KW, 1, false>)
             : group == 64 ? (zeros ? &w4_rows_kernel<XR, NT, NW, KW, 2, true> : &w4_rows_kernel<XR, NT, NW, KW, 2, false>)
                           : (zeros ? &w4_rows_kernel<XR, NT, NW, KW, 4, true> : &w4_rows_kernel<XR, NT, NW, KW, 4, false>);
@@ -387,7 +388,7 @@ hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, in
     auto* k = group == 128  ? (zeros ? &w4_short_kernel<1, true> : &w4_short_kernel<1, false>)
               : group == 64 ? (zeros ? &w4_short_kernel<2, true> : &w4_short_kernel<2, false>)
                             : (zeros ? &w4_short_kernel<4, true> : &w4_short_kernel<4, false>);
-    return launch(k, dim3((unsigned)tiles_n), dim3(64 * kShortWaves), stream, x, p, meta_at, M, N, K, y);
+    return launch(k, folded_grid(tiles_n), dim3(64 * kShortWaves), stream, x, p, meta_at, M, N, K, y);
   }
   // Weight rows per workgroup: as few as give each CU one workgroup, with all
   // wavefronts along the channels; more once there are enough, which reads x

@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from activation_sparse_gemm_token_amd import training  # noqa: E402
+from activation_sparse_gemm_token_amd import training, w4  # noqa: E402
 
 DEV = "cuda:0"
 
@@ -34,3 +34,23 @@ def test_checkpoint_of_the_most_tokens(m, k):
              "positions": (kept.idx[:, 0] & 15) == 0 + (2 << 2), "values": kept.unpack() == x}
     wrong = [n for n, ok in right.items() if not bool(ok.all())]   # names only: a failure prints no tensor of this size
     assert wrong == []
+
+
+@pytest.mark.parametrize("m,n", [(1, (1 << 28) + 17), (17, (1 << 29) + 33)])
+def test_4_bit_weight_of_the_most_rows(m, n):
+    """The same of w4.linear: short channels, and the form for more rows."""
+    say(m, n)
+    g = torch.Generator(device=DEV).manual_seed(m)
+    k = 32
+    x = torch.randint(-3, 4, (m, k), generator=g, device=DEV).bfloat16()
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    scales = torch.randint(1, 5, (n, 1), generator=g, device=DEV).bfloat16() / 4
+    y = w4.linear(x, w4.pack(codes, scales, group=32))
+    step = 1 << 22
+    wrong = 0
+    for lo in list(range(0, n, 17 * step)) + [n - step]:           # parts of it, its end among them
+        part = codes[lo:lo + step]
+        q = torch.stack([part & 15, part >> 4], -1).flatten(1).float() - 8
+        want = (x.float() @ q.t()) * scales[lo:lo + step, 0].float()    # whole quarters: exact in fp32
+        wrong += int((y[:, lo:lo + step] != want.bfloat16()).sum())
+    assert wrong == 0
