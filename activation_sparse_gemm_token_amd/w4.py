@@ -34,9 +34,15 @@ def packed_bytes(n: int, k: int, group: int, zeros: bool = False) -> int:
 
 
 class Weight:
-    """A weight [n, k] laid out by ``pack``."""
+    """A weight [n, k] laid out by ``pack``: contiguous uint8 bytes on the device
+    (one read back from a file is put together here; its size is checked by the
+    library)."""
 
     def __init__(self, packed, n: int, k: int, group: int, zeros: bool):
+        if packed.dtype != _torch().uint8:
+            raise TypeError(f"packed must be uint8, got {packed.dtype}")
+        if not packed.is_cuda or not packed.is_contiguous():
+            raise ValueError("packed must be a contiguous device tensor")
         self.packed, self.n, self.k, self.group, self.zeros = packed, n, k, group, zeros
 
 
