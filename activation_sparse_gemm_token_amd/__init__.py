@@ -177,6 +177,15 @@ def _out(out, m: int, n: int, lead, device):
     return out
 
 
+def _separate(out, **tensors):
+    """Refuses a caller's output that overlaps an input (both contiguous)."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for name, t in tensors.items():
+        at = t.data_ptr()
+        if at < hi and lo < at + t.numel() * t.element_size():
+            raise ValueError(f"out overlaps {name}")
+
+
 def _workspace(workspace, need: int, device):
     """A caller's workspace, or a new one: contiguous uint8 bytes on the
     inputs' device (its size is checked by the library)."""

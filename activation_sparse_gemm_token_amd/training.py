@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _as_2d, _check, _here, _on, _out, _stream, _torch, _workspace, lib
+from . import _as_2d, _check, _here, _on, _out, _separate, _stream, _torch, _workspace, lib
 
 __all__ = ["Checkpoint", "checkpoint", "unpack", "sparse_linear_backward", "backward_workspace_bytes"]
 
@@ -118,6 +118,8 @@ def unpack(codes, exps, out=None):
         raise ValueError("codes and exps must be contiguous device tensors")
     m, k = codes.shape
     y = _out(out, m, k, (m,), codes.device)
+    if out is not None:
+        _separate(out, codes=codes, exps=exps)
     _run("rtl_checkpoint_unpack", (codes.data_ptr(), exps.data_ptr(), m, k, y.data_ptr()), codes, exps=exps)
     return y
 

@@ -6,7 +6,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _as_2d, _check, _here, _on, _out, _stream, _torch, lib
+from . import _as_2d, _check, _here, _on, _out, _separate, _stream, _torch, lib
 
 __all__ = ["Weight", "pack", "linear", "packed_bytes", "GROUPS", "MAX_ROWS"]
 
@@ -78,13 +78,16 @@ def pack(codes, scales, zeros=None, group: int = 128) -> Weight:
 
 def linear(x, weight: Weight, out=None):
     """y [..., n] bf16 = x [..., k] bf16 times the weight: made for 1 to 64
-    rows, accepts up to ``MAX_ROWS``.  x must be finite."""
+    rows, accepts up to ``MAX_ROWS``.  x must be finite; ``out`` shares no memory
+    with it."""
     x2 = _as_2d(x, "x")
     m, k = x2.shape
     if k != weight.k:
         raise ValueError(f"the weight has {weight.k} input channels, x has {k}")
     y = x2.new_empty((*x.shape[:-1], weight.n)) if out is None else _out(out, m, weight.n, x.shape[:-1], x2.device)
     packed = weight.packed
+    if out is not None:
+        _separate(out, x=x2, weight=packed)
     args = (x2.data_ptr(), packed.data_ptr(), packed.numel(), m, weight.n, k, weight.group,
             _ZEROS if weight.zeros else 0, y.data_ptr())
     stream = _here(x2, packed)
