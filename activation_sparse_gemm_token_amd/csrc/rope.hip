@@ -74,7 +74,8 @@ rope_kernel(RopeArgs a) {
   using P = Pack<raw, V>;
   extern __shared__ float table[];                 // [token][cos pairs, sin pairs]
   const int pairs = a.rot / 2;
-  const int64_t tok0 = (int64_t)blockIdx.x * a.group;
+  const int64_t tok0 = folded_block() * a.group;
+  if (tok0 >= a.total) return;
   const int ntok = (int)(a.total - tok0 < a.group ? a.total - tok0 : a.group);
   const int64_t b0 = tok0 / a.tokens, t0 = tok0 - b0 * a.tokens;
   // Batch and position of local token t: the group's tokens are consecutive.
@@ -250,8 +251,7 @@ hipError_t launch_rope(RopeArgs a, int elem_bytes, bool fp16, bool inter, int co
     const int64_t most = (all + kThreads - 1) / kThreads;
     if (split > most) split = most;
   }
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks, (unsigned)split);
+  const dim3 grid = folded_grid(blocks, (unsigned)split);
   const size_t lds = (size_t)group * 2 * pairs * sizeof(float);
   if (elem_bytes == 4) {
     if (vec >= 4) return launch_v<Fp32, 4>(a, inter, grid, lds, stream);

@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from activation_sparse_gemm_token_amd import training, w4  # noqa: E402
+from activation_sparse_gemm_token_amd import rotary, training, w4  # noqa: E402
 
 DEV = "cuda:0"
 
@@ -54,3 +54,26 @@ def test_4_bit_weight_of_the_most_rows(m, n):
         want = (x.float() @ q.t()) * scales[lo:lo + step, 0].float()    # whole quarters: exact in fp32
         wrong += int((y[:, lo:lo + step] != want.bfloat16()).sum())
     assert wrong == 0
+
+
+def test_rotary_of_more_workgroups_than_a_launch_dimension():
+    """2^26 tokens of 1024 channels (137 GB), four to a workgroup, in place."""
+    t, d, first = (1 << 26) + 6, 1024, 1 << 20
+    if torch.cuda.mem_get_info()[0] < (150 << 30):
+        pytest.skip("needs 150 GB of free device memory")
+    x = torch.empty(t, 1, d, dtype=torch.bfloat16, device=DEV)
+    x[:first] = torch.randn(first, 1, d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).bfloat16()
+    for lo in range(first, t, first):                              # the same rows again and again
+        x[lo:lo + first] = x[:min(first, t - lo)]
+    pos = torch.arange(t, device=DEV) % 1021
+    f = rotary.frequencies(d).to(DEV)
+    head = x[:first].clone()
+    rotary.rope(x, pos, f, out=x)
+    bad = 0
+    for lo in [0, first, 31 * first, (1 << 24) * 4 - 4 - first, t // first * first]:
+        n = min(first, t - lo)
+        row = torch.arange(lo, lo + n, device=DEV) % first
+        bad += int((x[lo:lo + n] != rotary.rope(head[row], pos[lo:lo + n].contiguous(), f)).sum())
+    del x
+    torch.cuda.empty_cache()
+    assert bad == 0
