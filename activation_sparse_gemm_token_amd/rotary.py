@@ -66,8 +66,8 @@ def frequencies_by_parts(rot_dim: int, factor: float, trained_length: int, base:
     between the two the share moves linearly with the pair's index.
     Returns (float64 host tensor, scale = 0.1 ln(factor) + 1)."""
     torch = _torch()
-    if factor < 1 or trained_length < 1 or not fast_turns > slow_turns > 0:
-        raise ValueError("need factor >= 1, trained_length >= 1 and fast_turns > slow_turns > 0")
+    if not factor >= 1 or trained_length < 1 or not fast_turns > slow_turns > 0 or not base > 1:
+        raise ValueError("need factor >= 1, trained_length >= 1, fast_turns > slow_turns > 0 and base > 1")
     f = frequencies(rot_dim, base)
 
     def index(turns):                        # pair that turns so often over the trained length
