@@ -139,6 +139,15 @@ RTL_API size_t rtl_sparse_linear_backward_workspace_bytes(int64_t M, int64_t N, 
   return rtl::backward_layout(M, N, K, r).total;
 }
 
+RTL_API rtl_status rtl_sparse_linear_backward_form(int64_t M, int64_t N, int64_t K, int64_t r, int64_t form[6]) {
+  if (form == nullptr) return RTL_ERR_NULL_POINTER;
+  if (!back_ok(M, N, K, r)) return RTL_ERR_BAD_SHAPE;
+  const rtl::BackwardLayout L = rtl::backward_layout(M, N, K, r);
+  const int64_t f[6] = {L.p_tile, L.p_splits, L.p_length, L.chunk_g, L.chunk_x, L.chunk_t};
+  for (int i = 0; i < 6; ++i) form[i] = f[i];
+  return RTL_OK;
+}
+
 RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* codes, const uint8_t* exps,
                                               const uint8_t* idx, const float* stats, const uint16_t* w_t,
                                               const uint16_t* lora_a, const uint16_t* lora_b, int64_t M, int64_t N,

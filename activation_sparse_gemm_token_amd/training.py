@@ -13,13 +13,15 @@ import ctypes
 
 from . import _as_2d, _check, _here, _on, _out, _separate, _stream, _torch, _workspace, lib
 
-__all__ = ["Checkpoint", "checkpoint", "unpack", "sparse_linear_backward", "backward_workspace_bytes"]
+__all__ = ["Checkpoint", "checkpoint", "unpack", "sparse_linear_backward", "backward_workspace_bytes",
+           "backward_form"]
 
 _c_i64, _c_vp, _c_size, _c_int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _SIGNATURES = {
     "rtl_checkpoint_pack": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "rtl_checkpoint_unpack": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
     "rtl_sparse_linear_backward_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "rtl_sparse_linear_backward_form": (_c_int, [_c_i64] * 4 + [ctypes.POINTER(_c_i64)]),
     "rtl_sparse_linear_backward": (_c_int, [_c_vp] * 8 + [_c_i64] * 4 + [ctypes.c_float] + [_c_vp] * 4 +
                                    [_c_size, _c_vp]),
 }
@@ -126,6 +128,15 @@ def unpack(codes, exps, out=None):
 
 def backward_workspace_bytes(m: int, n: int, k: int, r: int) -> int:
     return int(_fn("rtl_sparse_linear_backward_workspace_bytes")(m, n, k, r))
+
+
+def backward_form(m: int, n: int, k: int, r: int):
+    """Which kernels ``sparse_linear_backward`` takes at these sizes: (tile columns
+    of G W, its ranges, its row length, channels per range over n and over k,
+    tokens per range)."""
+    form = (_c_i64 * 6)()
+    _check(_fn("rtl_sparse_linear_backward_form")(m, n, k, r, form), "rtl_sparse_linear_backward_form")
+    return tuple(form)
 
 
 def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, lora_scale: float = 1.0,

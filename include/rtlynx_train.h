@@ -56,6 +56,20 @@ rtl_status rtl_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64
 size_t rtl_sparse_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 
 /*
+ * rtl_sparse_linear_backward_form - which kernels a call of these sizes takes, for
+ * tests and for reading profiles (host only; the form depends on the sizes alone):
+ *
+ *   form[0]  tile columns of G W: 256 or 192, or 64 for the form of few tokens.
+ *   form[1]  ranges of its contraction over N.
+ *   form[2]  length of G's rows there: N, or N + 4 for padded copies.
+ *   form[3], form[4]  channels of a range of G B, and of the checkpoint by A^T.
+ *   form[5]  tokens of a range of the products over tokens.
+ *
+ * RTL_ERR_BAD_SHAPE for the sizes that rtl_sparse_linear_backward refuses.
+ */
+rtl_status rtl_sparse_linear_backward_form(int64_t M, int64_t N, int64_t K, int64_t r, int64_t form[6]);
+
+/*
  * rtl_sparse_linear_backward - gradients of the layer from G = dL / dY.
  *
  * With X, M, s, Lk = L1 of the kept channels as the checkpoint holds them:
