@@ -30,7 +30,8 @@ extern "C" {
 /*
  * rtl_checkpoint_pack - the input of a sparse layer in 8 bits.
  *
- *   x      [M, K] bf16, finite.
+ *   x      [M, K] bf16, finite, a token's L1 norm within fp32's range (past it s is
+ *          NaN, as the layer's is).
  *   codes  [M, K] int8 and exps [M, ceil(K / 32)] uint8: x is stored as
  *          code * 2^(exp - 133), exp the biased exponent of the block's
  *          largest magnitude (so the largest code is 64 .. 127) and code the
