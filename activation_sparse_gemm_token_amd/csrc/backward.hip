@@ -90,26 +90,23 @@ __device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t t, uint32_t row, i
 // 8 channels of the checkpoint at channel c, raw, then pruned and kept values.
 struct CkptRaw {
   u32x2 q;
-  uint32_t e, idx;
+  uint32_t e, p, idx;                                   // p: the pruned channels' exponent
 };
 template <bool WIDE>
 __device__ __forceinline__ CkptRaw ckpt_load8(const CkptRsrc& k, const CkptRow& r, int c, int K) {
   CkptRaw f;
   f.q = buf_load8(k.codes, c < K ? r.codes + c : kOobOffset);
   f.e = __builtin_amdgcn_raw_buffer_load_b8(k.exps, c < K ? r.exps + c / 32 : kOobOffset, 0, 0);
+  f.p = __builtin_amdgcn_raw_buffer_load_b8(k.pruned_exps, c < K ? r.exps + c / 32 : kOobOffset, 0, 0);
   f.idx = __builtin_amdgcn_raw_buffer_load_b8(k.idx, c < K ? r.idx + c / 8 : kOobOffset, 0, 0);
   return f;
 }
 __device__ __forceinline__ void ckpt_split(const CkptRaw& r, u32x4& pruned, u32x4& kept) {
-  const u32x4 v = ckpt_values(r.q, (int)r.e), m = kept_masks(r.idx);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    kept[i] = v[i] & m[i];
-    pruned[i] = v[i] & ~m[i];
-  }
+  ckpt_split8(r.q, r.e, r.p, r.idx, pruned, kept);
 }
 __device__ __forceinline__ void ckpt_split(const Ckpt16& r, int half, u32x4& pruned, u32x4& kept) {
-  ckpt_split(CkptRaw{{r.codes[2 * half], r.codes[2 * half + 1]}, r.exp, half ? r.idx1 : r.idx0}, pruned, kept);
+  const u32x2 q = {r.codes[2 * half], r.codes[2 * half + 1]};
+  ckpt_split8(q, r.exp, r.pruned_exp, half ? r.idx1 : r.idx0, pruned, kept);
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -253,7 +250,7 @@ __device__ __forceinline__ void x_rows(const Ckpt& ck, const u32x4* __restrict__
   f32x4 acc[2 * MT * JT];                               // pruned, kept
 #pragma unroll
   for (int i = 0; i < 2 * MT * JT; ++i) acc[i] = kZero4;
-  const CkptRsrc kr = ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K);
+  const CkptRsrc kr = ckpt_rsrc(ck, L.M, L.K);
   const int K = (int)L.K;
   CkptRow row[MT];
 #pragma unroll
@@ -449,6 +446,7 @@ __device__ __forceinline__ void col_step(const uint16_t* tile, const u32x4 (&w)[
     for (int n = 0; n < 3; ++n)
 #pragma unroll
       for (int i = 0; i < CT; ++i) acc[i * JT + j] = mfma(x[i], s.w[n], acc[i * JT + j]);
+    if constexpr (JT == 8) __builtin_amdgcn_sched_barrier(0);   // one split at a time: no registers for more
   }
 }
 
@@ -522,7 +520,7 @@ __device__ __forceinline__ void x_columns(const Ckpt& ck, const u32x4* __restric
   for (int i = 0; i < CT * JT; ++i) acc[i] = kZero4;
   CkptRaw v[T::kLoads];
   u32x4 w[2 * JT];
-  const CkptRsrc kr = ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K);
+  const CkptRsrc kr = ckpt_rsrc(ck, L.M, L.K);
   auto load = [&](int64_t at) {
     const int64_t t = at < hi ? at : hi - 32;
 #pragma unroll
@@ -685,7 +683,7 @@ few_tokens_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ w
     use(s0);
   }
   const int64_t row = m0 + 16 * wave + col;             // this wavefront's tokens from here on
-  Ckpt16 f = ckpt_load16(ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K), ckpt_row(row, L.K), (int)(64 * tn) + 16 * quad,
+  Ckpt16 f = ckpt_load16(ckpt_rsrc(ck, L.M, L.K), ckpt_row(row, L.K), (int)(64 * tn) + 16 * quad,
                          (int)L.K);
 #pragma unroll
   for (int i = 0; i < 16; ++i) lds[(wave * 16 + i) * 64 + lane] = acc[i];
@@ -750,7 +748,7 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
   const int64_t b0 = 2 * (blockIdx.x % groups);
   const int64_t lo = blockIdx.x / groups * chunk, hi = lo + chunk < steps ? lo + chunk : steps;
   float s[2], lk[2];
-  const CkptRsrc kr = ckpt_rsrc(ck.codes, ck.exps, ck.idx, L.M, L.K);
+  const CkptRsrc kr = ckpt_rsrc(ck, L.M, L.K);
   const int K = (int)L.K;
   CkptRow rows[2];
   const f32x4* pr[2];

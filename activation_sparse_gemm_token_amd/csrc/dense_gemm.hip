@@ -282,7 +282,7 @@ dense_gemm_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     constexpr int kGroups = kCB / 4 + (kCB % 4 != 0);
     // All of the checkpoint's loads go out first, then P's stores, so the sums
     // wait for neither.
-    const CkptRsrc ck = ckpt_rsrc(y.ck.codes, y.ck.exps, y.ck.idx, M, N);
+    const CkptRsrc ck = ckpt_rsrc(y.ck, M, N);
     Ckpt16 f[kRB][kGroups];
 #pragma unroll
     for (int rb = 0; rb < kRB; ++rb) {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "rtl_common.hpp"
+#include "rtl_operators.hpp"
 
 namespace rtl {
 
@@ -44,16 +45,29 @@ __device__ __forceinline__ u32x4 kept_masks(uint32_t byte) {
   return m;
 }
 
+// 8 codes with exponents e (kept channels) and p (pruned), idx byte `byte`, as the
+// kept values and the pruned ones, each zero at the other's channels.
+__device__ __forceinline__ void ckpt_split8(u32x2 q, uint32_t e, uint32_t p, uint32_t byte, u32x4& pruned, u32x4& kept) {
+  const u32x4 m = kept_masks(byte);
+  kept = ckpt_values(q, (int)e);
+  pruned = ckpt_values(q, (int)p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    kept[i] &= m[i];
+    pruned[i] &= ~m[i];
+  }
+}
+
 // The checkpoint through buffer resources: a load past the tensors or at
 // kOobOffset gives zeros and needs no branch, so none is ever under a condition
 // (a conditional load makes the compiler wait for every load in flight where it
 // waits for one).  All of it is below 2 GiB: 32-bit offsets.
 struct CkptRsrc {
-  __amdgpu_buffer_rsrc_t codes, exps, idx;
+  __amdgpu_buffer_rsrc_t codes, exps, pruned_exps, idx;
 };
-__device__ __forceinline__ CkptRsrc ckpt_rsrc(const int8_t* codes, const uint8_t* exps, const uint8_t* idx, int64_t M,
-                                              int64_t K) {
-  return {make_rsrc(codes, M * K), make_rsrc(exps, M * ((K + 31) / 32)), make_rsrc(idx, M * ((K + 7) / 8))};
+__device__ __forceinline__ CkptRsrc ckpt_rsrc(const Ckpt& c, int64_t M, int64_t K) {
+  return {make_rsrc(c.codes, M * K), make_rsrc(c.exps, M * ((K + 31) / 32)),
+          make_rsrc(c.pruned_exps, M * ((K + 31) / 32)), make_rsrc(c.idx, M * ((K + 7) / 8))};
 }
 // A token's offsets in the three; a token past M gives zeros.
 struct CkptRow {
@@ -67,12 +81,13 @@ __device__ __forceinline__ CkptRow ckpt_row(int64_t row, int64_t K) {
 // Channels past K have code 0.
 struct Ckpt16 {
   u32x4 codes;
-  uint32_t exp, idx0, idx1;               // idx: 4 bits per group, two groups each
+  uint32_t exp, pruned_exp, idx0, idx1;   // idx: 4 bits per group, two groups each
 };
 __device__ __forceinline__ Ckpt16 ckpt_load16(const CkptRsrc& c, const CkptRow& r, int k, int K) {
   Ckpt16 f;
   f.codes = buf_load16(c.codes, k < K ? r.codes + k : kOobOffset);
   f.exp = __builtin_amdgcn_raw_buffer_load_b8(c.exps, k < K ? r.exps + k / 32 : kOobOffset, 0, 0);
+  f.pruned_exp = __builtin_amdgcn_raw_buffer_load_b8(c.pruned_exps, k < K ? r.exps + k / 32 : kOobOffset, 0, 0);
   f.idx0 = __builtin_amdgcn_raw_buffer_load_b8(c.idx, k < K ? r.idx + k / 8 : kOobOffset, 0, 0);
   f.idx1 = __builtin_amdgcn_raw_buffer_load_b8(c.idx, k + 8 < K ? r.idx + k / 8 + 1 : kOobOffset, 0, 0);
   return f;

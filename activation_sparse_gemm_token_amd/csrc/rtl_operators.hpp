@@ -42,14 +42,17 @@ hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, in
 // 8-bit activation checkpoint (include/rtlynx_train.h).
 struct Ckpt {
   const int8_t* codes;
-  const uint8_t* exps;
+  const uint8_t* exps;                   // of the kept channels
+  const uint8_t* pruned_exps;            // exps itself where both share one
   const uint8_t* idx;
   const float* stats;
 };
+// pruned_exps: NULL for one exponent per block.
 hipError_t launch_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
-                                  uint8_t* idx, float* stats, int compute_units, hipStream_t stream);
-hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K,
-                                    uint16_t* y, hipStream_t stream);
+                                  uint8_t* pruned_exps, uint8_t* idx, float* stats, int compute_units,
+                                  hipStream_t stream);
+hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, const uint8_t* pruned_exps,
+                                    const uint8_t* idx, int64_t M, int64_t K, uint16_t* y, hipStream_t stream);
 
 // Sizes, splits and workspace regions of the layer's backward pass.  Rank is
 // padded to 32, 64 or 128, channels and tokens to 64 (zeros).  Operands of the

@@ -106,32 +106,62 @@ rtl::BackwardLayout rtl::backward_layout(int64_t M, int64_t N, int64_t K, int64_
   return L;
 }
 
-RTL_API rtl_status rtl_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
-                                       uint8_t* idx, float* stats, void* hip_stream) {
+namespace {
+
+// pruned_exps: NULL for one exponent per block (`fine` says which is meant).
+rtl_status pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps, uint8_t* pruned_exps,
+                uint8_t* idx, float* stats, bool fine, void* hip_stream) {
   if (!act_ok(M, K)) return RTL_ERR_BAD_SHAPE;
   if (M == 0) return RTL_OK;
-  if (x == nullptr || codes == nullptr || exps == nullptr || idx == nullptr || stats == nullptr)
+  if (x == nullptr || codes == nullptr || exps == nullptr || idx == nullptr || stats == nullptr ||
+      (fine && pruned_exps == nullptr))
     return RTL_ERR_NULL_POINTER;
   if (!rtl::aligned(x, 16) || !rtl::aligned(codes, 16) || !rtl::aligned(exps, 16) || !rtl::aligned(idx, 16) ||
-      !rtl::aligned(stats, 16))
+      !rtl::aligned(stats, 16) || !rtl::aligned(pruned_exps, 16))
     return RTL_ERR_MISALIGNED;
   int cus = 0;
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const rtl_status d = rtl::check_device(stream, &cus);
   if (d != RTL_OK) return d;
-  return rtl::from_hip(rtl::launch_checkpoint_pack(x, M, K, codes, exps, idx, stats, cus, stream));
+  return rtl::from_hip(rtl::launch_checkpoint_pack(x, M, K, codes, exps, pruned_exps, idx, stats, cus, stream));
+}
+
+// pruned_exps and idx: NULL for one exponent per block.
+rtl_status unpack(const int8_t* codes, const uint8_t* exps, const uint8_t* pruned_exps, const uint8_t* idx, int64_t M,
+                  int64_t K, uint16_t* y, bool fine, void* hip_stream) {
+  if (!act_ok(M, K)) return RTL_ERR_BAD_SHAPE;
+  if (M == 0) return RTL_OK;
+  if (codes == nullptr || exps == nullptr || y == nullptr || (fine && (pruned_exps == nullptr || idx == nullptr)))
+    return RTL_ERR_NULL_POINTER;
+  if (!rtl::aligned(codes, 16) || !rtl::aligned(exps, 16) || !rtl::aligned(y, 16) || !rtl::aligned(pruned_exps, 16) ||
+      !rtl::aligned(idx, 16))
+    return RTL_ERR_MISALIGNED;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  const rtl_status d = rtl::check_device(stream);
+  if (d != RTL_OK) return d;
+  return rtl::from_hip(rtl::launch_checkpoint_unpack(codes, exps, pruned_exps, idx, M, K, y, stream));
+}
+
+}  // namespace
+
+RTL_API rtl_status rtl_checkpoint_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
+                                       uint8_t* idx, float* stats, void* hip_stream) {
+  return pack(x, M, K, codes, exps, nullptr, idx, stats, false, hip_stream);
+}
+
+RTL_API rtl_status rtl_checkpoint_pack_fine(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
+                                            uint8_t* pruned_exps, uint8_t* idx, float* stats, void* hip_stream) {
+  return pack(x, M, K, codes, exps, pruned_exps, idx, stats, true, hip_stream);
 }
 
 RTL_API rtl_status rtl_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K, uint16_t* y,
                                          void* hip_stream) {
-  if (!act_ok(M, K)) return RTL_ERR_BAD_SHAPE;
-  if (M == 0) return RTL_OK;
-  if (codes == nullptr || exps == nullptr || y == nullptr) return RTL_ERR_NULL_POINTER;
-  if (!rtl::aligned(codes, 16) || !rtl::aligned(exps, 16) || !rtl::aligned(y, 16)) return RTL_ERR_MISALIGNED;
-  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  const rtl_status d = rtl::check_device(stream);
-  if (d != RTL_OK) return d;
-  return rtl::from_hip(rtl::launch_checkpoint_unpack(codes, exps, M, K, y, stream));
+  return unpack(codes, exps, nullptr, nullptr, M, K, y, false, hip_stream);
+}
+
+RTL_API rtl_status rtl_checkpoint_unpack_fine(const int8_t* codes, const uint8_t* exps, const uint8_t* pruned_exps,
+                                              const uint8_t* idx, int64_t M, int64_t K, uint16_t* y, void* hip_stream) {
+  return unpack(codes, exps, pruned_exps, idx, M, K, y, true, hip_stream);
 }
 
 RTL_API size_t rtl_sparse_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
@@ -148,12 +178,11 @@ RTL_API rtl_status rtl_sparse_linear_backward_form(int64_t M, int64_t N, int64_t
   return RTL_OK;
 }
 
-RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* codes, const uint8_t* exps,
-                                              const uint8_t* idx, const float* stats, const uint16_t* w_t,
-                                              const uint16_t* lora_a, const uint16_t* lora_b, int64_t M, int64_t N,
-                                              int64_t K, int64_t r, float lora_scale, uint16_t* dx, uint16_t* da,
-                                              uint16_t* db, void* workspace, size_t workspace_bytes,
-                                              void* hip_stream) {
+namespace {
+
+rtl_status backward(const uint16_t* g, const rtl::Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
+                    const uint16_t* lora_b, int64_t M, int64_t N, int64_t K, int64_t r, float lora_scale, uint16_t* dx,
+                    uint16_t* da, uint16_t* db, void* workspace, size_t workspace_bytes, void* hip_stream) {
   if (!back_ok(M, N, K, r)) return RTL_ERR_BAD_SHAPE;
   if ((da == nullptr) != (db == nullptr)) return RTL_ERR_NULL_POINTER;
   if (r == 0 && da != nullptr) return RTL_ERR_BAD_SHAPE;
@@ -163,11 +192,12 @@ RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* c
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const rtl::BackwardLayout L = rtl::backward_layout(M, N, K, r);
   if (M > 0) {
-    if (g == nullptr || codes == nullptr || exps == nullptr || idx == nullptr || stats == nullptr ||
+    if (g == nullptr || ck.codes == nullptr || ck.exps == nullptr || ck.pruned_exps == nullptr || ck.idx == nullptr ||
+        ck.stats == nullptr ||
         (dx != nullptr && w_t == nullptr) || (r > 0 && (lora_a == nullptr || lora_b == nullptr)))
       return RTL_ERR_NULL_POINTER;
-    if (!rtl::aligned(g, 16) || !rtl::aligned(codes, 16) || !rtl::aligned(exps, 16) || !rtl::aligned(idx, 16) ||
-        !rtl::aligned(stats, 16) || (dx != nullptr && !rtl::aligned(w_t, 16)) ||
+    if (!rtl::aligned(g, 16) || !rtl::aligned(ck.codes, 16) || !rtl::aligned(ck.exps, 16) ||
+        !rtl::aligned(ck.pruned_exps, 16) || !rtl::aligned(ck.idx, 16) || !rtl::aligned(ck.stats, 16) || (dx != nullptr && !rtl::aligned(w_t, 16)) ||
         (r > 0 && (!rtl::aligned(lora_a, 16) || !rtl::aligned(lora_b, 16))))
       return RTL_ERR_MISALIGNED;
     if (workspace == nullptr || workspace_bytes < L.total) return RTL_ERR_WORKSPACE;
@@ -175,7 +205,28 @@ RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* c
   }
   const rtl_status d = rtl::check_device(stream);
   if (d != RTL_OK) return d;
-  const rtl::Ckpt ck{codes, exps, idx, stats};
   return rtl::from_hip(rtl::launch_backward(g, ck, w_t, lora_a, lora_b, L, lora_scale, dx, da, db,
                                             static_cast<char*>(workspace), stream));
+}
+
+}  // namespace
+
+RTL_API rtl_status rtl_sparse_linear_backward(const uint16_t* g, const int8_t* codes, const uint8_t* exps,
+                                              const uint8_t* idx, const float* stats, const uint16_t* w_t,
+                                              const uint16_t* lora_a, const uint16_t* lora_b, int64_t M, int64_t N,
+                                              int64_t K, int64_t r, float lora_scale, uint16_t* dx, uint16_t* da,
+                                              uint16_t* db, void* workspace, size_t workspace_bytes,
+                                              void* hip_stream) {
+  return backward(g, {codes, exps, exps, idx, stats}, w_t, lora_a, lora_b, M, N, K, r, lora_scale, dx, da, db, workspace,
+                  workspace_bytes, hip_stream);
+}
+
+RTL_API rtl_status rtl_sparse_linear_backward_fine(const uint16_t* g, const int8_t* codes, const uint8_t* exps,
+                                                   const uint8_t* pruned_exps, const uint8_t* idx, const float* stats,
+                                                   const uint16_t* w_t, const uint16_t* lora_a, const uint16_t* lora_b,
+                                                   int64_t M, int64_t N, int64_t K, int64_t r, float lora_scale,
+                                                   uint16_t* dx, uint16_t* da, uint16_t* db, void* workspace,
+                                                   size_t workspace_bytes, void* hip_stream) {
+  return backward(g, {codes, exps, pruned_exps, idx, stats}, w_t, lora_a, lora_b, M, N, K, r, lora_scale, dx, da, db,
+                  workspace, workspace_bytes, hip_stream);
 }

@@ -2,7 +2,7 @@
 layer's input kept in 8 bits, and the backward pass that reads it.
 
     y    = sparse_linear(x, w, a, b, alpha)         # forward
-    kept = training.checkpoint(x)                   # instead of keeping x
+    kept = training.checkpoint(x, fine=True)        # instead of keeping x
     dx, da, db = training.sparse_linear_backward(dy, kept, w_t, a, b, alpha)
 
 Argument marshalling only, as in the package's other bindings.
@@ -19,11 +19,15 @@ __all__ = ["Checkpoint", "checkpoint", "unpack", "sparse_linear_backward", "back
 _c_i64, _c_vp, _c_size, _c_int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _SIGNATURES = {
     "rtl_checkpoint_pack": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "rtl_checkpoint_pack_fine": (_c_int, [_c_vp, _c_i64, _c_i64] + [_c_vp] * 6),
     "rtl_checkpoint_unpack": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
+    "rtl_checkpoint_unpack_fine": (_c_int, [_c_vp] * 4 + [_c_i64, _c_i64, _c_vp, _c_vp]),
     "rtl_sparse_linear_backward_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64]),
     "rtl_sparse_linear_backward_form": (_c_int, [_c_i64] * 4 + [ctypes.POINTER(_c_i64)]),
     "rtl_sparse_linear_backward": (_c_int, [_c_vp] * 8 + [_c_i64] * 4 + [ctypes.c_float] + [_c_vp] * 4 +
                                    [_c_size, _c_vp]),
+    "rtl_sparse_linear_backward_fine": (_c_int, [_c_vp] * 9 + [_c_i64] * 4 + [ctypes.c_float] + [_c_vp] * 4 +
+                                        [_c_size, _c_vp]),
 }
 
 
@@ -51,9 +55,10 @@ class Checkpoint:
     2^(``exps`` - 133) per 32 channels (uint8 [m, ceil(k / 32)]), the kept
     channels ``idx`` uint8 [m, ceil(k / 8)] and ``stats`` fp32 [m, 2] (the
     token's scale, the L1 norm of its kept channels).  ``lead`` is the shape of
-    x without its channels."""
+    x without its channels.  With ``pruned_exps``, shaped like ``exps``, the pruned
+    channels' codes count steps of 2^(``pruned_exps`` - 133)."""
 
-    def __init__(self, codes, exps, idx, stats, lead=None):
+    def __init__(self, codes, exps, idx, stats, lead=None, pruned_exps=None):
         torch = _torch()
         if codes.dim() != 2:
             raise ValueError("codes must be [m, k]")
@@ -63,7 +68,10 @@ class Checkpoint:
         for name, t, dtype, shape in (("codes", codes, torch.int8, (m, k)),
                                       ("exps", exps, torch.uint8, (m, (k + 31) // 32)),
                                       ("idx", idx, torch.uint8, (m, (k + 7) // 8)),
-                                      ("stats", stats, torch.float32, (m, 2))):
+                                      ("stats", stats, torch.float32, (m, 2)),
+                                      ("pruned_exps", pruned_exps, torch.uint8, (m, (k + 31) // 32))):
+            if t is None and name == "pruned_exps":
+                continue
             if t.dtype != dtype:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             if tuple(t.shape) != shape:
@@ -72,31 +80,45 @@ class Checkpoint:
                 raise ValueError(f"{name} must be a contiguous device tensor")
             if t.device != codes.device:
                 raise ValueError(f"{name} is on {t.device}, codes on {codes.device}")
-        self._set(codes, exps, idx, stats, (m,) if lead is None else tuple(lead))
+        self._set(codes, exps, idx, stats, (m,) if lead is None else tuple(lead), pruned_exps)
 
-    def _set(self, codes, exps, idx, stats, lead):
+    def _set(self, codes, exps, idx, stats, lead, pruned_exps):
         self.codes, self.exps, self.idx, self.stats, self.lead = codes, exps, idx, stats, lead
+        self.pruned_exps = pruned_exps
         self.m, self.k = codes.shape
 
     @classmethod
-    def _made(cls, codes, exps, idx, stats, lead):
+    def _made(cls, codes, exps, idx, stats, lead, pruned_exps):
         """A checkpoint of tensors that ``checkpoint`` made: nothing to check."""
         kept = cls.__new__(cls)
-        kept._set(codes, exps, idx, stats, tuple(lead))
+        kept._set(codes, exps, idx, stats, tuple(lead), pruned_exps)
         return kept
 
     def unpack(self, out=None):
         """The stored values [*lead, k] in bf16 (exact)."""
         codes = self.codes
         if out is not None:
-            return unpack(codes, self.exps, out=out).view(*self.lead, self.k)
-        y = codes.new_empty((*self.lead, self.k), dtype=_torch().bfloat16)
-        _run("rtl_checkpoint_unpack", (codes.data_ptr(), self.exps.data_ptr(), self.m, self.k, y.data_ptr()), codes)
+            y = _out(out, self.m, self.k, self.lead, codes.device).view(*self.lead, self.k)
+            _separate(y, codes=codes, exps=self.exps, idx=self.idx)
+        else:
+            y = codes.new_empty((*self.lead, self.k), dtype=_torch().bfloat16)
+        if self.pruned_exps is None:
+            _run("rtl_checkpoint_unpack", (codes.data_ptr(), self.exps.data_ptr(), self.m, self.k, y.data_ptr()), codes)
+        else:
+            _run("rtl_checkpoint_unpack_fine", (codes.data_ptr(), self.exps.data_ptr(), self.pruned_exps.data_ptr(),
+                                                self.idx.data_ptr(), self.m, self.k, y.data_ptr()), codes)
         return y
 
 
-def checkpoint(x) -> Checkpoint:
-    """Keeps x [..., k] (bf16, finite) in 8 bits for the backward pass."""
+def checkpoint(x, fine: bool = False) -> Checkpoint:
+    """Keeps x [..., k] (bf16, finite) in 8 bits for the backward pass.
+
+    ``fine`` keeps a second exponent per 32 channels, of the pruned ones, and their
+    signs (1.19 bytes a channel instead of 1.16).  Where a few channels are far
+    larger than the rest, the one exponent makes more than half of the pruned
+    channels zero, and with 8 % of them large dA and dB are off by 17 % and dX by 9 %;
+    ``fine`` makes it 1.9 % and 0.2 %.  With activations of one scale both are within
+    3 % (include/rtlynx_train.h)."""
     torch = _torch()
     x2 = _as_2d(x, "x")
     m, k = x2.shape
@@ -104,13 +126,19 @@ def checkpoint(x) -> Checkpoint:
     exps = x2.new_empty((m, (k + 31) // 32), dtype=torch.uint8)
     idx = x2.new_empty((m, (k + 7) // 8), dtype=torch.uint8)
     stats = x2.new_empty((m, 2), dtype=torch.float32)
-    _run("rtl_checkpoint_pack", (x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), idx.data_ptr(),
-                                 stats.data_ptr()), x2)
-    return Checkpoint._made(codes, exps, idx, stats, x.shape[:-1])
+    pruned_exps = torch.empty_like(exps) if fine else None
+    if fine:
+        _run("rtl_checkpoint_pack_fine", (x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), pruned_exps.data_ptr(),
+                                          idx.data_ptr(), stats.data_ptr()), x2)
+    else:
+        _run("rtl_checkpoint_pack", (x2.data_ptr(), m, k, codes.data_ptr(), exps.data_ptr(), idx.data_ptr(),
+                                     stats.data_ptr()), x2)
+    return Checkpoint._made(codes, exps, idx, stats, x.shape[:-1], pruned_exps)
 
 
 def unpack(codes, exps, out=None):
-    """bf16 values [m, k] of int8 codes [m, k] and exponents [m, ceil(k / 32)]."""
+    """bf16 values [m, k] of int8 codes [m, k] and exponents [m, ceil(k / 32)] (one
+    exponent per block; ``Checkpoint.unpack`` serves both forms)."""
     torch = _torch()
     if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
         raise TypeError("codes must be int8 and exps uint8")
@@ -174,8 +202,9 @@ def sparse_linear_backward(g, kept: Checkpoint, w_t, lora_a=None, lora_b=None, l
     db = g2.new_empty((n, r)) if lora else None
     workspace = _workspace(workspace, backward_workspace_bytes(m, n, k, r), dev)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _run("rtl_sparse_linear_backward",
-         (g2.data_ptr(), kept.codes.data_ptr(), kept.exps.data_ptr(), kept.idx.data_ptr(), kept.stats.data_ptr(),
+    fine = () if kept.pruned_exps is None else (kept.pruned_exps.data_ptr(),)
+    _run("rtl_sparse_linear_backward_fine" if fine else "rtl_sparse_linear_backward",
+         (g2.data_ptr(), kept.codes.data_ptr(), kept.exps.data_ptr(), *fine, kept.idx.data_ptr(), kept.stats.data_ptr(),
           ptr(w_t), ptr(lora_a) if r else None, ptr(lora_b) if r else None, m, n, k, r, float(lora_scale), ptr(dx),
           ptr(da), ptr(db), workspace.data_ptr(), workspace.numel()),
          g2, kept=kept.codes, w_t=w_t, lora_a=lora_a, lora_b=lora_b)
