@@ -730,11 +730,15 @@ pad_kernel(const u32x2* __restrict__ g, const u32x2* __restrict__ w_t, int64_t r
 // position bytes and 32 bytes of dX.  Workgroups past `blocks` sum dA and dB, which
 // saves a launch where both are asked for.
 template <int RT, bool SPLIT>                           // RT: rp / 32, 0 without LoRA; SPLIT: P in ranges
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckpt ck, const u32x4* __restrict__ u,
               const u32x4* __restrict__ a_up, const float* __restrict__ d_lora, BackwardLayout L, int64_t chunk,
               uint16_t* __restrict__ dx, int64_t blocks, Factors factors) {
   __shared__ float red[256];
+  // U's words, the same for the four wavefronts: [rank step][word][16 tokens].  (In
+  // registers they left one wavefront per SIMD above rank 64: 4096 x 3072 x 12288,
+  // r = 128: 435 us a call instead of 419.)
+  __shared__ u32x4 us[RT > 0 ? RT * 3 * 2 * 64 : 1];
   if constexpr (RT > 0) {
     if (blockIdx.x >= blocks) {
       join_columns(factors, L, (blockIdx.x - blocks) * 256 + threadIdx.x, (gridDim.x - blocks) * 256);
@@ -808,14 +812,13 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
     for (int64_t i = threadIdx.x >> 5; i < L.p_splits * L.p_tiles; i += 8) d += d_part[i * L.M + row];
     red[threadIdx.x] = d;
   }
-  Words us[2][RT > 0 ? RT : 1];
+  for (int z = wave; z < 2 * RT; z += 4) {
+    const int i = z & 1, r = z >> 1;
+    const u32x4* const f = u + (((b0 + i) * RT + r) * 2) * 64 + lane;
+    const Words s3 = split24(f[0], f[64]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const u32x4* const f = u + (((b0 + i) * RT + r) * 2) * 64 + lane;
-      us[i][r] = split24(f[0], f[64]);
-    }
+    for (int w = 0; w < 3; ++w) us[((r * 3 + w) * 2 + i) * 64 + lane] = s3.w[w];
+  }
   __syncthreads();
   float per[2], per_kept[2];                            // D / Lk of a pruned channel; times 1 - s of a kept one
 #pragma unroll
@@ -832,17 +835,26 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
     uint32_t out[2][8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) ckpt_clip16(f.x[i], (int)(64 * t + 16 * quad), K);
+    f32x4 v[4][2];                                      // U A
+#pragma unroll
+    for (int n = 0; n < 4; ++n) v[n][0] = v[n][1] = kZero4;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      u32x4 a[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) a[n] = a_up[((4 * t + n) * RT + r) * 64 + lane];
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const u32x4 b = us[((r * 3 + w) * 2 + i) * 64 + lane];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) v[n][i] = mfma(a[n], b, v[n][i]);
+        }
+      if constexpr (RT == 4) __builtin_amdgcn_sched_barrier(0);   // one rank step's operands at a time
+    }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      f32x4 v[2] = {kZero4, kZero4};
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const u32x4 a = a_up[((4 * t + n) * RT + r) * 64 + lane];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int w = 0; w < 3; ++w) v[i] = mfma(a, us[i][r].w[w], v[i]);
-      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t b = ckpt_kept16(f.x[i], n), q = f.x[i].codes[n];
@@ -851,8 +863,8 @@ finish_kernel(const float* __restrict__ p, const float* __restrict__ d_part, Ckp
         for (int e = 0; e < 4; ++e) {
           const int c = (int)(q << (24 - 8 * e)) >> 24;
           const float sign = c > 0 ? 1.f : c < 0 ? -1.f : 0.f;
-          o[e] = (b >> e) & 1u ? v[i][e] + s[i] * (f.p[i][n][e] - v[i][e]) + sign * per_kept[i]
-                               : v[i][e] + sign * per[i];
+          o[e] = (b >> e) & 1u ? v[n][i][e] + s[i] * (f.p[i][n][e] - v[n][i][e]) + sign * per_kept[i]
+                               : v[n][i][e] + sign * per[i];
         }
         out[i][2 * n] = cvt_pk_bf16(o[0], o[1]);
         out[i][2 * n + 1] = cvt_pk_bf16(o[2], o[3]);
