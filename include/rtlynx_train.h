@@ -9,7 +9,9 @@
  *   s = L1(X) / L1(M * X) per token (1 where that is 0 / 0)
  *
  * with M the 0/1 pattern of the kept channels.  W is frozen; A and B learn.
- * Beside X's checkpoint the backward pass needs nothing from the forward.
+ * Beside X's checkpoint the backward pass needs nothing from the forward.  It is the
+ * default layer's only: the variants of rtl_sparse_linear_prepare_variant and the
+ * dense product have no backward here.
  *
  * Conventions are those of rtlynx.h (bf16 tensors as raw words, 16-byte
  * aligned bases, each tensor below 2 GiB counting 256 rows past its end, K a
