@@ -18,12 +18,18 @@ Entry points (same names as the C ABI in include/rtlynx.h, without the
   (no workspace: the library's fixed per-GPU scratch array)
 * ``dense_linear(x, w)`` -> y
 * ``sparse_linear_workspace_bytes(M, K, r)``
+
+No call records an autograd graph: results have no ``grad_fn``, and a gradient is a
+call of its own (``training.sparse_linear_backward``, ``rotary.rope_backward``), for
+instance in a ``torch.autograd.Function``.  The layers, ``w4.linear`` and
+``rotary.rope`` warn where gradients are enabled and an input requires one.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import os
+import warnings
 
 __all__ = [
     "RtlError", "lib", "library_path", "sparsify_2of4", "sparse_linear", "dense_linear",
@@ -128,6 +134,19 @@ def _as_2d(t, name: str):
     return t.reshape(-1, t.shape[-1]) if t.dim() != 2 else t
 
 
+def _no_graph(where: str, gradient: str, *tensors, level: int = 3) -> None:
+    """Warns the caller whose gradients would stop here without a word."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            if _torch().is_grad_enabled():
+                warnings.warn(f"{where} records no autograd graph: no gradient reaches its inputs ({gradient})",
+                              stacklevel=level)
+            return
+
+
+_BACKWARD = "training.sparse_linear_backward forms it"
+
+
 def _stream():
     """The current device's current stream (inside ``_on``: the tensors')."""
     torch = _torch()
@@ -222,7 +241,9 @@ def sparsify_2of4(x, fold_scale: bool = False, with_scale: bool = True):
 
 def sparse_linear(x, w, lora_a=None, lora_b=None, lora_scale: float = 1.0, out=None, workspace=None):
     """Y = S(X) W^T + lora_scale * ((X - S(X)) A^T) B^T for x [..., K], w [N, K],
-    lora_a [r, K], lora_b [N, r] (bf16, device).  Returns y [..., N] bf16."""
+    lora_a [r, K], lora_b [N, r] (bf16, device).  Returns y [..., N] bf16, without
+    an autograd graph."""
+    _no_graph("sparse_linear", _BACKWARD, x, lora_a, lora_b)
     x2 = _as_2d(x, "x")
     w2 = _as_2d(w, "w")
     m, k = x2.shape
@@ -255,6 +276,7 @@ def sparse_linear_noalloc(x, w, lora_a=None, lora_b=None, lora_scale: float = 1.
     library's fixed per-GPU scratch array (NOALLOC_SCRATCH_BYTES) stands in
     for it, so with ``out`` given nothing is allocated.  Calls that can
     overlap on one GPU share that array and must be serialised."""
+    _no_graph("sparse_linear_noalloc", _BACKWARD, x, lora_a, lora_b)
     x2 = _as_2d(x, "x")
     w2 = _as_2d(w, "w")
     m, k = x2.shape
@@ -293,6 +315,7 @@ def prepare(x, lora_a=None, lora_scale: float = 1.0, workspace=None, variant: in
     """First half of sparse_linear: reads x once (rtl_sparse_linear_prepare,
     or rtl_sparse_linear_prepare_variant for a nonzero ``variant``: one of
     COMP_* | one of LORA_*)."""
+    _no_graph("prepare", _BACKWARD, x, lora_a)
     x2 = _as_2d(x, "x")
     m, k = x2.shape
     r = 0
@@ -317,6 +340,7 @@ def prepare(x, lora_a=None, lora_scale: float = 1.0, workspace=None, variant: in
 
 def apply(prep: Prepared, w, lora_b=None, out=None):
     """Second half of sparse_linear: sparse GEMM + scale + LoRA-up (rtl_sparse_linear_apply)."""
+    _no_graph("apply", _BACKWARD, lora_b)
     w2 = _as_2d(w, "w")
     n = w2.shape[0]
     if w2.shape[1] != prep.k:

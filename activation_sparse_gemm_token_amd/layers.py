@@ -18,7 +18,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _as_2d, _check, _on, _out, _stream, _workspace, lib, sparse_linear_workspace_bytes
+from . import (_BACKWARD, _as_2d, _check, _no_graph, _on, _out, _stream, _workspace, lib,
+               sparse_linear_workspace_bytes)
 
 DENSE = 0x100
 STREAM_W = 0x200
@@ -65,7 +66,10 @@ class LayerPolicy:
     def linear(self, layer: int, x, w, lora_a=None, lora_b=None, lora_scale: float = 1.0, out=None,
                workspace=None):
         """Layer ``layer`` on x [..., K] with weight w [N, K] and LoRA factors
-        (used by sparse layers only).  Returns y [..., N] bf16."""
+        (used by sparse layers only).  Returns y [..., N] bf16, without an autograd
+        graph; the training module's gradients are those of the default layer
+        (variant 0) only."""
+        _no_graph("LayerPolicy.linear", _BACKWARD, x, lora_a, lora_b)
         x2 = _as_2d(x, "x")
         w2 = _as_2d(w, "w")
         m, k = x2.shape

@@ -12,7 +12,7 @@ import ctypes
 import math
 import struct
 
-from . import _check, _here, _on, _stream, _torch, lib
+from . import _check, _here, _no_graph, _on, _stream, _torch, lib
 
 __all__ = ["rope", "rope_backward", "frequencies", "frequencies_by_parts", "LAYOUTS"]
 
@@ -260,7 +260,10 @@ def rope(x, positions, inv_freq, k=None, layout: str = "half", sections=None, sc
     last dimension of that many axes.  ``inv_freq`` float64 [rot / 2] on the
     device (``frequencies``); channels past rot are copied.  ``layout``
     "half" pairs channels (i, i + rot / 2), "interleaved" (2i, 2i + 1).
-    ``out`` / ``k_out`` may be the input itself.  Returns y, or (y, k's y)."""
+    ``out`` / ``k_out`` may be the input itself.  Returns y, or (y, k's y), without
+    an autograd graph (``rope_backward``)."""
+    if x.requires_grad or (k is not None and k.requires_grad):
+        _no_graph("rotary.rope", "rotary.rope_backward forms it", x, k)
     return _rope(x, positions, inv_freq, k, layout, sections, scale, out, k_out, False)
 
 

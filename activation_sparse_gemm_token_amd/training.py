@@ -5,7 +5,11 @@ layer's input kept in 8 bits, and the backward pass that reads it.
     kept = training.checkpoint(x, fine=True)        # instead of keeping x
     dx, da, db = training.sparse_linear_backward(dy, kept, w_t, a, b, alpha)
 
-Argument marshalling only, as in the package's other bindings.
+No call records an autograd graph: a model calls these in the forward and backward
+of its own ``torch.autograd.Function``.  The gradients are those of ``sparse_linear``
+(the default layer); dense layers and the compensation and LoRA-input variants of
+``layers.LayerPolicy`` have none here.  Argument marshalling only, as in the
+package's other bindings.
 """
 from __future__ import annotations
 

@@ -6,7 +6,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _as_2d, _check, _here, _on, _out, _separate, _stream, _torch, lib
+from . import _as_2d, _check, _here, _no_graph, _on, _out, _separate, _stream, _torch, lib
 
 __all__ = ["Weight", "pack", "linear", "packed_bytes", "GROUPS", "MAX_ROWS"]
 
@@ -79,7 +79,9 @@ def pack(codes, scales, zeros=None, group: int = 128) -> Weight:
 def linear(x, weight: Weight, out=None):
     """y [..., n] bf16 = x [..., k] bf16 times the weight: made for 1 to 64
     rows, accepts up to ``MAX_ROWS``.  x must be finite; ``out`` shares no memory
-    with it."""
+    with it.  For inference: the result has no autograd graph."""
+    if x.requires_grad:
+        _no_graph("w4.linear", "it has none", x)
     x2 = _as_2d(x, "x")
     m, k = x2.shape
     if k != weight.k:
