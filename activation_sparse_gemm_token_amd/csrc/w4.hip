@@ -230,8 +230,9 @@ w4_rows_kernel(const uint16_t* __restrict__ x, const char* __restrict__ packed, 
   }
   constexpr int kAhead = 4;                             // steps of weights requested ahead,
   // and of x; at 16 rows x 64 weight rows two steps took 9.1 us where one took 9.8
-  // (16 x 4096 x 12288), elsewhere two were slower or spilled.
-  constexpr int kAheadX = XR == 8 ? 4 : XR == 16 && NT == 2 ? 2 : 1;
+  // (16 x 4096 x 12288, groups of 128).  With groups of 32 two steps spill; at other
+  // rows two were slower or spilled.
+  constexpr int kAheadX = XR == 8 ? 4 : XR == 16 && NT == 2 && GROUPS < 4 ? 2 : 1;
   u32x4 w[kAhead][NT], xv[kAheadX][kLoads];
   MetaT s[kAhead][NT];
   auto load_w = [&](int b, int64_t tile) {
