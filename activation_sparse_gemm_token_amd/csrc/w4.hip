@@ -196,11 +196,11 @@ w4_short_kernel(const uint16_t* __restrict__ x, const char* __restrict__ packed,
 // memory channel), and the NW x KW wavefronts take NT weight tiles and 128
 // channels each.  Weights are requested four steps before they are used.
 //
-// What bounds it: at 8 rows a wavefront issues about 75 vector instructions for
-// each KiB of weights (48 of them widen the codes, the least this form needs),
-// which a CU can just sustain at its share of the card's memory rate; 1 x 4096 x
-// 24576 takes 11.5 us (4.5 TB/s).  From 32 rows on LDS reads and the matrix
-// cores' share grow instead: 64 x 4096 x 12288 takes 17 us.
+// What bounds it: at 8 rows a wavefront issues 50 vector instructions for each KiB
+// of weights with groups of 128 (32 of them widen the codes, the least this form
+// needs) and 61 with groups of 64 and zero points; 1 x 4096 x 24576 takes 11.5 us
+// (4.5 TB/s).  From 32 rows on LDS reads and the matrix cores' share grow instead:
+// 64 x 4096 x 12288 takes 17.6 us.
 template <int XR, int NT, int NW, int KW, int GROUPS, bool ZEROS>
 __global__ void __launch_bounds__(64 * NW * KW)
 w4_rows_kernel(const uint16_t* __restrict__ x, const char* __restrict__ packed, int64_t meta_at, int64_t M,
@@ -394,15 +394,23 @@ hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, in
   // Weight rows per workgroup: as few as give each CU one workgroup, with all
   // wavefronts along the channels; more once there are enough, which reads x
   // less often, or with few channels, whose steps the loop rounds up to four.
-  // Either way round at the other's sizes (us):
-  //   1 x 12288 x 4096:  16 rows 8.7, 32 rows 12.4;  1 x 12288 x 4099: 14.2, 12.2;
-  //   1 x 4096 x 4096:   16 rows 5.3, 32 rows 6.2;   1 x 4096 x 12288: 11.5, 9.3;
-  //   1 x 1536 x 4096:   16 rows 5.3, 32 rows 4.7;
-  //   16 x 4096 x 8192:  16 rows 8.4, 64 rows 8.9;   16 x 4096 x 12288: 11.3, 9.3;
-  //   16 x 1536 x 4096:  16 rows 5.7, 64 rows 6.1;   16 x 1536 x 4099: 6.8, 6.0;
-  //   32 x 4096 x 4096:  32 rows 9.7, 64 rows 12.9;  32 x 4096 x 12288: 13.7, 11.8;
-  //   64 x 4096 x 4096:  32 rows of 32 x rows 8.7, 64 of 64 16.2;
-  //   64 x 4096 x 12288: 19.2, 17.1.
+  // Rows of x per workgroup: 64, which reads the weights least often, where that
+  // makes a workgroup per CU.  Either way round at the other's sizes (us a call on
+  // the GPU in a captured run, groups of 64 without zero points, weights and scales
+  // of 600 MB in turn):
+  //   1 x 12288 x 4096:  16 rows 10.5, 32 rows 12.8;  1 x 12288 x 4099: 16.7, 12.6;
+  //   1 x 4096 x 4096:   16 rows 5.5, 32 rows 6.2;    1 x 4096 x 12288: 13.6, 9.8;
+  //   1 x 1536 x 4096:   16 rows 5.1, 32 rows 4.6;
+  //   16 x 4096 x 8192:  16 rows 10.9, 64 rows 10.1;  16 x 4096 x 12288: 15.0, 11.0;
+  //   16 x 1536 x 4096:  16 rows 6.0, 64 rows 6.1;    16 x 1536 x 4099: 7.6, 6.1;
+  //   32 x 4096 x 4096:  32 rows 9.3, 64 rows 11.5;   32 x 4096 x 12288: 16.7, 14.3;
+  //   32 weight rows of 32 x rows, 64 of 32, 64 of 64:
+  //   64 x 4096 x 4096:  9.6, 11.7, 18.0;    64 x 4096 x 12288:  24.3, 24.6, 21.1;
+  //   128 x 4096 x 4096: 15.2, 12.5, 18.5;   128 x 4096 x 8192:  30.1, 26.0, 21.5;
+  //   256 x 4096 x 4096: 28.3, 24.7, 20.8;   1024 x 4096 x 4096: 99, 85, 72.
+  // (1 x 12288 x 4099 makes 257 workgroups of 16 rows: with groups of 64 they have
+  // 145 registers, so a CU holds one, and the last waits for a second round; with
+  // groups of 128 there is room for two and they take 12.7.)
   const bool deep = tiles_k > 16;
   if (M <= 8)
     return tiles_n <= 256 && deep ? launch_rows<8, 1, 1, 8>(x, p, meta_at, M, N, K, group, zeros, y, stream)
@@ -410,7 +418,8 @@ hipError_t launch_w4_linear(const uint16_t* x, const void* packed, int64_t M, in
   if (M <= 16)
     return tiles_n <= (deep ? 512 : 256) ? launch_rows<16, 1, 1, 8>(x, p, meta_at, M, N, K, group, zeros, y, stream)
                                          : launch_rows<16, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
-  if (tiles_n <= 512) return launch_rows<32, 1, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
+  if (tiles_n <= 512 && (M + 63) / 64 * ((tiles_n + 3) / 4) < 256)
+    return launch_rows<32, 1, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
   if (M <= 32) return launch_rows<32, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
   return launch_rows<64, 2, 2, 4>(x, p, meta_at, M, N, K, group, zeros, y, stream);
 }

@@ -6,8 +6,10 @@
  * The layers of a model that see one row per image or a few rows per prompt
  * (time embedding, modulation, short prompts) are weight traffic and nothing
  * else; beside rtl_sparse_linear, which serves thousands of tokens, these
- * entry points serve 1 to 64 rows at a quarter of the bf16 weights' bytes.
- * More rows are accepted and read the weights once per 64 of them.
+ * entry points serve 1 to 32 rows at a quarter of the bf16 weights' bytes, and up
+ * to 64 where N is above 8192.  More rows are accepted: the weights are read once per
+ * 64 of them, or once per 32 where N <= 8192 and tiles of 64 x 64 would be fewer
+ * than 256.
  *
  * q is 0..15, z the group's zero point (8 for every group when a weight has
  * none), s a bf16 scale.  Products are formed in fp32 from exact operands:
