@@ -150,7 +150,10 @@ _BACKWARD = "training.sparse_linear_backward forms it"
 def _stream():
     """The current device's current stream (inside ``_on``: the tensors')."""
     torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    except AttributeError:                              # not part of torch's interface: a faster way to the same number
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _here(t, *others):
@@ -162,7 +165,10 @@ def _here(t, *others):
     for o in others:
         if o is not None and o.get_device() != device:
             return None
-    return c._cuda_getCurrentRawStream(device) if c._cuda_getDevice() == device else None
+    try:
+        return c._cuda_getCurrentRawStream(device) if c._cuda_getDevice() == device else None
+    except AttributeError:
+        return None
 
 
 _HERE_CONTEXT = contextlib.nullcontext()                # the device is current already
