@@ -104,6 +104,8 @@ class Checkpoint:
         if out is not None:
             y = _out(out, self.m, self.k, self.lead, codes.device).view(*self.lead, self.k)
             _separate(y, codes=codes, exps=self.exps, idx=self.idx)
+            if self.pruned_exps is not None:
+                _separate(y, pruned_exps=self.pruned_exps)
         else:
             y = codes.new_empty((*self.lead, self.k), dtype=_torch().bfloat16)
         if self.pruned_exps is None:
