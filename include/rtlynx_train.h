@@ -115,8 +115,8 @@ rtl_status rtl_sparse_linear_backward_form(int64_t M, int64_t N, int64_t K, int6
  *   dA = U^T R                          [r, K]
  *   dB = alpha G^T (R A^T)              [N, r]
  *
- *   g        [M, N] bf16, finite: an infinity or NaN gives NaN in its token's row of
- *            dX, in dA and in what of dB it reaches, and leaves the rest as it is.
+ *   g        [M, N] bf16, finite: an infinity or NaN makes its token's row of dX, all of
+ *            dA and its channel's row of dB not finite, and leaves the rest as it is.
  *   codes, exps, idx, stats: as rtl_checkpoint_pack wrote them.
  *   w_t      [K, N] bf16, the frozen weight transposed (laid out once: it does
  *            not change in training).  Needed for dx only.

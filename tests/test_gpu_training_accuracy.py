@@ -99,3 +99,25 @@ def test_the_layer_on_the_stored_values_is_the_layer(m, n, k, r, law):
     tol += 2 * plain.depth(k) * plain.U24 * (reach @ np.abs(W.T)) + (2 * plain.depth(k) * plain.U24 + plain.U16) * (reach_r @ up)
     got = plain.bf16(y)
     assert (np.abs(got - want) <= tol + plain.HALF_BF16 * (np.abs(want) + tol)).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("m,n,k,r", [(70, 136, 260, 16), (600, 264, 1032, 64), (33, 64, 68, 100), (70, 136, 260, 0)])
+def test_what_a_gradient_that_is_not_finite_reaches(m, n, k, r, value):
+    """Its token's row of dX, dA, and its channel's row of dB."""
+    rng, row, col = np.random.default_rng(m), m // 2, n // 3
+    x, g = to_dev(gen.mixture_bernoulli(rng, m, k)), dev(0.01 * rng.standard_normal((m, n)))
+    w_t, a, b = (dev(0.05 * rng.standard_normal(s)) for s in ((k, n), (r, k), (n, r)))
+    lora = (a, b) if r else (None, None)
+    for fine in (False, True):
+        kept = training.checkpoint(x, fine=fine)
+        want = training.sparse_linear_backward(g, kept, w_t, *lora)
+        bad = g.clone()
+        bad[row, col] = value
+        got = training.sparse_linear_backward(bad, kept, w_t, *lora)
+        others = torch.arange(m, device=DEV) != row
+        assert torch.equal(got[0][others], want[0][others]) and not bool(torch.isfinite(got[0][row]).any())
+        if r:
+            assert not bool(torch.isfinite(got[1]).any()) and not bool(torch.isfinite(got[2][col]).any())
+            rest = torch.arange(n, device=DEV) != col
+            assert torch.equal(got[2][rest], want[2][rest])
