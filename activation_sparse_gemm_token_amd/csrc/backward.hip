@@ -27,10 +27,11 @@
 // A kept value's residual (1 - s) x is not a bf16 number; multiplying U (or the
 // joined sum) by 1 - s instead keeps the checkpoint's values exact operands.
 //
-// At 4096 x 3072 x 12288, r = 64 (us): factors 5, rows 38, join 7, columns 48, G W
-// 250 to 280 as the clock drops, dX with the sums of dA and dB 30 (27 and, in a
-// launch of their own, 7.6).  Rows and columns read G (100 MB) and the checkpoint
-// (14 MB), 22 us at the card's copy rate.
+// At 4096 x 3072 x 12288, r = 64 (us, inputs changing from call to call): factors 5,
+// rows 43, join 7, columns 49, G W 250 to 275 as the clock drops, dX with the sums of
+// dA and dB 29 (27 and, in a launch of their own, 7.6).  Rows and columns read G
+// (100 MB) and the checkpoint (14 MB), 22 us at the card's copy rate, and their
+// factors' fragments from L2 as often as that.
 //
 // Fragments instead of transposed matrices: a matrix whose rows are N channels
 // apart puts the 16 rows of an operand load on one memory channel; as 1 KiB

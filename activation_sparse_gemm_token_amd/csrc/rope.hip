@@ -8,10 +8,11 @@
 //
 // A thread's unit is 16 bytes of a head where the layout's alignment allows (in
 // the half layout 16 bytes from each half of the rotated part), else the widest
-// power of two that does, and the kernel is bound by HBM: each element is read
-// once and written once.  2 x 4608 tokens, 24 + 24 heads of 128, bf16: 35 us
-// (6.4 TB/s); 32768 tokens, 10 heads of 64, fp32: 29 us (5.8 TB/s); one token, 40
-// heads: 3.2 us.
+// power of two that does, and the kernel is bound by memory: each element is read
+// once and written once.  With inputs and outputs out of the caches 2 x 4608 tokens,
+// 24 + 24 heads of 128, bf16 take 46 us (4.9 TB/s; a copy reaches 5.15) and 32768
+// tokens, 10 heads of 64, fp32 35 us; with the same ones again and again, partly in
+// the last-level cache, 35 and 28.  One token, 40 heads: 3.3 us.
 #include "rtl_common.hpp"
 #include "rtl_operators.hpp"
 
