@@ -29,15 +29,6 @@ inline hipError_t launch(void (*k)(P...), dim3 grid, dim3 block, hipStream_t str
   return launch_tuple(k, grid, block, stream, args, std::index_sequence_for<P...>{});
 }
 
-// A launch dimension holds less than 2^32 threads: more workgroups than that of up
-// to 512 go to z, in rows of 2^22.  folded_block() is the workgroup's number; those
-// past the last one have nothing to do.
-inline dim3 folded_grid(int64_t blocks, unsigned y = 1) {
-  constexpr int64_t kRow = (int64_t)1 << 22;
-  return blocks <= kRow ? dim3((unsigned)blocks, y) : dim3((unsigned)kRow, y, (unsigned)((blocks + kRow - 1) / kRow));
-}
-__device__ __forceinline__ int64_t folded_block() { return (int64_t)blockIdx.z * gridDim.x + blockIdx.x; }
-
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
