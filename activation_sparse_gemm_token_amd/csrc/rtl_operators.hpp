@@ -1,6 +1,6 @@
 // Launch wrappers of the operators beside the sparse layer: rotary positions,
-// 4-bit linears, the activation checkpoint and the layer's backward pass
-// (internal; the public interfaces are include/rtlynx_*.h).
+// 4-bit linears, the activation checkpoint, the layer's backward pass, layer
+// norm, dense linears with an epilogue and attention (internal; the public interfaces are include/rtlynx_*.h).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -89,5 +89,73 @@ hipError_t launch_grad_gemm(const uint16_t* g, const uint16_t* w_t, const Ckpt& 
 hipError_t launch_backward(const uint16_t* g, const Ckpt& ck, const uint16_t* w_t, const uint16_t* lora_a,
                            const uint16_t* lora_b, const BackwardLayout& L, float alpha, uint16_t* dx,
                            uint16_t* da, uint16_t* db, char* workspace, hipStream_t stream);
+
+// Layer norm (include/rtlynx_norm.h).  Strides in elements; rows = batch * tokens.
+struct NormArgs {
+  const void* x;
+  void* y;
+  const void* weight;
+  const void* bias;
+  float* mean;
+  float* rstd;
+  int64_t rows, tokens;
+  int64_t xb, xt, yb, yt, wb, bb;
+  float offset, eps, inv_c;
+  int C;
+  bool affine_fp32;
+};
+struct NormBackArgs {
+  const void* dy;
+  const void* x;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  void* dweight;
+  void* dbias;
+  float* partials;                       // [groups][parts][2][C], NULL without dweight
+  int64_t rows, tokens, groups, parts;
+  int64_t gb, gt, xb, xt, db, dt, wb;
+  float offset, inv_c;
+  int C;
+  bool affine_fp32;
+};
+int64_t norm_parts(int64_t rows, int64_t groups, int64_t C);
+// vec: elements per access, 8 (16-bit types only), 4 or 1.
+hipError_t launch_norm(const NormArgs& a, int type, int vec, hipStream_t stream);
+hipError_t launch_norm_backward(const NormBackArgs& a, int type, int vec, hipStream_t stream);
+
+// Attention (include/rtlynx_attention.h).  Strides in elements.
+struct AttnTensor {
+  uint16_t* p;
+  int64_t b, t, h;
+};
+struct AttnArgs {
+  AttnTensor q, k, v, o;
+  float* lse;
+  const int32_t* q_starts;               // NULL: a batch
+  const int32_t* k_starts;
+  const int32_t* k_lens;                 // NULL: every key
+  int64_t sequences, tq, tk;             // tokens of a sequence, or of all (packed)
+  int64_t tiles;                         // of queries (of keys: dK, dV), per head
+  int64_t groups;                        // workgroups
+  int hq, hk, group, d;
+  float scale, c;                        // c = scale log2(e)
+  bool causal, zero_rest;
+  // Few queries over many keys.
+  int splits;
+  float* part_o;                         // [splits][rows][d]
+  float* part_ml;                        // [splits][rows][2]: maximum, sum
+};
+struct AttnBackArgs {
+  AttnArgs f;                            // o and lse of the forward pass
+  AttnTensor d_o, dq, dk, dv;
+  float* lse2;                           // log2 of the sum, +inf where no key is seen
+  float* delta;
+};
+// Splits of the keys for the kernel for few queries, 0 where the other one serves.
+int attn_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, bool packed);
+hipError_t launch_attention(AttnArgs a, bool fp16, hipStream_t stream);
+hipError_t launch_attention_backward(AttnBackArgs a, hipStream_t stream);
 
 }  // namespace rtl

@@ -1,0 +1,196 @@
+"""Layer norm of the tokens that a block's projections read, and its gradients
+(include/rtlynx_norm.h).
+
+    y = (x - mean) * rstd * (offset + weight) + bias
+
+``weight`` and ``bias`` have one value per channel or one row per sequence (a
+block's modulation: ``offset=1`` makes the factor 1 + weight).  Strided tensors
+go as they are (slices of a joint sequence, of a modulation row); only the
+channel stride must be 1.  Argument marshalling only, as in the package's other
+bindings.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _here, _no_graph, _on, _stream, _torch, _workspace, lib
+from .rotary import _apart, _distinct, _same
+
+__all__ = ["layer_norm", "layer_norm_backward", "backward_workspace_bytes", "MAX_CHANNELS"]
+
+MAX_CHANNELS = 32768
+_AFFINE_FP32 = 0x10
+
+_i64, _vp, _size, _f, _u32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint32
+_SIGNATURES = {
+    "rtl_layer_norm": (ctypes.c_int, [_vp] + [_i64] * 5 + [_vp, _i64, _vp, _i64, _f, _f, _vp, _i64, _i64, _vp, _vp, _u32, _vp]),
+    "rtl_layer_norm_backward_workspace_bytes": (_size, [_i64] * 4),
+    "rtl_layer_norm_backward": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64,
+                                               _f, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _size, _u32, _vp]),
+}
+
+
+def _fn(name):
+    fn = getattr(lib(), name)
+    if fn.argtypes is None:
+        fn.restype, fn.argtypes = _SIGNATURES[name]
+    return fn
+
+
+def _run(name, args, t, **tensors):
+    stream = _here(t, *tensors.values())
+    if stream is None:
+        with _on(t.device, **tensors):
+            st = _fn(name)(*args, _stream())
+    else:
+        st = _fn(name)(*args, stream)
+    _check(st, name)
+
+
+def _type_flag(t, name):
+    torch = _torch()
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float16:
+        return 1
+    if t.dtype is torch.float32:
+        return 2
+    raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+
+
+def _layout(t, name):
+    """(batch, tokens, batch stride, token stride) of [..., C]; more than three
+    dimensions must lie like one row after another."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    shape, stride = t.shape, t.stride()
+    if not shape:
+        raise ValueError(f"{name} must have a channel dimension")
+    if shape[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the channel stride must be 1")
+    if len(shape) == 3:
+        return shape[0], shape[1], stride[0], stride[1]
+    if len(shape) == 2:
+        return 1, shape[0], 0, stride[0]
+    if len(shape) == 1:
+        return 1, 1, 0, 0
+    if not t.is_contiguous():
+        raise ValueError(f"{name} with more than three dimensions must be contiguous")
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return 1, rows, 0, shape[-1]
+
+
+def _affine(p, name, x, batched):
+    """(pointer, stride between sequences, rows) of weight or bias."""
+    torch = _torch()
+    c = x.shape[-1]
+    if p.dtype is not x.dtype and p.dtype is not torch.float32:
+        raise TypeError(f"{name} must be {x.dtype} or float32, got {p.dtype}")
+    if tuple(p.shape) == (c,):
+        stride, rows = 0, 1
+    elif batched and tuple(p.shape) == (x.shape[0], c):
+        stride, rows = p.stride(0), p.shape[0]
+    else:
+        raise ValueError(f"{name} must have shape {(c,)}" + (f" or {(x.shape[0], c)}" if batched else "") +
+                         f", got {tuple(p.shape)}")
+    if c > 1 and p.stride(-1) != 1:
+        raise ValueError(f"{name}: the channel stride must be 1")
+    return p.data_ptr(), stride, rows
+
+
+def _check_out(out, like, **others):
+    if out.dtype != like.dtype:
+        raise TypeError(f"out must be {like.dtype}, got {out.dtype}")
+    if out.device != like.device or out.shape != like.shape:
+        raise ValueError(f"out must be on {like.device} with shape {tuple(like.shape)}")
+    if not _distinct(out):
+        raise ValueError("out must have no overlapping elements")
+    for name, t in others.items():
+        if t is not None and t.numel() and out.numel() and not (name == "x" and _same(out, t)) and not _apart(out, t):
+            raise ValueError(f"out overlaps {name}")
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, offset: float = 0.0, out=None, return_stats: bool = False):
+    """Layer norm of x [batch, tokens, C], [tokens, C] or [C] (bf16, fp16 or fp32)
+    over its channels.
+
+    ``weight`` [C] or [batch, C] and ``bias`` likewise, of x's type or fp32 (both
+    the same); the factor is ``offset + weight``, and 1 without a weight.  ``out``
+    may be x itself.  Returns y, or with ``return_stats`` (y, mean, rstd), the
+    statistics fp32 of x's shape without the channels, without an autograd graph
+    (``layer_norm_backward``)."""
+    torch = _torch()
+    _no_graph("norm.layer_norm", "norm.layer_norm_backward forms it", x, weight, bias)
+    flags = _type_flag(x, "x")
+    batch, tokens, xb, xt = _layout(x, "x")
+    batched = x.dim() == 3
+    wp = bp = None
+    ws = bs = 0
+    if weight is not None:
+        wp, ws, _ = _affine(weight, "weight", x, batched)
+        if weight.dtype is torch.float32:
+            flags |= _AFFINE_FP32
+    if bias is not None:
+        if weight is None:
+            raise ValueError("a bias needs a weight")
+        if bias.dtype is not weight.dtype:
+            raise TypeError(f"bias must be {weight.dtype} like weight, got {bias.dtype}")
+        bp, bs, _ = _affine(bias, "bias", x, batched)
+    if out is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _check_out(out, x, x=x, weight=weight, bias=bias)
+        y = out
+    _, _, yb, yt = _layout(y, "out")
+    mean = rstd = mp = rp = None
+    if return_stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    _run("rtl_layer_norm", (x.data_ptr(), batch, tokens, x.shape[-1], xb, xt, wp, ws, bp, bs, float(offset), float(eps),
+                            y.data_ptr(), yb, yt, mp, rp, flags), x, weight=weight, bias=bias)
+    return (y, mean, rstd) if return_stats else y
+
+
+def backward_workspace_bytes(batch: int, tokens: int, c: int, groups: int) -> int:
+    return int(_fn("rtl_layer_norm_backward_workspace_bytes")(batch, tokens, c, groups))
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, offset: float = 0.0, need_dx: bool = True,
+                        need_affine: bool = True, workspace=None):
+    """Gradients of ``layer_norm`` from dy, its x and the statistics that it
+    returned: (dx, dweight, dbias), None where not asked for.
+
+    dweight and dbias have weight's shape and type, summed over the tokens (and
+    the sequences that share a row); without a weight both are None."""
+    torch = _torch()
+    flags = _type_flag(x, "x")
+    if dy.dtype is not x.dtype:
+        raise TypeError(f"dy must be {x.dtype} like x, got {dy.dtype}")
+    if dy.shape != x.shape:
+        raise ValueError(f"dy must have shape {tuple(x.shape)}, got {tuple(dy.shape)}")
+    batch, tokens, xb, xt = _layout(x, "x")
+    _, _, gb, gt = _layout(dy, "dy")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype is not torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])}")
+    wp, ws, groups = None, 0, 1
+    dw = db = work = None
+    if weight is not None:
+        wp, ws, groups = _affine(weight, "weight", x, x.dim() == 3)
+        if weight.dtype is torch.float32:
+            flags |= _AFFINE_FP32
+        if need_affine:
+            dw = torch.empty(weight.shape, dtype=weight.dtype, device=x.device)
+            db = torch.empty_like(dw)
+            work = _workspace(workspace, backward_workspace_bytes(batch, tokens, x.shape[-1], groups), x.device)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+    _, _, db_, dt = _layout(dx, "dx") if need_dx else (0, 0, 0, 0)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _run("rtl_layer_norm_backward",
+         (dy.data_ptr(), gb, gt, x.data_ptr(), xb, xt, mean.data_ptr(), rstd.data_ptr(), batch, tokens, x.shape[-1], wp, ws,
+          float(offset), groups, ptr(dx), db_, dt, ptr(dw), ptr(db), ptr(work), 0 if work is None else work.numel(), flags),
+         x, dy=dy, mean=mean, rstd=rstd, weight=weight)
+    return dx, dw, db
