@@ -1,0 +1,413 @@
+// Attention, forward (include/rtlynx_attention.h): one pass over the keys with
+// the softmax's running maximum and sum.
+//
+// attn_forward_kernel.  A wavefront holds 32 queries: their operands, O^T in
+// fp32 and, per lane, one query's maximum and sum; its workgroup shares tiles of
+// 64 keys and values in LDS, copied one tile ahead.  Scores are compared with
+// the maximum the accumulators are scaled by; that maximum moves (and O^T is
+// rescaled) only when some score passes it by more than 2^8, which changes no
+// result (any reference would do) and leaves the rescaling out of most steps.
+//
+// attn_few_kernel.  Few queries over many keys are bound by reading K and V:
+// the queries of all heads that share a key head are one tile of 32 rows, every
+// wavefront walks its own tiles of 32 keys (its own copies, no barrier), and the
+// keys are split over workgroups until the card is full; attn_join_kernel adds
+// the parts up.
+#include "attn_common.hpp"
+
+namespace rtl {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+// p relative to the reference maximum stays below 2^8: exact enough in fp16 too (65504).
+constexpr float kSlack = 8.f;
+
+__device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ float ninf() { return -__builtin_inff(); }
+
+// A lane's running softmax: maximum the sums are scaled by (log2 units), its stand-in where no
+// key was seen, this half's share of the sum.
+struct Running {
+  float m, mu, l;
+  __device__ __forceinline__ void init() { m = ninf(), mu = 0.f, l = 0.f; }
+};
+
+// One block of scores into weights; O^T is rescaled where the maximum moved.  `top`: the largest
+// score of the lane's query in this step, in log2 units.
+template <int NB>
+__device__ __forceinline__ void move_maximum(Running& r, float top, f32x16 (&o)[NB]) {
+  if (__any(top > r.m + kSlack)) {
+    const float m = __builtin_fmaxf(r.m, top);
+    r.mu = m == ninf() ? 0.f : m;
+    const float f = exp2_(r.m - r.mu);
+    r.m = m;
+    r.l *= f;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[nb][i] *= f;
+  }
+}
+
+__device__ __forceinline__ float max16(const f32x16& s) {
+  float m = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) m = __builtin_fmaxf(m, s[i]);
+  return m;
+}
+
+template <int TYPE, int NB, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 2)
+attn_forward_kernel(AttnArgs a) {
+  using T = Tile<NB>;
+  constexpr int kKeys = 64, kQueries = 32 * WAVES, kTile = kKeys * T::kPitch;
+  __shared__ __attribute__((aligned(16))) char lds[4 * kTile];          // K, V of two steps
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  QueryWork w;
+  if (folded_block() >= a.groups) return;
+  const int64_t id = xcd_order(folded_block(), a.groups);
+  if (!query_work(a, id, kQueries, w)) {
+    // No tile left: some rows may lie in no sequence.
+    const int64_t used = (id % a.tiles) - w.tile, spare = a.tiles - used;
+    rest_rows(a.q_starts, a.sequences, a.tq, w.tile * 64 * WAVES + threadIdx.x, spare * 64 * WAVES, [&](int64_t row) {
+      if (a.lse != nullptr) a.lse[w.head * a.tq + row] = ninf();
+      if (a.zero_rest) {
+        uint16_t* p = a.o.p + row * a.o.t + w.head * a.o.h;
+        for (int c = 0; c < a.d; c += 8) *reinterpret_cast<u32x4*>(p + c) = (u32x4){0, 0, 0, 0};
+      }
+    });
+    return;
+  }
+  const int64_t q0 = w.tile * kQueries + 32 * wave, shift = w.k.len - w.q.len;
+  const int64_t row = q0 + (lane & 31);
+  // Keys that the tile, and this wavefront, see; keys that all of its queries see.
+  const int64_t tile_end = (w.tile + 1) * kQueries < w.q.len ? (w.tile + 1) * kQueries : w.q.len;
+  const int64_t wave_end = q0 + 32 < w.q.len ? q0 + 32 : w.q.len;
+  int64_t keys = w.k.len, mine = q0 < w.q.len ? w.k.len : 0, all = w.k.len, limit = w.k.len;
+  if (a.causal) {
+    keys = tile_end + shift < keys ? tile_end + shift : keys;
+    mine = wave_end + shift < mine ? wave_end + shift : mine;
+    all = q0 + shift + 1 < all ? q0 + shift + 1 : all;
+    limit = row + shift + 1 < limit ? row + shift + 1 : limit;
+  }
+  const int steps = keys > 0 ? (int)((keys + kKeys - 1) / kKeys) : 0;
+
+  TileCopy<NB, kKeys, WAVES> ck, cv;
+  ck.init(wave, a.k.t, a.d);
+  cv.init(wave, a.v.t, a.d);
+  const uint32_t lds0 = lds_address(lds);
+  auto copy = [&](int j) {
+    const int64_t at = (int64_t)j * kKeys;
+    const uint32_t buf = lds0 + (j & 1) * 2 * kTile;
+    ck.run(w.kp + at * a.k.t, w.k.len - at, buf);
+    cv.run(w.vp + at * a.v.t, w.k.len - at, buf + kTile);
+  };
+  if (steps > 0) copy(0);
+
+  u32x4 qf[2 * NB];
+  load_rows<NB>(a.q.p + w.q_off + q0 * a.q.t, a.q.t, w.q.len - q0, a.d, qf);
+  f32x16 o[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) o[nb] = zero16();
+  Running run;
+  run.init();
+  uint32_t row_off[2 * NB], col_off[NB][2];
+#pragma unroll
+  for (int c = 0; c < 2 * NB; ++c) row_off[c] = T::row_operand(c);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    col_off[nb][0] = T::column_operand(nb, 0);
+    col_off[nb][1] = T::column_operand(nb, 1);
+  }
+
+  for (int j = 0; j < steps; ++j) {
+    wait_copies<0>();
+    group_barrier();                                    // tile j is whole, tile j - 1 is no longer read
+    if (j + 1 < steps) copy(j + 1);
+    const int64_t k0 = (int64_t)j * kKeys;
+    if (k0 >= mine) continue;
+    const char* const kt = lds + (j & 1) * 2 * kTile;
+    const char* const vt = kt + kTile;
+    f32x16 s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[kb] = zero16();
+#pragma unroll
+      for (int c = 0; c < 2 * NB; ++c) s[kb] = mfma32<TYPE>(lds_read16(kt + kb * 32 * T::kPitch + row_off[c]), qf[c], s[kb]);
+    }
+    if (k0 + kKeys > all) {
+      const int left = (int)(limit < k0 ? 0 : limit - k0 < kKeys ? limit - k0 : kKeys);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kb][i] = 32 * kb + block_row(i) < left ? s[kb][i] : ninf();
+    }
+    const float top = half_max(__builtin_fmaxf(max16(s[0]), max16(s[1]))) * a.c;
+    move_maximum<NB>(run, top, o);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16 p;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[i] = exp2_(__builtin_fmaf(s[kb][i], a.c, -run.mu));
+        run.l += p[i];
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const u32x4 pw = pack_half<TYPE>(p, half);
+        const char* const base = vt + (32 * kb + 16 * half) * T::kPitch;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) o[nb] = mfma32<TYPE>(column_read(base, col_off[nb][0], col_off[nb][1]), pw, o[nb]);
+      }
+    }
+  }
+  const float l = half_sum(run.l);
+  const int64_t left = w.q.len - q0;
+  store_rows<TYPE, NB>(a.o.p + w.o_off + q0 * a.o.t, a.o.t, left, a.d, o, l == 0.f ? 0.f : 1.f / l);
+  if (a.lse != nullptr && lane < 32 && lane < left)
+    a.lse[w.lse_off + row] = l == 0.f ? ninf() : (run.mu + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// --- Few queries ------------------------------------------------------------
+// Row r of a key head's queries is token r / group, head group kv + r % group.
+constexpr int kFewWaves = 4, kFewKeys = 32;
+
+template <int TYPE, int NB>
+__global__ void __launch_bounds__(64 * kFewWaves, 1)
+attn_few_kernel(AttnArgs a) {
+  using T = Tile<NB>;
+  constexpr int kTile = kFewKeys * T::kPitch, kWaveBytes = 4 * kTile;
+  constexpr int kJoin = kFewWaves * 64 * (16 * NB + 2) * 4;             // O^T, maximum and sum of every wavefront
+  __shared__ __attribute__((aligned(16))) char lds[kFewWaves * kWaveBytes > kJoin ? kFewWaves * kWaveBytes : kJoin];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t rows = a.tq * a.group, tiles = (rows + 31) / 32;
+  int64_t id = folded_block();
+  if (id >= a.groups) return;
+  const int split = (int)(id % a.splits);
+  id /= a.splits;
+  const int64_t tile = id % tiles;
+  id /= tiles;
+  const int64_t kv = id % a.hk, seq = id / a.hk;
+  int64_t len = a.tk;
+  if (a.k_lens != nullptr) {
+    const int64_t n = a.k_lens[seq];
+    len = n < 0 ? 0 : n < a.tk ? n : a.tk;
+  }
+  // This workgroup's keys [lo, hi), in whole rounds of the wavefronts' tiles.
+  constexpr int64_t kRound = kFewWaves * kFewKeys;
+  const int64_t per = (((len + a.splits - 1) / a.splits) + kRound - 1) / kRound * kRound;
+  const int64_t lo = split * per, hi = lo + per < len ? lo + per : len;
+
+  const int64_t r = tile * 32 + (lane & 31), tok = r / a.group, head = kv * a.group + r % a.group;
+  const bool live = r < rows;
+  const int64_t shift = len - a.tq;
+  int64_t limit = len;
+  if (a.causal && tok + shift + 1 < limit) limit = tok + shift + 1;
+  const int64_t first_tok = tile * 32 / a.group;
+  const int64_t all = a.causal && first_tok + shift + 1 < len ? first_tok + shift + 1 : len;
+
+  const uint16_t* const kp = a.k.p + seq * a.k.b + kv * a.k.h;
+  const uint16_t* const vp = a.v.p + seq * a.v.b + kv * a.v.h;
+  TileCopy<NB, kFewKeys, 1> ck, cv;
+  ck.init(0, a.k.t, a.d);
+  cv.init(0, a.v.t, a.d);
+  char* const mine = lds + wave * kWaveBytes;
+  const uint32_t lds0 = lds_address(mine);
+  auto copy = [&](int64_t at, int buf) {
+    ck.run(kp + at * a.k.t, len - at, lds0 + buf * 2 * kTile);
+    cv.run(vp + at * a.v.t, len - at, lds0 + buf * 2 * kTile + kTile);
+  };
+  const int64_t first = lo + kFewKeys * wave;
+  if (first < hi) copy(first, 0);
+  u32x4 qf[2 * NB];
+#pragma unroll
+  for (int c = 0; c < 2 * NB; ++c) {
+    qf[c] = (u32x4){0, 0, 0, 0};
+    const int ch = 16 * c + 8 * (lane >> 5);
+    if (live && ch < a.d) qf[c] = *reinterpret_cast<const u32x4*>(a.q.p + seq * a.q.b + tok * a.q.t + head * a.q.h + ch);
+  }
+  f32x16 o[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) o[nb] = zero16();
+  Running run;
+  run.init();
+  uint32_t row_off[2 * NB], col_off[NB][2];
+#pragma unroll
+  for (int c = 0; c < 2 * NB; ++c) row_off[c] = T::row_operand(c);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    col_off[nb][0] = T::column_operand(nb, 0);
+    col_off[nb][1] = T::column_operand(nb, 1);
+  }
+  int buf = 0;
+  for (int64_t k0 = first; k0 < hi; k0 += kRound, buf ^= 1) {
+    // The other buffer's last reads were consumed in the step before.
+    if (k0 + kRound < hi) {
+      copy(k0 + kRound, buf ^ 1);
+      wait_copies<2 * TileCopy<NB, kFewKeys, 1>::kCount>();
+    } else {
+      wait_copies<0>();
+    }
+    const char* const kt = mine + buf * 2 * kTile;
+    const char* const vt = kt + kTile;
+    f32x16 s = zero16();
+#pragma unroll
+    for (int c = 0; c < 2 * NB; ++c) s = mfma32<TYPE>(lds_read16(kt + row_off[c]), qf[c], s);
+    if (k0 + kFewKeys > all || k0 + kFewKeys > hi) {
+      const int64_t end = limit < hi ? limit : hi;
+      const int left = (int)(end < k0 ? 0 : end - k0 < kFewKeys ? end - k0 : kFewKeys);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = block_row(i) < left ? s[i] : ninf();
+    }
+    move_maximum<NB>(run, half_max(max16(s)) * a.c, o);
+    f32x16 p;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      p[i] = exp2_(__builtin_fmaf(s[i], a.c, -run.mu));
+      run.l += p[i];
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const u32x4 pw = pack_half<TYPE>(p, half);
+      const char* const base = vt + 16 * half * T::kPitch;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) o[nb] = mfma32<TYPE>(column_read(base, col_off[nb][0], col_off[nb][1]), pw, o[nb]);
+    }
+    // The next step copies over the buffer read here.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+  // The wavefronts' results joined: every one brings its own, then sums a block of 32 channels.
+  __syncthreads();
+  float* const jo = reinterpret_cast<float*>(lds);                      // [wave][16 NB][64]
+  float* const jm = jo + kFewWaves * 16 * NB * 64;                      // [wave][2][64]
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) jo[((wave * NB + nb) * 16 + i) * 64 + lane] = o[nb][i];
+  jm[(wave * 2) * 64 + lane] = run.m;
+  jm[(wave * 2 + 1) * 64 + lane] = half_sum(run.l);
+  __syncthreads();
+  float m = ninf(), l = 0.f, f[kFewWaves];
+#pragma unroll
+  for (int v = 0; v < kFewWaves; ++v) m = __builtin_fmaxf(m, jm[(v * 2) * 64 + lane]);
+  const float mu = m == ninf() ? 0.f : m;
+#pragma unroll
+  for (int v = 0; v < kFewWaves; ++v) {
+    f[v] = exp2_(jm[(v * 2) * 64 + lane] - mu);
+    l += f[v] * jm[(v * 2 + 1) * 64 + lane];
+  }
+  if (wave >= NB) return;
+  float sum[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    sum[i] = 0.f;
+#pragma unroll
+    for (int v = 0; v < kFewWaves; ++v) sum[i] += f[v] * jo[((v * NB + wave) * 16 + i) * 64 + lane];
+  }
+  if (!live) return;
+  const int h = lane >> 5;
+  const int64_t at = (seq * a.hk + kv) * rows + r;                      // row of the parts
+  if (a.splits > 1) {
+    float* const out = a.part_o + ((int64_t)split * a.sequences * a.hk * rows + at) * a.d;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = 32 * wave + 8 * q + 4 * h;
+      if (c < a.d) *reinterpret_cast<f32x4*>(out + c) = (f32x4){sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]};
+    }
+    if (wave == 0 && h == 0) {
+      float* const ml = a.part_ml + ((int64_t)split * a.sequences * a.hk * rows + at) * 2;
+      ml[0] = m;
+      ml[1] = l;
+    }
+    return;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* const out = a.o.p + seq * a.o.b + tok * a.o.t + head * a.o.h;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int c = 32 * wave + 8 * q + 4 * h;
+    if (c < a.d)
+      *reinterpret_cast<u32x2*>(out + c) = (u32x2){pack2<TYPE>(sum[4 * q] * inv, sum[4 * q + 1] * inv),
+                                                   pack2<TYPE>(sum[4 * q + 2] * inv, sum[4 * q + 3] * inv)};
+  }
+  if (a.lse != nullptr && wave == 0 && h == 0)
+    a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Adds up the splits' parts: 4 channels of a row per thread.
+template <int TYPE>
+__global__ void __launch_bounds__(256)
+attn_join_kernel(AttnArgs a) {
+  const int per_row = a.d / 4;
+  const int64_t rows = a.tq * a.group, total = a.sequences * a.hk * rows;
+  const int64_t i = folded_block() * 256 + threadIdx.x, at = i / per_row;
+  if (at >= total) return;
+  const int c = 4 * (int)(i - at * per_row);
+  float m = ninf();
+  for (int s = 0; s < a.splits; ++s) m = __builtin_fmaxf(m, a.part_ml[(s * total + at) * 2]);
+  const float mu = m == ninf() ? 0.f : m;
+  float l = 0.f;
+  f32x4 sum = {0, 0, 0, 0};
+  for (int s = 0; s < a.splits; ++s) {
+    const float* const ml = a.part_ml + (s * total + at) * 2;
+    const float f = exp2_(ml[0] - mu);
+    l += f * ml[1];
+    sum += f * *reinterpret_cast<const f32x4*>(a.part_o + (s * total + at) * a.d + c);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t r = at % rows, kv = at / rows % a.hk, seq = at / rows / a.hk;
+  const int64_t tok = r / a.group, head = kv * a.group + r % a.group;
+  *reinterpret_cast<u32x2*>(a.o.p + seq * a.o.b + tok * a.o.t + head * a.o.h + c) =
+      (u32x2){pack2<TYPE>(sum[0] * inv, sum[1] * inv), pack2<TYPE>(sum[2] * inv, sum[3] * inv)};
+  if (a.lse != nullptr && c == 0)
+    a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+constexpr int kForwardWaves = 4;
+
+template <int TYPE, int NB>
+hipError_t run_forward(AttnArgs a, hipStream_t stream) {
+  if (a.splits > 0) {
+    const int64_t rows = a.tq * a.group;
+    a.groups = a.sequences * a.hk * ((rows + 31) / 32) * a.splits;
+    const hipError_t e = launch(&attn_few_kernel<TYPE, NB>, folded_grid(a.groups), dim3(64 * kFewWaves), stream, a);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t items = a.sequences * a.hk * rows * (a.d / 4);
+    return launch(&attn_join_kernel<TYPE>, folded_grid((items + 255) / 256), dim3(256), stream, a);
+  }
+  constexpr int kQueries = 32 * kForwardWaves;
+  // Packed: as many tiles as the sequences can have, and one for the rows in none.
+  const bool packed = a.q_starts != nullptr;
+  a.tiles = packed ? a.tq / kQueries + a.sequences + 1 : (a.tq + kQueries - 1) / kQueries;
+  a.groups = a.tiles * a.hq * (packed ? 1 : a.sequences);
+  return launch(&attn_forward_kernel<TYPE, NB, kForwardWaves>, folded_grid(a.groups), dim3(64 * kForwardWaves), stream, a);
+}
+
+template <int TYPE>
+hipError_t by_blocks(const AttnArgs& a, hipStream_t stream) {
+  if (a.d <= 32) return run_forward<TYPE, 1>(a, stream);
+  if (a.d <= 64) return run_forward<TYPE, 2>(a, stream);
+  if (a.d <= 96) return run_forward<TYPE, 3>(a, stream);
+  return run_forward<TYPE, 4>(a, stream);
+}
+
+}  // namespace
+
+int attn_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, bool packed) {
+  if (packed || sequences == 0 || tq == 0 || hk == 0) return 0;
+  const int64_t tiles = sequences * hq * ((tq + 127) / 128);            // of the other kernel
+  if (tiles >= 256) return 0;
+  const int64_t rows = tq * (hq / hk), groups = sequences * hk * ((rows + 31) / 32);
+  if (tq > 32 && groups >= 512) return 0;
+  int64_t splits = (768 + groups - 1) / groups;
+  const int64_t most = (tk + 511) / 512;                                // 512 keys at least for each
+  if (splits > most) splits = most;
+  return splits < 1 ? 1 : (int)splits;
+}
+
+hipError_t launch_attention(AttnArgs a, bool fp16, hipStream_t stream) {
+  return fp16 ? by_blocks<kFp16>(a, stream) : by_blocks<kBf16>(a, stream);
+}
+
+}  // namespace rtl

@@ -1,0 +1,112 @@
+"""rtl_attention and its binding on the host, without a GPU: argument checks."""
+import ctypes
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from activation_sparse_gemm_token_amd import attention as at  # noqa: E402
+
+OK, NULLP, SHAPE, MISAL, WS, NODEV, ARCH, HIP, FLAGS = range(9)
+P = 0x10000
+
+
+def _shape(**kw):
+    s = at._Shape(2, 5, 7, 4, 2, 64, None, None, None, 0.125)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def _tensors(n, which, **kw):
+    t = [at._Tensor(P * (i + 1), 1 << 16, 256, 64) for i in range(n)]
+    for k, v in kw.items():
+        setattr(t[which], k, v)
+    return t
+
+
+def _forward(flags=0, ws=None, wsb=0, lse=None, which=0, t=None, **kw):
+    shape = {k: v for k, v in kw.items() if hasattr(at._Shape, k)}
+    tensor = {k: v for k, v in kw.items() if not hasattr(at._Shape, k)}
+    return at._fn("rtl_attention")(*(t or _tensors(4, which, **tensor)), lse, _shape(**shape), ws, wsb, flags, None)
+
+
+def _backward(flags=0, ws=P, wsb=1 << 20, lse=P, which=0, t=None, **kw):
+    shape = {k: v for k, v in kw.items() if hasattr(at._Shape, k)}
+    tensor = {k: v for k, v in kw.items() if not hasattr(at._Shape, k)}
+    t = t or _tensors(8, which, **tensor)
+    return at._fn("rtl_attention_backward")(*t[:5], lse, *t[5:], _shape(**shape), ws, wsb, flags, None)
+
+
+def _no_gpu():
+    return torch.cuda.device_count() == 0
+
+
+BAD_SHAPES = (dict(sequences=-1), dict(tokens_q=-1), dict(tokens_k=-1), dict(heads_q=-1), dict(heads_k=-1), dict(heads_q=5),
+              dict(heads_k=0), dict(head_dim=0), dict(head_dim=4), dict(head_dim=12), dict(head_dim=136),
+              dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(tokens_q=1 << 31), dict(tokens_k=1 << 31),
+              dict(sequences=1 << 31), dict(heads_q=1 << 20, heads_k=1), dict(sequences=1 << 30, tokens_q=1 << 10),
+              dict(q_starts=P, k_starts=P, k_lens=P), dict(token_stride=1 << 23), dict(batch_stride=1 << 40),
+              dict(head_stride=-8), dict(token_stride=260), dict(head_stride=4))
+
+
+@pytest.mark.parametrize("call", [_forward, _backward])
+def test_refusals(call):
+    for bad in BAD_SHAPES:
+        assert call(**bad) == SHAPE, bad
+    for bad in (0x2, 0x40, 0xF, 0x100):
+        assert call(flags=bad) == FLAGS, bad
+    for bad in (dict(q_starts=P), dict(k_starts=P)):
+        assert call(**bad) == NULLP, bad
+    n = 4 if call is _forward else 8
+    for which in range(n):
+        assert call(which=which, data=None) == NULLP
+        assert call(which=which, data=P + 8) == MISAL
+    for bad in (dict(k_lens=P + 2), dict(q_starts=P + 1, k_starts=P)):
+        assert call(**bad) == MISAL, bad
+    assert call(lse=P + 2) == MISAL
+    assert call(ws=P + 8) == MISAL
+
+
+def test_workspaces():
+    assert _backward(lse=None) == NULLP
+    need = 2 * 4 * 5 * 8
+    assert at._fn("rtl_attention_backward_workspace_bytes")(_shape()) == need
+    assert _backward(wsb=need - 1) == WS and _backward(ws=None, wsb=0) == WS
+    assert _backward(flags=1) == FLAGS and _backward(flags=0x20) == FLAGS
+    few = dict(tokens_q=1, tokens_k=100_000)
+    need = at._fn("rtl_attention_workspace_bytes")(_shape(**few))
+    assert need > 0
+    assert _forward(ws=P, wsb=need - 1, **few) == WS and _forward(**few) == WS
+    assert at._fn("rtl_attention_workspace_bytes")(_shape(head_dim=7)) == 0
+    assert at._fn("rtl_attention_workspace_bytes")(_shape(q_starts=P, k_starts=P, **few)) == 0
+
+
+def test_empty_calls_and_valid_ones():
+    for empty in (dict(sequences=0), dict(tokens_q=0), dict(heads_q=0)):
+        assert _forward(data=None, **empty) == OK
+    assert _backward(sequences=0, data=None) == OK
+    if _no_gpu():
+        assert _forward() == NODEV and _backward() == NODEV
+        assert _forward(flags=0x31, lse=P) == NODEV
+        assert _forward(which=1, tokens_k=0, data=None) == NODEV
+        assert _forward(q_starts=P, k_starts=P + 4) == NODEV
+        assert _backward(flags=0x10, q_starts=P, k_starts=P) == NODEV
+
+
+def test_binding_needs_device_tensors_that_fit():
+    q = torch.zeros(2, 5, 4, 64, dtype=torch.bfloat16)
+    k = torch.zeros(2, 7, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        at.attention(q, k, k)                                      # host tensors
+    with pytest.raises(TypeError):
+        at.attention(q.float(), k.float(), k.float())
+    for scale in (-1.0, math.inf, math.nan):
+        with pytest.raises(ValueError):
+            at.attention(q, k, k, scale=scale)
+
+
+def test_structures_match_the_header():
+    assert ctypes.sizeof(at._Tensor) == 32 and ctypes.sizeof(at._Shape) == 80
+    assert at._Shape.scale.offset == 72
