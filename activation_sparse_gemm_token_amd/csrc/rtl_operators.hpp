@@ -158,4 +158,46 @@ int attn_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t h
 hipError_t launch_attention(AttnArgs a, bool fp16, hipStream_t stream);
 hipError_t launch_attention_backward(AttnBackArgs a, hipStream_t stream);
 
+// Dense linears (include/rtlynx_dense.h).
+struct LinearEpi {
+  const uint16_t* bias;
+  const uint16_t* gate;
+  const uint16_t* residual;
+  uint16_t* y;
+  uint16_t* z;
+  int64_t gate_tokens, gate_stride;      // rows of x to a gate row
+  int act;
+};
+struct LinearGemm {                      // [M, N] over K
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;                      // elements
+  int64_t a_bytes, b_bytes;              // of the whole tensors, < 2^31
+  int64_t M, N, K;
+  int tile, splits;                      // tile 0: the kernel for few rows
+  float* part;                           // [splits][M][N]
+  LinearEpi e;
+};
+struct LinearDz {
+  const uint16_t* dy;
+  const uint16_t* z;
+  const uint16_t* gate;
+  uint16_t* dz;                          // [M][np], NULL: sums only
+  float* bias_part;                      // [groups parts][N]
+  float* gate_part;
+  uint16_t* dbias;
+  uint16_t* dgate;
+  int64_t M, N, np, groups, parts, gate_stride;
+  int act;
+};
+struct LinearForm {
+  int tile, splits;
+};
+LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel);
+int64_t linear_dz_parts(int64_t M, int64_t N, int64_t groups);
+hipError_t launch_linear(const LinearGemm& g, bool fp16, hipStream_t stream);
+hipError_t launch_linear_dx(const LinearGemm& g, bool fp16, hipStream_t stream);
+hipError_t launch_linear_dw(const LinearGemm& g, bool fp16, hipStream_t stream);
+hipError_t launch_linear_dz(const LinearDz& a, bool fp16, hipStream_t stream);
+
 }  // namespace rtl
