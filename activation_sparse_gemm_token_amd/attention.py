@@ -39,7 +39,7 @@ class _Shape(ctypes.Structure):
 
 _TP, _SP = ctypes.POINTER(_Tensor), ctypes.POINTER(_Shape)
 _SIGNATURES = {
-    "rtl_attention_workspace_bytes": (_size, [_SP]),
+    "rtl_attention_workspace_bytes": (_size, [_SP, _u32]),
     "rtl_attention": (ctypes.c_int, [_TP] * 4 + [_vp, _SP, _vp, _size, _u32, _vp]),
     "rtl_attention_backward_workspace_bytes": (_size, [_SP]),
     "rtl_attention_backward": (ctypes.c_int, [_TP] * 5 + [_vp] + [_TP] * 3 + [_SP, _vp, _size, _u32, _vp]),
@@ -145,21 +145,22 @@ def _lse_shape(q):
     return (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
 
 
-def workspace_bytes(q, k, q_starts=None) -> int:
-    """Bytes that ``attention`` wants for tensors of these shapes."""
+def _sizes(q, k, q_starts):
     s = _Shape(q.shape[0] if q_starts is None else q_starts.shape[0] - 1, q.shape[-3], k.shape[-3], q.shape[-2], k.shape[-2],
                q.shape[-1], None, None, None, 1.0)
     if q_starts is not None:
         s.q_starts = s.k_starts = 16                      # only whether there are any counts
-    return int(_fn("rtl_attention_workspace_bytes")(s))
+    return s
 
 
-def backward_workspace_bytes(q) -> int:
-    """Bytes that ``attention_backward`` wants for queries of this shape."""
-    n = 8
-    for i in q.shape[:-1]:
-        n *= i
-    return n
+def workspace_bytes(q, k, q_starts=None, causal: bool = False) -> int:
+    """Bytes that ``attention`` wants for tensors of these shapes."""
+    return int(_fn("rtl_attention_workspace_bytes")(_sizes(q, k, q_starts), _CAUSAL if causal else 0))
+
+
+def backward_workspace_bytes(q, k, q_starts=None) -> int:
+    """Bytes that ``attention_backward`` wants for tensors of these shapes."""
+    return int(_fn("rtl_attention_backward_workspace_bytes")(_sizes(q, k, q_starts)))
 
 
 def attention(q, k, v, causal: bool = False, scale: float = None, q_starts=None, k_starts=None, k_lens=None, out=None,
@@ -198,7 +199,7 @@ def attention(q, k, v, causal: bool = False, scale: float = None, q_starts=None,
     lse = torch.empty(_lse_shape(q), dtype=torch.float32, device=q.device) if return_lse else None
     if lse is not None and s.sequences == 0:
         lse.fill_(-math.inf)
-    need = int(_fn("rtl_attention_workspace_bytes")(s))
+    need = int(_fn("rtl_attention_workspace_bytes")(s, flags))
     if workspace is not None or need:
         workspace = _workspace(workspace, need, q.device)
     args = (_tensor(q2), _tensor(k2), _tensor(v2), _tensor(_even(o)), None if lse is None else lse.data_ptr(), s,

@@ -57,20 +57,39 @@ __device__ __forceinline__ float max16(const f32x16& s) {
   return m;
 }
 
-template <int TYPE, int NB, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, 2)
+// Queries and keys of a tile, wavefronts per SIMD.  Two wavefronts with tiles of 64 keys and 236
+// registers leave the matrix cores idle through each other's waits; three fit with 32 keys and 168
+// registers (head_dim 128, 2 x 4608 tokens, 24 heads: 1350 TFLOP/s while all CUs are busy, against 1210).
+constexpr int kForwardWaves = 4, kForwardQueries = 32 * kForwardWaves;
+template <int NB>
+constexpr int forward_keys() { return NB <= 2 ? 64 : 32; }
+template <int NB>
+constexpr int forward_occupancy() { return NB <= 2 ? 4 : 3; }
+
+template <int TYPE, int NB>
+__global__ void __launch_bounds__(64 * kForwardWaves, forward_occupancy<NB>())
 attn_forward_kernel(AttnArgs a) {
   using T = Tile<NB>;
-  constexpr int kKeys = 64, kQueries = 32 * WAVES, kTile = kKeys * T::kPitch;
+  constexpr int kKeys = forward_keys<NB>(), kKb = kKeys / 32, kTile = kKeys * T::kPitch;
   __shared__ __attribute__((aligned(16))) char lds[4 * kTile];          // K, V of two steps
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t id = folded_block();
+  if (id >= a.groups) return;
+  // The first workgroups take whole tiles, the others a part of the keys of one (launch_attention).
+  int part = -1;
+  int64_t part_tile = 0;
+  if (id < a.whole) {
+    id = xcd_order(id, a.whole);
+  } else {
+    part_tile = (id - a.whole) / a.splits;
+    part = (int)(id - a.whole - part_tile * a.splits);
+    id = a.whole + part_tile;
+  }
   QueryWork w;
-  if (folded_block() >= a.groups) return;
-  const int64_t id = xcd_order(folded_block(), a.groups);
-  if (!query_work(a, id, kQueries, w)) {
+  if (!query_work(a, id, kForwardQueries, w)) {
     // No tile left: some rows may lie in no sequence.
     const int64_t used = (id % a.tiles) - w.tile, spare = a.tiles - used;
-    rest_rows(a.q_starts, a.sequences, a.tq, w.tile * 64 * WAVES + threadIdx.x, spare * 64 * WAVES, [&](int64_t row) {
+    rest_rows(a.q_starts, a.sequences, a.tq, w.tile * 256 + threadIdx.x, spare * 256, [&](int64_t row) {
       if (a.lse != nullptr) a.lse[w.head * a.tq + row] = ninf();
       if (a.zero_rest) {
         uint16_t* p = a.o.p + row * a.o.t + w.head * a.o.h;
@@ -79,10 +98,10 @@ attn_forward_kernel(AttnArgs a) {
     });
     return;
   }
-  const int64_t q0 = w.tile * kQueries + 32 * wave, shift = w.k.len - w.q.len;
+  const int64_t q0 = w.tile * kForwardQueries + 32 * wave, shift = w.k.len - w.q.len;
   const int64_t row = q0 + (lane & 31);
-  // Keys that the tile, and this wavefront, see; keys that all of its queries see.
-  const int64_t tile_end = (w.tile + 1) * kQueries < w.q.len ? (w.tile + 1) * kQueries : w.q.len;
+  // Keys that the tile, and this wavefront, see; keys that all of its queries see; this lane's.
+  const int64_t tile_end = (w.tile + 1) * kForwardQueries < w.q.len ? (w.tile + 1) * kForwardQueries : w.q.len;
   const int64_t wave_end = q0 + 32 < w.q.len ? q0 + 32 : w.q.len;
   int64_t keys = w.k.len, mine = q0 < w.q.len ? w.k.len : 0, all = w.k.len, limit = w.k.len;
   if (a.causal) {
@@ -91,22 +110,35 @@ attn_forward_kernel(AttnArgs a) {
     all = q0 + shift + 1 < all ? q0 + shift + 1 : all;
     limit = row + shift + 1 < limit ? row + shift + 1 : limit;
   }
-  const int steps = keys > 0 ? (int)((keys + kKeys - 1) / kKeys) : 0;
+  // Steps [from, steps) of the workgroup, below my_steps of the wavefront, hidden keys from cut_step on.
+  int from = 0, steps = keys > 0 ? (int)((keys + kKeys - 1) / kKeys) : 0;
+  const int my_steps = mine > 0 ? (int)((mine + kKeys - 1) / kKeys) : 0, cut_step = all > 0 ? (int)(all / kKeys) : 0;
+  if (part >= 0) {
+    const int per = (steps + a.splits - 1) / a.splits;
+    from = part * per;
+    steps = from + per < steps ? from + per : steps;
+  }
 
-  TileCopy<NB, kKeys, WAVES> ck, cv;
+  TileCopy<NB, kKeys, kForwardWaves> ck, cv;
   ck.init(wave, a.k.t, a.d);
   cv.init(wave, a.v.t, a.d);
   const uint32_t lds0 = lds_address(lds);
+  const uint16_t* kp = w.kp + (int64_t)from * kKeys * a.k.t;
+  const uint16_t* vp = w.vp + (int64_t)from * kKeys * a.v.t;
+  int64_t left = w.k.len - (int64_t)from * kKeys;       // keys from the next copy's first on
   auto copy = [&](int j) {
-    const int64_t at = (int64_t)j * kKeys;
     const uint32_t buf = lds0 + (j & 1) * 2 * kTile;
-    ck.run(w.kp + at * a.k.t, w.k.len - at, buf);
-    cv.run(w.vp + at * a.v.t, w.k.len - at, buf + kTile);
+    ck.run(kp, clamp_rows(left), buf);
+    cv.run(vp, clamp_rows(left), buf + kTile);
+    kp += kKeys * a.k.t;
+    vp += kKeys * a.v.t;
+    left -= kKeys;
   };
-  if (steps > 0) copy(0);
+  if (from < steps) copy(from);
 
   u32x4 qf[2 * NB];
   load_rows<NB>(a.q.p + w.q_off + q0 * a.q.t, a.q.t, w.q.len - q0, a.d, qf);
+  settle(qf);
   f32x16 o[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) o[nb] = zero16();
@@ -121,32 +153,32 @@ attn_forward_kernel(AttnArgs a) {
     col_off[nb][1] = T::column_operand(nb, 1);
   }
 
-  for (int j = 0; j < steps; ++j) {
+  for (int j = from; j < steps; ++j) {
     wait_copies<0>();
     group_barrier();                                    // tile j is whole, tile j - 1 is no longer read
     if (j + 1 < steps) copy(j + 1);
-    const int64_t k0 = (int64_t)j * kKeys;
-    if (k0 >= mine) continue;
+    if (j >= my_steps) continue;
     const char* const kt = lds + (j & 1) * 2 * kTile;
     const char* const vt = kt + kTile;
-    f32x16 s[2];
+    f32x16 s[kKb];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < kKb; ++kb) {
       s[kb] = zero16();
 #pragma unroll
       for (int c = 0; c < 2 * NB; ++c) s[kb] = mfma32<TYPE>(lds_read16(kt + kb * 32 * T::kPitch + row_off[c]), qf[c], s[kb]);
     }
-    if (k0 + kKeys > all) {
-      const int left = (int)(limit < k0 ? 0 : limit - k0 < kKeys ? limit - k0 : kKeys);
+    if (j >= cut_step) {
+      const int seen = clamp_rows(limit - (int64_t)j * kKeys);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < kKb; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][i] = 32 * kb + block_row(i) < left ? s[kb][i] : ninf();
+        for (int i = 0; i < 16; ++i) s[kb][i] = 32 * kb + block_row(i) < seen ? s[kb][i] : ninf();
     }
-    const float top = half_max(__builtin_fmaxf(max16(s[0]), max16(s[1]))) * a.c;
-    move_maximum<NB>(run, top, o);
+    float top = max16(s[0]);
+    if constexpr (kKb == 2) top = __builtin_fmaxf(top, max16(s[kKb - 1]));
+    move_maximum<NB>(run, half_max(top) * a.c, o);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < kKb; ++kb) {
       f32x16 p;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -163,9 +195,28 @@ attn_forward_kernel(AttnArgs a) {
     }
   }
   const float l = half_sum(run.l);
-  const int64_t left = w.q.len - q0;
-  store_rows<TYPE, NB>(a.o.p + w.o_off + q0 * a.o.t, a.o.t, left, a.d, o, l == 0.f ? 0.f : 1.f / l);
-  if (a.lse != nullptr && lane < 32 && lane < left)
+  const int64_t rows = w.q.len - q0;
+  if (part >= 0) {
+    const int r = 32 * wave + (lane & 31), h = lane >> 5;
+    const int64_t at = (part_tile * a.splits + part) * kForwardQueries + r;
+    if ((lane & 31) >= rows) return;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = 32 * nb + 8 * q + 4 * h;
+        if (c < a.d)
+          *reinterpret_cast<f32x4*>(a.part_o + at * a.d + c) =
+              (f32x4){o[nb][4 * q], o[nb][4 * q + 1], o[nb][4 * q + 2], o[nb][4 * q + 3]};
+      }
+    if (h == 0) {
+      a.part_ml[2 * at] = run.m;
+      a.part_ml[2 * at + 1] = l;
+    }
+    return;
+  }
+  store_rows<TYPE, NB>(a.o.p + w.o_off + q0 * a.o.t, a.o.t, rows, a.d, o, l == 0.f ? 0.f : 1.f / l);
+  if (a.lse != nullptr && lane < 32 && lane < rows)
     a.lse[w.lse_off + row] = l == 0.f ? ninf() : (run.mu + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
@@ -215,8 +266,8 @@ attn_few_kernel(AttnArgs a) {
   char* const mine = lds + wave * kWaveBytes;
   const uint32_t lds0 = lds_address(mine);
   auto copy = [&](int64_t at, int buf) {
-    ck.run(kp + at * a.k.t, len - at, lds0 + buf * 2 * kTile);
-    cv.run(vp + at * a.v.t, len - at, lds0 + buf * 2 * kTile + kTile);
+    ck.run(kp + at * a.k.t, clamp_rows(len - at), lds0 + buf * 2 * kTile);
+    cv.run(vp + at * a.v.t, clamp_rows(len - at), lds0 + buf * 2 * kTile + kTile);
   };
   const int64_t first = lo + kFewKeys * wave;
   if (first < hi) copy(first, 0);
@@ -227,6 +278,7 @@ attn_few_kernel(AttnArgs a) {
     const int ch = 16 * c + 8 * (lane >> 5);
     if (live && ch < a.d) qf[c] = *reinterpret_cast<const u32x4*>(a.q.p + seq * a.q.b + tok * a.q.t + head * a.q.h + ch);
   }
+  settle(qf);
   f32x16 o[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) o[nb] = zero16();
@@ -335,79 +387,127 @@ attn_few_kernel(AttnArgs a) {
     a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Adds up the splits' parts: 4 channels of a row per thread.
-template <int TYPE>
+// Adds up the splits' parts: 4 channels of a row per thread.  TILES: parts [tile][split][row] of the
+// last tiles of attn_forward_kernel, else [split][row] of attn_few_kernel.
+template <int TYPE, bool TILES>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(AttnArgs a) {
   const int per_row = a.d / 4;
-  const int64_t rows = a.tq * a.group, total = a.sequences * a.hk * rows;
   const int64_t i = folded_block() * 256 + threadIdx.x, at = i / per_row;
-  if (at >= total) return;
   const int c = 4 * (int)(i - at * per_row);
+  int64_t first, step, seq, head, tok;                  // rows of the parts; the query
+  if constexpr (TILES) {
+    const int64_t tile = at / kForwardQueries, r = at - tile * kForwardQueries;
+    if (tile >= (a.groups - a.whole) / a.splits) return;
+    first = tile * a.splits * kForwardQueries + r;
+    step = kForwardQueries;
+    const int64_t id = a.whole + tile, item = id / a.tiles, t = id - item * a.tiles;
+    tok = (a.causal ? a.tiles - 1 - t : t) * kForwardQueries + r;
+    if (tok >= a.tq) return;
+    seq = item / a.hq;
+    head = item - seq * a.hq;
+  } else {
+    const int64_t rows = a.tq * a.group, total = a.sequences * a.hk * rows;
+    if (at >= total) return;
+    first = at;
+    step = total;
+    const int64_t r = at % rows, kv = at / rows % a.hk;
+    seq = at / rows / a.hk;
+    tok = r / a.group;
+    head = kv * a.group + r % a.group;
+  }
   float m = ninf();
-  for (int s = 0; s < a.splits; ++s) m = __builtin_fmaxf(m, a.part_ml[(s * total + at) * 2]);
+  for (int s = 0; s < a.splits; ++s) m = __builtin_fmaxf(m, a.part_ml[(first + s * step) * 2]);
   const float mu = m == ninf() ? 0.f : m;
   float l = 0.f;
   f32x4 sum = {0, 0, 0, 0};
   for (int s = 0; s < a.splits; ++s) {
-    const float* const ml = a.part_ml + (s * total + at) * 2;
+    const float* const ml = a.part_ml + (first + s * step) * 2;
     const float f = exp2_(ml[0] - mu);
     l += f * ml[1];
-    sum += f * *reinterpret_cast<const f32x4*>(a.part_o + (s * total + at) * a.d + c);
+    sum += f * *reinterpret_cast<const f32x4*>(a.part_o + (first + s * step) * a.d + c);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t r = at % rows, kv = at / rows % a.hk, seq = at / rows / a.hk;
-  const int64_t tok = r / a.group, head = kv * a.group + r % a.group;
   *reinterpret_cast<u32x2*>(a.o.p + seq * a.o.b + tok * a.o.t + head * a.o.h + c) =
       (u32x2){pack2<TYPE>(sum[0] * inv, sum[1] * inv), pack2<TYPE>(sum[2] * inv, sum[3] * inv)};
   if (a.lse != nullptr && c == 0)
     a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-constexpr int kForwardWaves = 4;
-
 template <int TYPE, int NB>
-hipError_t run_forward(AttnArgs a, hipStream_t stream) {
-  if (a.splits > 0) {
+hipError_t run_forward(AttnArgs a, const AttnPlan& plan, hipStream_t stream) {
+  a.splits = plan.splits;
+  if (plan.few) {
     const int64_t rows = a.tq * a.group;
     a.groups = a.sequences * a.hk * ((rows + 31) / 32) * a.splits;
     const hipError_t e = launch(&attn_few_kernel<TYPE, NB>, folded_grid(a.groups), dim3(64 * kFewWaves), stream, a);
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t items = a.sequences * a.hk * rows * (a.d / 4);
-    return launch(&attn_join_kernel<TYPE>, folded_grid((items + 255) / 256), dim3(256), stream, a);
+    return launch(&attn_join_kernel<TYPE, false>, folded_grid((items + 255) / 256), dim3(256), stream, a);
   }
-  constexpr int kQueries = 32 * kForwardWaves;
   // Packed: as many tiles as the sequences can have, and one for the rows in none.
   const bool packed = a.q_starts != nullptr;
-  a.tiles = packed ? a.tq / kQueries + a.sequences + 1 : (a.tq + kQueries - 1) / kQueries;
-  a.groups = a.tiles * a.hq * (packed ? 1 : a.sequences);
-  return launch(&attn_forward_kernel<TYPE, NB, kForwardWaves>, folded_grid(a.groups), dim3(64 * kForwardWaves), stream, a);
+  a.tiles = packed ? a.tq / kForwardQueries + a.sequences + 1 : (a.tq + kForwardQueries - 1) / kForwardQueries;
+  const int64_t tiles = a.tiles * a.hq * (packed ? 1 : a.sequences);
+  a.whole = tiles - plan.tail;
+  a.groups = a.whole + plan.tail * a.splits;
+  const hipError_t e = launch(&attn_forward_kernel<TYPE, NB>, folded_grid(a.groups), dim3(64 * kForwardWaves), stream, a);
+  if (e != hipSuccess || plan.tail == 0) return e;
+  const int64_t items = plan.tail * kForwardQueries * (a.d / 4);
+  return launch(&attn_join_kernel<TYPE, true>, folded_grid((items + 255) / 256), dim3(256), stream, a);
 }
 
 template <int TYPE>
-hipError_t by_blocks(const AttnArgs& a, hipStream_t stream) {
-  if (a.d <= 32) return run_forward<TYPE, 1>(a, stream);
-  if (a.d <= 64) return run_forward<TYPE, 2>(a, stream);
-  if (a.d <= 96) return run_forward<TYPE, 3>(a, stream);
-  return run_forward<TYPE, 4>(a, stream);
+hipError_t by_blocks(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
+  if (a.d <= 32) return run_forward<TYPE, 1>(a, plan, stream);
+  if (a.d <= 64) return run_forward<TYPE, 2>(a, plan, stream);
+  if (a.d <= 96) return run_forward<TYPE, 3>(a, plan, stream);
+  return run_forward<TYPE, 4>(a, plan, stream);
 }
 
 }  // namespace
 
-int attn_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, bool packed) {
-  if (packed || sequences == 0 || tq == 0 || hk == 0) return 0;
-  const int64_t tiles = sequences * hq * ((tq + 127) / 128);            // of the other kernel
-  if (tiles >= 256) return 0;
-  const int64_t rows = tq * (hq / hk), groups = sequences * hk * ((rows + 31) / 32);
-  if (tq > 32 && groups >= 512) return 0;
-  int64_t splits = (768 + groups - 1) / groups;
-  const int64_t most = (tk + 511) / 512;                                // 512 keys at least for each
-  if (splits > most) splits = most;
-  return splits < 1 ? 1 : (int)splits;
+// Up to 32 queries of a sequence go to attn_few_kernel, its keys in ranges of at least 512 until there
+// are three workgroups per CU.  Otherwise tiles of 128 queries; a batch's tiles are alike, so where their
+// number is no multiple of what the card holds (256 CUs times the wavefronts per SIMD) the last, partly
+// filled round would leave CUs idle: the keys of its tiles are split over workgroups, 256 keys at least for
+// each.  Causal tiles shrink towards the end by themselves, and packed ones differ anyway.
+AttnPlan attn_plan(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, int64_t d, bool packed, bool causal) {
+  AttnPlan p{false, 1, 0};
+  if (packed || sequences == 0 || tq == 0 || hk == 0 || hq == 0) return p;
+  if (tq <= 32) {
+    const int64_t rows = tq * (hq / hk), groups = sequences * hk * ((rows + 31) / 32);
+    int64_t splits = (768 + groups - 1) / groups;
+    const int64_t most = (tk + 511) / 512;
+    if (splits > most) splits = most;
+    p.few = true;
+    p.splits = splits < 1 ? 1 : (int)splits;
+    return p;
+  }
+  if (causal) return p;
+  const int64_t slots = 256 * (d <= 64 ? forward_occupancy<2>() : forward_occupancy<4>());
+  const int64_t tiles = sequences * hq * ((tq + kForwardQueries - 1) / kForwardQueries), tail = tiles % slots;
+  if (tail == 0) return p;
+  int64_t splits = slots / tail;
+  if (splits > tk / 256) splits = tk / 256;
+  if (splits > 16) splits = 16;
+  if (splits >= 2) {
+    p.splits = (int)splits;
+    p.tail = tail;
+  }
+  return p;
 }
 
-hipError_t launch_attention(AttnArgs a, bool fp16, hipStream_t stream) {
-  return fp16 ? by_blocks<kFp16>(a, stream) : by_blocks<kBf16>(a, stream);
+size_t attn_plan_bytes(const AttnPlan& p, int64_t sequences, int64_t tq, int64_t hq, int64_t d) {
+  if (p.splits <= 1) return 0;
+  return (size_t)p.splits * (size_t)(p.few ? sequences * hq * tq : p.tail * kForwardQueries) * (size_t)(d + 2) * 4;
+}
+
+hipError_t launch_attention(AttnArgs a, const AttnPlan& plan, bool fp16, void* workspace, hipStream_t stream) {
+  const int64_t rows = plan.few ? a.sequences * a.hq * a.tq : plan.tail * kForwardQueries;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = plan.splits > 1 ? a.part_o + plan.splits * rows * a.d : nullptr;
+  return fp16 ? by_blocks<kFp16>(a, plan, stream) : by_blocks<kBf16>(a, plan, stream);
 }
 
 }  // namespace rtl

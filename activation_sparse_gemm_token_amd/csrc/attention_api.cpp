@@ -49,17 +49,28 @@ rtl::AttnTensor tensor(const rtl_attn_tensor* t) {
   return {static_cast<uint16_t*>(t->data), t->batch_stride, t->token_stride, t->head_stride};
 }
 
-int splits_of(const rtl_attn_shape* s) {
-  return rtl::attn_splits(s->sequences, s->tokens_q, s->tokens_k, s->heads_q, s->heads_k, s->q_starts != nullptr);
+rtl::AttnPlan plan_of(const rtl_attn_shape* s, bool causal) {
+  return rtl::attn_plan(s->sequences, s->tokens_q, s->tokens_k, s->heads_q, s->heads_k, s->head_dim, s->q_starts != nullptr,
+                        causal);
 }
 
-size_t forward_bytes(const rtl_attn_shape* s) {
-  const int splits = splits_of(s);
-  if (splits <= 1) return 0;
-  return (size_t)splits * (size_t)(s->sequences * s->heads_q * s->tokens_q) * (size_t)(s->head_dim + 2) * 4;
+size_t plan_bytes(const rtl::AttnPlan& p, const rtl_attn_shape* s) {
+  return rtl::attn_plan_bytes(p, s->sequences, s->tokens_q, s->heads_q, s->head_dim);
 }
 
 int64_t query_rows(const rtl_attn_shape* s) { return (s->q_starts != nullptr ? 1 : s->sequences) * s->heads_q * s->tokens_q; }
+
+int back_splits(const rtl_attn_shape* s) {
+  return rtl::attn_back_splits(s->sequences, s->tokens_q, s->tokens_k, s->heads_q, s->heads_k, s->q_starts != nullptr);
+}
+
+size_t stats_bytes(const rtl_attn_shape* s) { return ((size_t)query_rows(s) * 8 + 15) / 16 * 16; }
+
+size_t backward_bytes(const rtl_attn_shape* s) {
+  const int splits = back_splits(s);
+  const size_t rows = (size_t)((s->q_starts != nullptr ? 1 : s->sequences) * s->tokens_k * s->heads_k);
+  return stats_bytes(s) + (splits > 1 ? (size_t)splits * 2 * rows * (size_t)s->head_dim * 4 : 0);
+}
 
 rtl::AttnArgs arguments(const rtl_attn_shape* s, uint32_t flags) {
   rtl::AttnArgs a{};
@@ -84,8 +95,8 @@ rtl::AttnArgs arguments(const rtl_attn_shape* s, uint32_t flags) {
 
 }  // namespace
 
-RTL_API size_t rtl_attention_workspace_bytes(const rtl_attn_shape* shape) {
-  return check_shape(shape) == RTL_OK ? forward_bytes(shape) : 0;
+RTL_API size_t rtl_attention_workspace_bytes(const rtl_attn_shape* shape, uint32_t flags) {
+  return check_shape(shape) == RTL_OK ? plan_bytes(plan_of(shape, (flags & RTL_ATTN_CAUSAL) != 0), shape) : 0;
 }
 
 RTL_API rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor* k, const rtl_attn_tensor* v,
@@ -103,7 +114,8 @@ RTL_API rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor
   }
   if (!any) return RTL_OK;
   if (!rtl::aligned(lse, 4) || !rtl::aligned(workspace, 16)) return RTL_ERR_MISALIGNED;
-  const size_t need = forward_bytes(shape);
+  const rtl::AttnPlan plan = plan_of(shape, (flags & RTL_ATTN_CAUSAL) != 0);
+  const size_t need = plan_bytes(plan, shape);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return RTL_ERR_WORKSPACE;
   rtl::AttnArgs a = arguments(shape, flags);
   a.q = tensor(q);
@@ -111,17 +123,14 @@ RTL_API rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor
   a.v = tensor(v);
   a.o = tensor(o);
   a.lse = lse;
-  a.splits = splits_of(shape);
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = need > 0 ? a.part_o + (size_t)a.splits * (size_t)query_rows(shape) * (size_t)a.d : nullptr;
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   st = rtl::check_device(stream);
   if (st != RTL_OK) return st;
-  return rtl::from_hip(rtl::launch_attention(a, (flags & 0xFu) == RTL_ATTN_FP16, stream));
+  return rtl::from_hip(rtl::launch_attention(a, plan, (flags & 0xFu) == RTL_ATTN_FP16, workspace, stream));
 }
 
 RTL_API size_t rtl_attention_backward_workspace_bytes(const rtl_attn_shape* shape) {
-  return check_shape(shape) == RTL_OK ? (size_t)query_rows(shape) * 8 : 0;
+  return check_shape(shape) == RTL_OK ? backward_bytes(shape) : 0;
 }
 
 RTL_API rtl_status rtl_attention_backward(const rtl_attn_tensor* d_o, const rtl_attn_tensor* q, const rtl_attn_tensor* k,
@@ -142,8 +151,8 @@ RTL_API rtl_status rtl_attention_backward(const rtl_attn_tensor* d_o, const rtl_
   if (!any_q && !any_k) return RTL_OK;
   if (any_q && lse == nullptr) return RTL_ERR_NULL_POINTER;
   if (!rtl::aligned(lse, 4) || !rtl::aligned(workspace, 16)) return RTL_ERR_MISALIGNED;
-  const size_t rows = any_q ? (size_t)query_rows(shape) : 0;
-  if (rows > 0 && (workspace == nullptr || workspace_bytes < rows * 8)) return RTL_ERR_WORKSPACE;
+  const size_t need = backward_bytes(shape);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return RTL_ERR_WORKSPACE;
   rtl::AttnBackArgs a{};
   a.f = arguments(shape, flags);
   a.f.q = tensor(q);
@@ -155,8 +164,9 @@ RTL_API rtl_status rtl_attention_backward(const rtl_attn_tensor* d_o, const rtl_
   a.dq = tensor(dq);
   a.dk = tensor(dk);
   a.dv = tensor(dv);
-  a.lse2 = static_cast<float*>(workspace);
-  a.delta = a.lse2 + rows;
+  a.stats = static_cast<rtl::f32x2*>(workspace);
+  a.f.splits = back_splits(shape);
+  a.f.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(shape));
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   st = rtl::check_device(stream);
   if (st != RTL_OK) return st;

@@ -1,7 +1,7 @@
 // Attention, backward (include/rtlynx_attention.h).
 //
-//   1. attn_delta_kernel   D = sum of d_o o per query and head, and the log-sum-exp in
-//                          log2 units.
+//   1. attn_delta_kernel   D = sum of d_o o per query and head, beside the log-sum-exp in
+//                          log2 units (+inf where no key is seen: p is 0 then).
 //   2. attn_dkv_kernel     dK, dV: a wavefront holds 32 keys, its workgroup walks the
 //                          queries of all heads that share the key head.
 //   3. attn_dq_kernel      dQ: as the forward pass, 32 queries a wavefront.
@@ -44,25 +44,28 @@ attn_delta_kernel(AttnBackArgs a) {
 #pragma unroll
   for (int d = 8; d >= 1; d /= 2) s += __shfl_xor(s, d, 16);
   if (lane == 0) {
-    a.delta[at] = s;
     const float l = a.f.lse[at];
-    a.lse2[at] = l == -__builtin_inff() ? __builtin_inff() : l * kLog2e;
+    a.stats[at] = (f32x2){l == -__builtin_inff() ? __builtin_inff() : l * kLog2e, s};
   }
 }
 
 // --- dK, dV -------------------------------------------------------------------
+// K of a wavefront's 32 keys stays in registers, V in LDS (both in registers, with dK and dV, take more than
+// 256: one wavefront per SIMD, 200 moves between register files for every 32 matrix
+// instructions, and half the speed); queries come 32 at a time.
 constexpr int kKvWaves = 4, kKvKeys = 32 * kKvWaves;
 
 template <int NB>
-__global__ void __launch_bounds__(64 * kKvWaves, 1)
+__global__ void __launch_bounds__(64 * kKvWaves, 2)
 attn_dkv_kernel(AttnBackArgs a) {
   using T = Tile<NB>;
-  constexpr int kQueries = 64, kTile = kQueries * T::kPitch, kStage = 2 * kTile + 512;
-  __shared__ __attribute__((aligned(16))) char lds[2 * kStage];         // Q, dO, lse2, delta of two steps
+  constexpr int kQueries = 32, kTile = kQueries * T::kPitch, kStage = 2 * kTile + 256, kVBytes = kKvKeys * T::kPitch;
+  __shared__ __attribute__((aligned(16))) char lds[kVBytes + 2 * kStage];   // V; Q, dO and their statistics of two steps
   const AttnArgs& f = a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (folded_block() >= f.groups) return;
-  const int64_t id = xcd_order(folded_block(), f.groups);
+  const int64_t block = xcd_order(folded_block(), f.groups), id = block / f.splits;
+  const int split = (int)(block - id * f.splits);
   int64_t item = id / f.tiles, t = id - item * f.tiles, seq = 0;
   const bool packed = f.q_starts != nullptr;
   Span qs, ks;
@@ -76,6 +79,12 @@ attn_dkv_kernel(AttnBackArgs a) {
     if (!found) {
       const int64_t spare = f.tiles - (given - t);
       rest_rows(f.k_starts, f.sequences, f.tk, t * 64 * kKvWaves + threadIdx.x, spare * 64 * kKvWaves, [&](int64_t row) {
+        if (f.splits > 1) {
+          float* p = f.part_o + ((split * 2 * f.tk + row) * f.hk + kv) * f.d;
+          for (int c = 0; c < f.d; c += 4)
+            *reinterpret_cast<f32x4*>(p + c) = *reinterpret_cast<f32x4*>(p + f.tk * f.hk * f.d + c) = (f32x4){0, 0, 0, 0};
+          return;
+        }
         uint16_t* p = a.dk.p + row * a.dk.t + kv * a.dk.h;
         uint16_t* q = a.dv.p + row * a.dv.t + kv * a.dv.h;
         for (int c = 0; c < f.d; c += 8)
@@ -103,27 +112,29 @@ attn_dkv_kernel(AttnBackArgs a) {
   if (f.causal && t * kKvKeys - shift > 0) from = (t * kKvKeys - shift) / kQueries * kQueries;
   if (t * kKvKeys >= ks.len) from = qs.len;             // behind the filled rows: zeros
   const int64_t per_head = from < qs.len ? (qs.len - from + kQueries - 1) / kQueries : 0;
-  const int64_t steps = per_head * f.group;
+  // Step j: head head0 + j / per_head, queries from + 32 (j % per_head) on; this workgroup's are [lo, steps).
+  int64_t steps = per_head * f.group;
+  const int64_t per_split = (steps + f.splits - 1) / f.splits, lo = split * per_split;
+  steps = lo + per_split < steps ? lo + per_split : steps;
 
   TileCopy<NB, kQueries, kKvWaves> cq, cd;
   cq.init(wave, f.q.t, f.d);
   cd.init(wave, a.d_o.t, f.d);
-  const uint32_t lds0 = lds_address(lds);
+  const uint32_t lds0 = lds_address(lds) + kVBytes;
   const int64_t head0 = kv * f.group;
-  // Step j: head head0 + j / per_head, queries from + 64 (j % per_head) on.
-  int64_t copy_head = 0, copy_at = from;
+  int64_t copy_head = lo < steps ? lo / per_head : 0, copy_at = lo < steps ? from + (lo - copy_head * per_head) * kQueries : from;
   auto copy = [&](int buf) {
     const int64_t head = head0 + copy_head, left = qs.len - copy_at;
     const uint32_t to = lds0 + buf * kStage;
-    cq.run(f.q.p + b * f.q.b + (qs.start + copy_at) * f.q.t + head * f.q.h, left, to);
-    cd.run(a.d_o.p + b * a.d_o.b + (qs.start + copy_at) * a.d_o.t + head * a.d_o.h, left, to + kTile);
-    // Wavefront 0 brings lse2, wavefront 1 delta: 64 values, zeros past the sequence (with Q and dO
-    // zero there, P = 1 and dS = 0 add nothing).
-    if (wave < 2) {
+    cq.run(f.q.p + b * f.q.b + (qs.start + copy_at) * f.q.t + head * f.q.h, clamp_rows(left), to);
+    cd.run(a.d_o.p + b * a.d_o.b + (qs.start + copy_at) * a.d_o.t + head * a.d_o.h, clamp_rows(left), to + kTile);
+    // Wavefront 0 brings the statistics, zeros past the sequence (with Q and dO zero there, P = 1 and
+    // dS = 0 add nothing).
+    if (wave == 0) {
       const int64_t at = (packed ? head * f.tq : (seq * f.hq + head) * f.tq) + qs.start + copy_at;
-      const __amdgpu_buffer_rsrc_t rs = make_rsrc((wave == 0 ? a.lse2 : a.delta) + at, 256);
-      const uint32_t off = lane < left ? 4 * lane : kOobOffset;
-      const uint32_t dst = __builtin_amdgcn_readfirstlane(to + 2 * kTile + 256 * wave);
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.stats + at, 256);
+      const uint32_t off = lane / 2 < left ? 4 * lane : kOobOffset;
+      const uint32_t dst = __builtin_amdgcn_readfirstlane(to + 2 * kTile);
       uint32_t saved;
       asm volatile(
           "s_nop 4\n\ts_mov_b32 %[sv], m0\n\ts_mov_b32 m0, %[l0]\n\ts_nop 0\n\t"
@@ -136,11 +147,17 @@ attn_dkv_kernel(AttnBackArgs a) {
     copy_at += kQueries;
     if (copy_at >= qs.len) copy_at = from, ++copy_head;
   };
-  if (steps > 0) copy(0);
+  int64_t q0 = copy_at;
+  if (lo < steps) copy((int)(lo & 1));
 
-  u32x4 kf[2 * NB], vf[2 * NB];
+  {
+    TileCopy<NB, kKvKeys, kKvWaves> cv;
+    cv.init(wave, f.v.t, f.d);
+    cv.run(f.v.p + b * f.v.b + (ks.start + t * kKvKeys) * f.v.t + kv * f.v.h, clamp_rows(ks.len - t * kKvKeys), lds_address(lds));
+  }
+  u32x4 kf[2 * NB];
   load_rows<NB>(f.k.p + b * f.k.b + (ks.start + k0) * f.k.t + kv * f.k.h, f.k.t, ks.len - k0, f.d, kf);
-  load_rows<NB>(f.v.p + b * f.v.b + (ks.start + k0) * f.v.t + kv * f.v.h, f.v.t, ks.len - k0, f.d, vf);
+  settle(kf);
   f32x16 dk[NB], dv[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) dk[nb] = dv[nb] = zero16();
@@ -154,59 +171,98 @@ attn_dkv_kernel(AttnBackArgs a) {
   }
   const bool dead = key >= ks.len;                      // this lane's key does not exist
   const bool any_dead = k0 + 32 > ks.len;
-  int64_t q0 = from;
-  for (int64_t j = 0; j < steps; ++j) {
+  const char* const vt = lds + wave * 32 * T::kPitch;
+  for (int64_t j = lo; j < steps; ++j) {
     wait_copies<0>();
     group_barrier();
     if (j + 1 < steps) copy((int)((j + 1) & 1));
-    const char* const qt = lds + (j & 1) * kStage;
+    const char* const qt = lds + kVBytes + (j & 1) * kStage;
     const char* const dt = qt + kTile;
-    const float* const lt = reinterpret_cast<const float*>(dt + kTile);
-    // First query that sees this lane's key; whether all of the step's see all of the wavefront's.
-    const int64_t first = f.causal ? key - shift - q0 : 0;
-    const bool cut = any_dead || (f.causal && k0 + 31 - shift > q0);
+    const float* const st = reinterpret_cast<const float*>(dt + kTile);
     if (k0 < ks.len && !(f.causal && k0 - shift >= q0 + kQueries)) {
+      f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb) {
-        const char* const qb = qt + rb * 32 * T::kPitch;
-        const char* const db = dt + rb * 32 * T::kPitch;
-        f32x16 s = zero16(), dp = zero16();
+      for (int c = 0; c < 2 * NB; ++c) s = mfma32<kBf16>(lds_read16(qt + row_off[c]), kf[c], s);
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) s = mfma32<kBf16>(lds_read16(qb + row_off[c]), kf[c], s);
+      for (int c = 0; c < 2 * NB; ++c) dp = mfma32<kBf16>(lds_read16(dt + row_off[c]), lds_read16(vt + row_off[c]), dp);
+      // Hidden scores: keys that do not exist, and queries before the first one that sees the lane's key.
+      if (any_dead || (f.causal && k0 + 31 - shift > q0)) {
+        const int first = dead ? kQueries : f.causal ? clamp_rows(key - shift - q0) : 0;
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) dp = mfma32<kBf16>(lds_read16(db + row_off[c]), vf[c], dp);
+        for (int i = 0; i < 16; ++i) s[i] = block_row(i) < first ? -__builtin_inff() : s[i];
+      }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 32 * rb + 8 * q + 4 * (lane >> 5);
-          const f32x4 l4 = *reinterpret_cast<const f32x4*>(lt + r), d4 = *reinterpret_cast<const f32x4*>(lt + 64 + r);
+      for (int q = 0; q < 4; ++q) {
+        const float* const r = st + 2 * (8 * q + 4 * (lane >> 5));
+        const f32x4 s0 = *reinterpret_cast<const f32x4*>(r), s1 = *reinterpret_cast<const f32x4*>(r + 4);
+        const float l4[4] = {s0[0], s0[2], s1[0], s1[2]}, d4[4] = {s0[1], s0[3], s1[1], s1[3]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float p = exp2_(__builtin_fmaf(s[4 * q + i], f.c, -l4[i]));
-            if (cut && (dead || r + i < first)) p = 0.f;
-            s[4 * q + i] = p;
-            dp[4 * q + i] = p * (dp[4 * q + i] - d4[i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float p = exp2_(__builtin_fmaf(s[4 * q + i], f.c, -l4[i]));
+          s[4 * q + i] = p;
+          dp[4 * q + i] = p * (dp[4 * q + i] - d4[i]);
         }
+      }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const u32x4 pw = pack_half<kBf16>(s, half), dw = pack_half<kBf16>(dp, half);
-          const char* const qh = qb + 16 * half * T::kPitch;
-          const char* const dh = db + 16 * half * T::kPitch;
+      for (int half = 0; half < 2; ++half) {
+        const u32x4 pw = pack_half<kBf16>(s, half), dw = pack_half<kBf16>(dp, half);
+        const char* const qh = qt + 16 * half * T::kPitch;
+        const char* const dh = dt + 16 * half * T::kPitch;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            dv[nb] = mfma32<kBf16>(column_read(dh, col_off[nb][0], col_off[nb][1]), pw, dv[nb]);
-            dk[nb] = mfma32<kBf16>(column_read(qh, col_off[nb][0], col_off[nb][1]), dw, dk[nb]);
-          }
-        }
+        for (int nb = 0; nb < NB; ++nb) dv[nb] = mfma32<kBf16>(column_read(dh, col_off[nb][0], col_off[nb][1]), pw, dv[nb]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) dk[nb] = mfma32<kBf16>(column_read(qh, col_off[nb][0], col_off[nb][1]), dw, dk[nb]);
       }
     }
     q0 += kQueries;
     if (q0 >= qs.len) q0 = from;
   }
+  if (lo >= steps) wait_copies<0>();                    // V's copy must not outlive the workgroup
   // A batch's rows behind the filled ones get zeros (their sums are).
   const int64_t left = (packed ? ks.len : f.tk) - k0;
+  if (f.splits > 1) {
+    const int64_t total = packed ? f.tk : f.sequences * f.tk, at = (packed ? ks.start : seq * f.tk) + key;
+    if ((lane & 31) >= left) return;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = 32 * nb + 8 * q + 4 * (lane >> 5);
+        if (c >= f.d) continue;
+        float* const p = f.part_o + ((split * 2 * total + at) * f.hk + kv) * f.d + c;
+        *reinterpret_cast<f32x4*>(p) = (f32x4){dk[nb][4 * q], dk[nb][4 * q + 1], dk[nb][4 * q + 2], dk[nb][4 * q + 3]};
+        *reinterpret_cast<f32x4*>(p + total * f.hk * f.d) =
+            (f32x4){dv[nb][4 * q], dv[nb][4 * q + 1], dv[nb][4 * q + 2], dv[nb][4 * q + 3]};
+      }
+    return;
+  }
   store_rows<kBf16, NB>(a.dk.p + b * a.dk.b + (ks.start + k0) * a.dk.t + kv * a.dk.h, a.dk.t, left, f.d, dk, f.scale);
   store_rows<kBf16, NB>(a.dv.p + b * a.dv.b + (ks.start + k0) * a.dv.t + kv * a.dv.h, a.dv.t, left, f.d, dv, 1.f);
+}
+
+// Adds the splits' dK and dV up, in order: 8 channels per thread.
+__global__ void __launch_bounds__(256)
+attn_dkv_join_kernel(AttnBackArgs a) {
+  const AttnArgs& f = a.f;
+  const bool packed = f.q_starts != nullptr;
+  const int64_t total = packed ? f.tk : f.sequences * f.tk, size = total * f.hk * f.d;
+  const int64_t i = (folded_block() * 256 + threadIdx.x) * 8;
+  if (i >= 2 * size) return;
+  const bool is_v = i >= size;
+  const int64_t at = is_v ? i - size : i;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < f.splits; ++s) {
+    const f32x4* const p = reinterpret_cast<const f32x4*>(f.part_o + s * 2 * size + i);
+    const f32x4 x = p[0], y = p[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += x[e], v[4 + e] += y[e];
+  }
+  const float factor = is_v ? 1.f : f.scale;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= factor;
+  const int64_t c = at % f.d, kv = at / f.d % f.hk, row = at / f.d / f.hk, seq = packed ? 0 : row / f.tk;
+  const AttnTensor& t = is_v ? a.dv : a.dk;
+  store_vec<kBf16, 8>(t.p + seq * t.b + (row - seq * f.tk) * t.t + kv * t.h + c, v);
 }
 
 // --- dQ -----------------------------------------------------------------------
@@ -251,8 +307,8 @@ attn_dq_kernel(AttnBackArgs a) {
   auto copy = [&](int j) {
     const int64_t at = (int64_t)j * kKeys;
     const uint32_t buf = lds0 + (j & 1) * 2 * kTile;
-    ck.run(w.kp + at * f.k.t, w.k.len - at, buf);
-    cv.run(w.vp + at * f.v.t, w.k.len - at, buf + kTile);
+    ck.run(w.kp + at * f.k.t, clamp_rows(w.k.len - at), buf);
+    cv.run(w.vp + at * f.v.t, clamp_rows(w.k.len - at), buf + kTile);
   };
   if (steps > 0) copy(0);
   u32x4 qf[2 * NB], df[2 * NB];
@@ -260,7 +316,11 @@ attn_dq_kernel(AttnBackArgs a) {
   const int64_t d_off = b * a.d_o.b + w.q.start * a.d_o.t + w.head * a.d_o.h;
   load_rows<NB>(a.d_o.p + d_off + q0 * a.d_o.t, a.d_o.t, w.q.len - q0, f.d, df);
   const bool live = row < w.q.len;
-  const float lse2 = live ? a.lse2[w.lse_off + row] : __builtin_inff(), delta = live ? a.delta[w.lse_off + row] : 0.f;
+  const f32x2 stats = live ? a.stats[w.lse_off + row] : (f32x2){__builtin_inff(), 0.f};
+  float lse2 = stats[0], delta = stats[1];
+  settle(qf);
+  settle(df);
+  asm volatile("" : "+v"(lse2), "+v"(delta));
   f32x16 dq[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) dq[nb] = zero16();
@@ -316,8 +376,12 @@ hipError_t run_backward(AttnBackArgs a, hipStream_t stream) {
   const int64_t batch = packed ? 1 : a.f.sequences;
   if (a.f.tk > 0 && a.f.hk > 0) {
     a.f.tiles = packed ? a.f.tk / kKvKeys + a.f.sequences + 1 : (a.f.tk + kKvKeys - 1) / kKvKeys;
-    a.f.groups = a.f.tiles * a.f.hk * batch;
-    const hipError_t e = launch(&attn_dkv_kernel<NB>, folded_grid(a.f.groups), dim3(64 * kKvWaves), stream, a);
+    a.f.groups = a.f.tiles * a.f.hk * batch * a.f.splits;
+    hipError_t e = launch(&attn_dkv_kernel<NB>, folded_grid(a.f.groups), dim3(64 * kKvWaves), stream, a);
+    if (e == hipSuccess && a.f.splits > 1) {
+      const int64_t items = batch * a.f.tk * a.f.hk * (a.f.d / 8) * 2;
+      e = launch(&attn_dkv_join_kernel, folded_grid((items + 255) / 256), dim3(256), stream, a);
+    }
     if (e != hipSuccess) return e;
   }
   if (a.f.tq == 0 || a.f.hq == 0) return hipSuccess;
@@ -328,6 +392,17 @@ hipError_t run_backward(AttnBackArgs a, hipStream_t stream) {
 }
 
 }  // namespace
+
+// Ranges of the queries that a tile of keys' sums are shared out over: few key heads leave few workgroups
+// with long walks.  Up to four workgroups per CU (two run at a time), 256 queries at least for each.
+int attn_back_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, bool packed) {
+  if (hk == 0 || tk == 0 || sequences == 0) return 1;
+  const int64_t tiles = (packed ? tk / kKvKeys + sequences / 2 + 1 : sequences * ((tk + kKvKeys - 1) / kKvKeys)) * hk;
+  int64_t splits = 1024 / tiles;
+  const int64_t queries = (packed ? tq / sequences : tq) * (hq / hk);
+  if (splits > queries / 256) splits = queries / 256;
+  return splits < 1 ? 1 : splits > 16 ? 16 : (int)splits;
+}
 
 hipError_t launch_attention_backward(AttnBackArgs a, hipStream_t stream) {
   const int64_t rows = a.f.tq * a.f.hq * (a.f.q_starts != nullptr ? 1 : a.f.sequences);

@@ -184,12 +184,16 @@ struct TileCopy {
     }
   }
   // Rows from `left` on are zeros.  `base` is the tile's first row (uniform).
-  __device__ __forceinline__ void run(const void* base, int64_t left, uint32_t lds_tile) const {
+  __device__ __forceinline__ void run(const void* base, int left, uint32_t lds_tile) const {
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, 0x7fffffff);
-    uint32_t v[kCount];
+    if (left >= ROWS) {
+      copy_to_lds<kCount>(rs, off, lds_tile + lds);
+    } else {
+      uint32_t v[kCount];
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) v[i] = row0 + i * T::kRowsPerCopy < left ? off[i] : kOobOffset;
-    copy_to_lds<kCount>(rs, v, lds_tile + lds);
+      for (int i = 0; i < kCount; ++i) v[i] = row0 + i * T::kRowsPerCopy < left ? off[i] : kOobOffset;
+      copy_to_lds<kCount>(rs, v, lds_tile + lds);
+    }
   }
 };
 
@@ -208,6 +212,14 @@ __device__ __forceinline__ void load_rows(const uint16_t* base, int64_t token_st
     f[c] = (u32x4){0, 0, 0, 0};
     if (row < left && 16 * c + 8 * (lane >> 5) < d) f[c] = *reinterpret_cast<const u32x4*>(p + 16 * c);
   }
+}
+
+// Waits for loaded operands here.  Left to the first product, the compiler's wait would stand inside
+// the loop, and take the copies in flight for the loads.
+template <int N>
+__device__ __forceinline__ void settle(u32x4 (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f[i]));
 }
 
 // Stores a transposed result (a lane's column is row l % 32 of the tensor): halves of the wavefront
@@ -276,6 +288,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int64_t sequenc
   }
   return false;
 }
+
+__device__ __forceinline__ int clamp_rows(int64_t v) { return (int)(v < 0 ? 0 : v < 1 << 20 ? v : 1 << 20); }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));

@@ -8,6 +8,8 @@
 
 namespace rtl {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 // A launch dimension holds less than 2^32 threads: more workgroups than that of up
 // to 512 go to z, in rows of 2^22.  folded_block() is the workgroup's number; those
 // past the last one have nothing to do.
@@ -142,20 +144,29 @@ struct AttnArgs {
   int hq, hk, group, d;
   float scale, c;                        // c = scale log2(e)
   bool causal, zero_rest;
-  // Few queries over many keys.
+  // Keys split over workgroups.
   int splits;
-  float* part_o;                         // [splits][rows][d]
-  float* part_ml;                        // [splits][rows][2]: maximum, sum
+  int64_t whole;                         // workgroups with a whole tile, before those with a part of one
+  float* part_o;                         // [parts][rows][d]
+  float* part_ml;                        // [parts][rows][2]: maximum, sum
 };
 struct AttnBackArgs {
   AttnArgs f;                            // o and lse of the forward pass
   AttnTensor d_o, dq, dk, dv;
-  float* lse2;                           // log2 of the sum, +inf where no key is seen
-  float* delta;
+  f32x2* stats;                          // per query and head: log2 of the softmax's sum (+inf: no key), D
 };
-// Splits of the keys for the kernel for few queries, 0 where the other one serves.
-int attn_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, bool packed);
-hipError_t launch_attention(AttnArgs a, bool fp16, hipStream_t stream);
+// How the forward pass is shared out: the kernel for few queries, its keys in `splits` ranges, or whole
+// tiles and, last, `tail` tiles in `splits` ranges each.
+struct AttnPlan {
+  bool few;
+  int splits;
+  int64_t tail;
+};
+AttnPlan attn_plan(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, int64_t d, bool packed, bool causal);
+size_t attn_plan_bytes(const AttnPlan& p, int64_t sequences, int64_t tq, int64_t hq, int64_t d);
+hipError_t launch_attention(AttnArgs a, const AttnPlan& plan, bool fp16, void* workspace, hipStream_t stream);
+// Ranges of the queries in the dK / dV kernel: parts [range][dK, dV][rows][heads][d] in f.part_o.
+int attn_back_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, bool packed);
 hipError_t launch_attention_backward(AttnBackArgs a, hipStream_t stream);
 
 // Dense linears (include/rtlynx_dense.h).

@@ -68,16 +68,16 @@ typedef struct {
  *   q, o     [.., heads_q, head_dim]; k, v [.., heads_k, head_dim].
  *   lse      fp32, may be NULL: log of the sum of exp(s), natural logarithm,
  *            [sequences, heads_q, tokens_q], packed: [heads_q, tokens_q].
- *   workspace  rtl_attention_workspace_bytes(shape) bytes, 16-byte aligned (0
- *            for most shapes: it serves few queries over many keys, which are
- *            shared out over workgroups and joined).
+ *   workspace  rtl_attention_workspace_bytes(shape, flags) bytes, 16-byte aligned:
+ *            where there are fewer queries than the card needs, keys are shared
+ *            out over workgroups and the parts joined (0: not for this shape).
  *
  * q_starts and k_starts go together and must rise; starts and lengths outside
  * the tensors are cut to them.  No tokens, heads or sequences is a no-op.
  * tokens < 2^31, token strides < 2^23, other strides < 2^40, none negative.
  * tokens_q * heads_q * sequences < 2^38.
  */
-size_t rtl_attention_workspace_bytes(const rtl_attn_shape* shape);
+size_t rtl_attention_workspace_bytes(const rtl_attn_shape* shape, uint32_t flags);
 
 rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor* k, const rtl_attn_tensor* v,
                          const rtl_attn_tensor* o, float* lse, const rtl_attn_shape* shape,

@@ -76,11 +76,11 @@ def test_workspaces():
     assert _backward(wsb=need - 1) == WS and _backward(ws=None, wsb=0) == WS
     assert _backward(flags=1) == FLAGS and _backward(flags=0x20) == FLAGS
     few = dict(tokens_q=1, tokens_k=100_000)
-    need = at._fn("rtl_attention_workspace_bytes")(_shape(**few))
+    need = at._fn("rtl_attention_workspace_bytes")(_shape(**few), 0)
     assert need > 0
     assert _forward(ws=P, wsb=need - 1, **few) == WS and _forward(**few) == WS
-    assert at._fn("rtl_attention_workspace_bytes")(_shape(head_dim=7)) == 0
-    assert at._fn("rtl_attention_workspace_bytes")(_shape(q_starts=P, k_starts=P, **few)) == 0
+    assert at._fn("rtl_attention_workspace_bytes")(_shape(head_dim=7), 0) == 0
+    assert at._fn("rtl_attention_workspace_bytes")(_shape(q_starts=P, k_starts=P, **few), 0) == 0
 
 
 def test_empty_calls_and_valid_ones():
