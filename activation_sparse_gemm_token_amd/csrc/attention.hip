@@ -79,7 +79,7 @@ attn_forward_kernel(AttnArgs a) {
   int part = -1;
   int64_t part_tile = 0;
   if (id < a.whole) {
-    id = xcd_order(id, a.whole);
+    id = a.q_starts != nullptr ? xcd_order4(id, a.whole) : xcd_order(id, a.whole);
   } else {
     part_tile = (id - a.whole) / a.splits;
     part = (int)(id - a.whole - part_tile * a.splits);
@@ -88,11 +88,11 @@ attn_forward_kernel(AttnArgs a) {
   QueryWork w;
   if (!query_work(a, id, kForwardQueries, w)) {
     // No tile left: some rows may lie in no sequence.
-    const int64_t used = (id % a.tiles) - w.tile, spare = a.tiles - used;
-    rest_rows(a.q_starts, a.sequences, a.tq, w.tile * 256 + threadIdx.x, spare * 256, [&](int64_t row) {
-      if (a.lse != nullptr) a.lse[w.head * a.tq + row] = ninf();
+    const int64_t spare = a.groups - (id - w.tile);
+    rest_rows(a.q_starts, a.sequences, a.tq, a.hq, w.tile, spare, [&](int64_t row, int64_t head) {
+      if (a.lse != nullptr) a.lse[head * a.tq + row] = ninf();
       if (a.zero_rest) {
-        uint16_t* p = a.o.p + row * a.o.t + w.head * a.o.h;
+        uint16_t* p = a.o.p + row * a.o.t + head * a.o.h;
         for (int c = 0; c < a.d; c += 8) *reinterpret_cast<u32x4*>(p + c) = (u32x4){0, 0, 0, 0};
       }
     });

@@ -64,37 +64,38 @@ attn_dkv_kernel(AttnBackArgs a) {
   const AttnArgs& f = a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (folded_block() >= f.groups) return;
-  const int64_t block = xcd_order(folded_block(), f.groups), id = block / f.splits;
-  const int split = (int)(block - id * f.splits);
-  int64_t item = id / f.tiles, t = id - item * f.tiles, seq = 0;
   const bool packed = f.q_starts != nullptr;
+  const int64_t block = packed ? xcd_order4(folded_block(), f.groups) : xcd_order(folded_block(), f.groups);
+  const int64_t id = block / f.splits;
+  int64_t seq, kv, t;
+  const int split = (int)(block - id * f.splits);
   Span qs, ks;
-  int64_t kv;
   if (packed) {
-    kv = item;
-    const int64_t given = t;
-    const bool found = find_tile(f.k_starts, f.sequences, f.tk, kKvKeys, t, seq);
-    t = uniform64(t);
-    seq = uniform64(seq);
-    if (!found) {
-      const int64_t spare = f.tiles - (given - t);
-      rest_rows(f.k_starts, f.sequences, f.tk, t * 64 * kKvWaves + threadIdx.x, spare * 64 * kKvWaves, [&](int64_t row) {
+    const PackedTile p = packed_tile(f.k_starts, f.sequences, f.tk, kKvKeys, f.hk, id);
+    if (!p.found) {
+      const int64_t spare = f.groups / f.splits - (id - p.tile);
+      rest_rows(f.k_starts, f.sequences, f.tk, f.hk, p.tile, spare, [&](int64_t row, int64_t head) {
         if (f.splits > 1) {
-          float* p = f.part_o + ((split * 2 * f.tk + row) * f.hk + kv) * f.d;
+          float* p = f.part_o + ((split * 2 * f.tk + row) * f.hk + head) * f.d;
           for (int c = 0; c < f.d; c += 4)
             *reinterpret_cast<f32x4*>(p + c) = *reinterpret_cast<f32x4*>(p + f.tk * f.hk * f.d + c) = (f32x4){0, 0, 0, 0};
           return;
         }
-        uint16_t* p = a.dk.p + row * a.dk.t + kv * a.dk.h;
-        uint16_t* q = a.dv.p + row * a.dv.t + kv * a.dv.h;
+        uint16_t* p = a.dk.p + row * a.dk.t + head * a.dk.h;
+        uint16_t* q = a.dv.p + row * a.dv.t + head * a.dv.h;
         for (int c = 0; c < f.d; c += 8)
           *reinterpret_cast<u32x4*>(p + c) = *reinterpret_cast<u32x4*>(q + c) = (u32x4){0, 0, 0, 0};
       });
       return;
     }
+    t = p.tile;
+    seq = p.seq;
+    kv = p.head;
     qs = packed_span(f.q_starts, seq, f.tq);
     ks = packed_span(f.k_starts, seq, f.tk);
   } else {
+    const int64_t item = id / f.tiles;
+    t = id - item * f.tiles;
     seq = item / f.hk;
     kv = item - seq * f.hk;
     qs = {0, f.tq};
@@ -277,12 +278,12 @@ attn_dq_kernel(AttnBackArgs a) {
   const AttnArgs& f = a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (folded_block() >= f.groups) return;
-  const int64_t id = xcd_order(folded_block(), f.groups);
+  const int64_t id = f.q_starts != nullptr ? xcd_order4(folded_block(), f.groups) : xcd_order(folded_block(), f.groups);
   QueryWork w;
   if (!query_work(f, id, kQueries, w)) {
-    const int64_t used = (id % f.tiles) - w.tile, spare = f.tiles - used;
-    rest_rows(f.q_starts, f.sequences, f.tq, w.tile * 64 * kDqWaves + threadIdx.x, spare * 64 * kDqWaves, [&](int64_t row) {
-      uint16_t* p = a.dq.p + row * a.dq.t + w.head * a.dq.h;
+    const int64_t spare = f.groups - (id - w.tile);
+    rest_rows(f.q_starts, f.sequences, f.tq, f.hq, w.tile, spare, [&](int64_t row, int64_t head) {
+      uint16_t* p = a.dq.p + row * a.dq.t + head * a.dq.h;
       for (int c = 0; c < f.d; c += 8) *reinterpret_cast<u32x4*>(p + c) = (u32x4){0, 0, 0, 0};
     });
     return;

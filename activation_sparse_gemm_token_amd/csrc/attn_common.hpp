@@ -263,44 +263,53 @@ __device__ __forceinline__ Span packed_span(const int32_t* starts, int64_t s, in
   return {lo, hi - lo};
 }
 
-// Tile number t of all packed sequences' tiles of `rows` rows: which sequence, which of its
-// tiles.  Returns false past the last one, t then less the number of tiles.
-__device__ __forceinline__ bool find_tile(const int32_t* starts, int64_t sequences, int64_t total, int rows, int64_t& t,
-                                          int64_t& seq) {
+// Number `id` of the workgroups of a packed batch: tile `tile` of `rows` rows of a sequence in a head.
+// Up to 64 sequences go longest first (a long one started last would run alone at the end), then
+// heads, then tiles.  Not found: none left, `tile` counts those past the last one.
+struct PackedTile {
+  bool found;
+  int64_t seq, head, tile;
+};
+__device__ __forceinline__ PackedTile packed_tile(const int32_t* starts, int64_t sequences, int64_t total, int rows,
+                                                  int64_t heads, int64_t id) {
   const int lane = threadIdx.x & 63;
   for (int64_t base = 0; base < sequences; base += 64) {
-    int64_t n = 0;
-    if (base + lane < sequences) n = (packed_span(starts, base + lane, total).len + rows - 1) / rows;
-    int64_t sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int64_t up = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += up;
+    int32_t n = 0;
+    if (base + lane < sequences) n = (int32_t)((packed_span(starts, base + lane, total).len + rows - 1) / rows);
+    int64_t before = 0, all = 0;                        // tiles of the sequences before this lane's, of all 64
+    const int count = sequences - base < 64 ? (int)(sequences - base) : 64;
+    for (int k = 0; k < count; ++k) {
+      const int32_t other = __builtin_amdgcn_readlane(n, k);
+      const bool first = sequences <= 64 ? other > n || (other == n && k < lane) : k < lane;
+      before += first ? other : 0;
+      all += other;
     }
-    const uint64_t hit = __ballot(t < sum);
+    const uint64_t hit = __ballot(id >= before * heads && id < (before + n) * heads);
     if (hit != 0) {
       const int at = __builtin_ctzll(hit);
-      t -= __shfl(sum - n, at, 64);
-      seq = base + at;
-      return true;
+      const int64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)before, at);
+      const int64_t hi = __builtin_amdgcn_readlane((int)(before >> 32), at);
+      const int64_t in = id - (hi << 32 | lo) * heads, tiles = __builtin_amdgcn_readlane(n, at), head = in / tiles;
+      return {true, base + at, head, in - head * tiles};
     }
-    t -= __shfl(sum, 63, 64);
+    id -= all * heads;
   }
-  return false;
+  return {false, 0, 0, id};
 }
 
 __device__ __forceinline__ int clamp_rows(int64_t v) { return (int)(v < 0 ? 0 : v < 1 << 20 ? v : 1 << 20); }
-
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
-}
 
 // Workgroups go to the 8 XCDs in turn, each with its own L2: number `id` of `total` renumbered so
 // that an XCD has consecutive ones (which share keys and values).
 __device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
   const int64_t xcd = id % 8, local = id / 8, per = total / 8, extra = total % 8;
   return xcd * per + (xcd < extra ? xcd : extra) + local;
+}
+
+// The same for packed batches, whose work falls from first to last: 4 consecutive ones to an XCD in turn.
+__device__ __forceinline__ int64_t xcd_order4(int64_t id, int64_t total) {
+  const int64_t in = id % 32, block = id - in;
+  return block + 32 <= total ? block + (in % 8) * 4 + in / 8 : id;
 }
 
 // Number of copies still in flight that may stay so.
@@ -317,24 +326,22 @@ struct QueryWork {
   int64_t q_off, o_off, lse_off;                        // query row 0: elements into q, o and lse
 };
 
-// Number `id` of the grid: heads outermost, then (packed) the sequences' tiles.  Causal tiles go
-// from the last, which sees the most keys, to the first.  False: no such tile, `tile` its number past
-// the last one.
+// Number `id` of the grid.  Causal tiles go from the last, which sees the most keys, to the first.  False: no
+// such tile, `tile` then counts the workgroups without one.
 __device__ __forceinline__ bool query_work(const AttnArgs& a, int64_t id, int rows, QueryWork& w) {
-  int64_t item = id / a.tiles, t = id - item * a.tiles;
-  bool found = true;
+  int64_t t;
   if (a.q_starts != nullptr) {
-    w.head = item;
-    w.seq = 0;
-    found = find_tile(a.q_starts, a.sequences, a.tq, rows, t, w.seq);
-    t = uniform64(t);
-    w.seq = uniform64(w.seq);
-    w.tile = t;
-    if (!found) return false;
+    const PackedTile p = packed_tile(a.q_starts, a.sequences, a.tq, rows, a.hq, id);
+    t = w.tile = p.tile;
+    if (!p.found) return false;
+    w.seq = p.seq;
+    w.head = p.head;
     w.q = packed_span(a.q_starts, w.seq, a.tq);
     w.k = packed_span(a.k_starts, w.seq, a.tk);
     w.lse_off = w.head * a.tq + w.q.start;
   } else {
+    const int64_t item = id / a.tiles;
+    t = id - item * a.tiles;
     w.seq = item / a.hq;
     w.head = item - w.seq * a.hq;
     w.q = {0, a.tq};
@@ -354,14 +361,18 @@ __device__ __forceinline__ bool query_work(const AttnArgs& a, int64_t id, int ro
   return true;
 }
 
-// The rows of a packed tensor that lie in no sequence, shared out over `parts`: f(row).
+// The rows of a packed tensor that lie in no sequence, in every head: f(row, head) for the share of workgroup
+// number `part` of those without a tile, which are at least one; `parts` of 256 threads at most stride over them.
 template <typename F>
-__device__ __forceinline__ void rest_rows(const int32_t* starts, int64_t sequences, int64_t total, int64_t part, int64_t parts,
-                                          F f) {
+__device__ __forceinline__ void rest_rows(const int32_t* starts, int64_t sequences, int64_t total, int64_t heads, int64_t part,
+                                          int64_t parts, F f) {
   const int64_t first = packed_span(starts, 0, total).start;
   const Span last = packed_span(starts, sequences - 1, total);
-  const int64_t end = last.start + last.len, rest = first + total - end;
-  for (int64_t i = part; i < rest; i += parts) f(i < first ? i : end + i - first);
+  const int64_t end = last.start + last.len, rest = (first + total - end) * heads;
+  for (int64_t i = part * blockDim.x + threadIdx.x; i < rest; i += parts * blockDim.x) {
+    const int64_t row = i / heads;
+    f(row < first ? row : end + row - first, i - row * heads);
+  }
 }
 
 }  // namespace rtl
