@@ -171,30 +171,35 @@ template <int T, bool ALONG>
 struct Operand {
   static constexpr int kBytes = T * 128, kPitch = ALONG ? 128 : 2 * T;
   static constexpr int kWaves = T / 32;                 // of the workgroup; 4 copy instructions each
-  uint32_t off[4];                                      // of the lane, in each instruction
-  int chunk[4];                                         // ALONG: channel within the step
-  uint32_t step_bytes;
+  // The lane's offset in instruction i: first[set(i)] + i / .. * row_bytes; the swizzle makes two sets across.
+  uint32_t first[ALONG ? 1 : 2];
+  uint32_t row_bytes, step_bytes;                       // uniform
+  int chunk;                                            // ALONG: channel within the step
 
   __device__ static __forceinline__ uint32_t swizzle(uint32_t row) {
     return ALONG ? row & 7 : (row & 3) << 1 | ((row >> 3) & 1) << 3;
   }
+  static constexpr int set(int i) { return ALONG ? 0 : T == 256 ? i & 1 : i >> 1; }
   // Rows from r0 on of a tensor with rows of ld elements.
   __device__ __forceinline__ void init(int wave, int64_t r0, int64_t ld) {
     const uint32_t lane = threadIdx.x & 63, slots = kPitch / 16, rows = 1024 / kPitch;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t row = (4 * wave + i) * rows + lane / slots, c = (lane % slots) ^ swizzle(row);
-      chunk[i] = ALONG ? 8 * (int)c : 0;
-      off[i] = ALONG ? (uint32_t)((r0 + row) * ld * 2 + 16 * c) : (uint32_t)(row * ld * 2 + r0 * 2 + 16 * c);
+      const uint32_t at = ALONG ? (uint32_t)((r0 + row) * ld * 2 + 16 * c) : (uint32_t)(row * ld * 2 + r0 * 2 + 16 * c);
+      if (i == 0 || (!ALONG && i == (T == 256 ? 1 : 2))) first[set(i)] = at - i * (uint32_t)(rows * ld * 2);
+      if (i == 0) chunk = ALONG ? 8 * (int)c : 0;
     }
-    step_bytes = ALONG ? 128u : (uint32_t)(64 * ld * 2);
+    row_bytes = __builtin_amdgcn_readfirstlane((uint32_t)(rows * ld * 2));
+    step_bytes = ALONG ? 128u : __builtin_amdgcn_readfirstlane((uint32_t)(64 * ld * 2));
   }
   // Step s of a contraction of K: what lies past it arrives as zeros (across: it lies past the buffer).
   __device__ __forceinline__ void copy(__amdgpu_buffer_rsrc_t rs, int64_t s, int64_t K, uint32_t lds, int wave) const {
     const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)s * step_bytes);
+    const bool inside = !ALONG || s * 64 + chunk < K;
     uint32_t v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = !ALONG || s * 64 + chunk[i] < K ? off[i] : kOobOffset - so;
+    for (int i = 0; i < 4; ++i) v[i] = inside ? first[set(i)] + i * row_bytes : kOobOffset - so;
     const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds + 4096u * wave);
     uint32_t saved;
     asm volatile(
@@ -241,11 +246,9 @@ linear_gemm_kernel(LinearGemm g) {
   using A = Operand<T, A_ALONG>;
   using B = Operand<T, B_ALONG>;
   constexpr int kWaves = T / 32, kWavesN = T / 64, kRB = T == 256 ? 8 : 4, kCB = 4;
-  constexpr int kAStages = 2, kBStages = 3, kTile = A::kBytes;
+  constexpr int kTile = A::kBytes, kRowBytes = 64 * 4 + 16, kStaging = kWaves * 64 * kRowBytes;
   static_assert(kWaves == (T / (16 * kRB)) * kWavesN, "wavefronts cover the tile");
-  __shared__ __attribute__((aligned(16))) char lds[(kAStages + kBStages) * kTile];
-  char* const lds_b = lds;
-  char* const lds_a = lds + kBStages * kTile;
+  __shared__ __attribute__((aligned(16))) char lds[kStaging > 4 * kTile ? kStaging : 4 * kTile];   // A, B of two steps; epilogue
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / kWavesN, wn = wave % kWavesN;
   const int64_t tiles_m = (g.M + T - 1) / T, tiles_n = (g.N + T - 1) / T, tiles = tiles_m * tiles_n;
@@ -268,70 +271,61 @@ linear_gemm_kernel(LinearGemm g) {
 #pragma unroll
     for (int j = 0; j < kCB; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
 
-  auto address = [](const char* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)(p); };
-  auto copy_a = [&](int64_t s, int stage) { oa.copy(ar, lo + s, g.K, address(lds_a) + stage * kTile, wave); };
-  auto copy_b = [&](int64_t s, int stage) { ob.copy(br, lo + s, g.K, address(lds_b) + stage * kTile, wave); };
-  // Step s: B stage s % 3, A stage s % 2; the A copy of step s + 1 and the B copy of step s + 2 go
-  // out at its top, where only the B copy of step s + 1 may still be in flight.
-  auto step = [&](int64_t s, auto bs_c, auto as_c) {
-    constexpr int bs = decltype(bs_c)::value, as = decltype(as_c)::value;
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vm<4>();
-    barrier_no_fence();
-    copy_a(s + 1 < steps ? s + 1 : steps - 1, 1 - as);
-    copy_b(s + 2 < steps ? s + 2 : steps - 1, (bs + 2) % kBStages);
-    __builtin_amdgcn_sched_barrier(0);
-    const char* const ta = lds_a + as * kTile;
-    const char* const tb = lds_b + bs * kTile;
-    u32x4 af[2][kRB];
+  // Two stages of both operands.  Half of a step's fragments (32 of the contraction) are in registers ahead of their
+  // products: the other half is read from LDS during the first half's products, and the next step's first
+  // half during the second's.  The barrier between them comes after the last read of a stage, so the copy of
+  // step s + 2 goes out there, a whole step before it is waited for.  (One stage more for B, the whole step's
+  // fragments read at its top: 429 us for the 4096 x 2048 x 8192 training step, 420 this way; the loop unrolled
+  // over the stages is 2 % faster at 4096 x 4096 x 12288 forward but spills where operands run across.)
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)(lds);
+  auto copy = [&](int64_t s, int stage) {
+    oa.copy(ar, lo + s, g.K, lds0 + stage * 2 * kTile, wave);
+    ob.copy(br, lo + s, g.K, lds0 + stage * 2 * kTile + kTile, wave);
+  };
+  u32x4 fa[2][kRB], fb[2][kCB];
+  using First = std::integral_constant<int, 0>;
+  using Second = std::integral_constant<int, 1>;
+  auto read = [&](int stage, auto half) {
+    constexpr int h = decltype(half)::value;
+    const char* const ta = lds + stage * 2 * kTile;
 #pragma unroll
-    for (int i = 0; i < kRB; ++i) {
-      af[0][i] = A::read(ta, at_a, i, 0);
-      af[1][i] = A::read(ta, at_a, i, 1);
-    }
-    u32x4 q0 = B::read(tb, at_b, 0, 0), q1 = B::read(tb, at_b, 0, 1);
+    for (int j = 0; j < kCB; ++j) fb[h][j] = B::read(ta + kTile, at_b, j, h);
 #pragma unroll
-    for (int j = 0; j < kCB; ++j) {
-      const u32x4 b0 = q0, b1 = q1;
-      if (j + 1 < kCB) {
-        q0 = B::read(tb, at_b, j + 1, 0);
-        q1 = B::read(tb, at_b, j + 1, 1);
-      }
+    for (int i = 0; i < kRB; ++i) fa[h][i] = A::read(ta, at_a, i, h);
+  };
+  auto multiply = [&](auto half) {
+    constexpr int h = decltype(half)::value;
 #pragma unroll
-      for (int i = 0; i < kRB; ++i) acc[i][j] = mfma16<TYPE>(b0, af[0][i], acc[i][j]);
+    for (int i = 0; i < kRB; ++i)
 #pragma unroll
-      for (int i = 0; i < kRB; ++i) acc[i][j] = mfma16<TYPE>(b1, af[1][i], acc[i][j]);
-    }
+      for (int j = 0; j < kCB; ++j) acc[i][j] = mfma16<TYPE>(fb[h][j], fa[h][i], acc[i][j]);
   };
   if (steps > 0) {
-    copy_b(0, 0);
-    copy_a(0, 0);
-    copy_b(steps > 1 ? 1 : 0, 1);
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
-    int64_t s = 0;
-    for (; s + 6 <= steps; s += 6) {
-      step(s + 0, I0{}, I0{});
-      step(s + 1, I1{}, I1{});
-      step(s + 2, I2{}, I0{});
-      step(s + 3, I0{}, I1{});
-      step(s + 4, I1{}, I0{});
-      step(s + 5, I2{}, I1{});
+    copy(0, 0);
+    wait_vm<0>();
+    barrier_no_fence();
+    if (steps > 1) copy(1, 1);
+    read(0, First{});
+#pragma unroll 1
+    for (int64_t s = 0; s < steps; ++s) {
+      const int stage = (int)(s & 1);
+      read(stage, Second{});
+      multiply(First{});
+      __builtin_amdgcn_sched_barrier(0);
+      // This wavefront's reads of the stage are back, and its copies of the next one.
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      barrier_no_fence();
+      if (s + 2 < steps) copy(s + 2, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      read(1 - stage, First{});                         // after the last step: not used
+      multiply(Second{});
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (s < steps) step(s + 0, I0{}, I0{});
-    if (s + 1 < steps) step(s + 1, I1{}, I1{});
-    if (s + 2 < steps) step(s + 2, I2{}, I0{});
-    if (s + 3 < steps) step(s + 3, I0{}, I1{});
-    if (s + 4 < steps) step(s + 4, I1{}, I0{});
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vm<0>();                                       // no copy outlives the workgroup
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
   barrier_no_fence();                                   // the rings are free
   // Through LDS, 64 rows x 64 channels of the wavefront at a time, so that a lane has 8 consecutive
   // channels of a row (16 bytes of y) and the epilogue is one short loop.
-  constexpr int kRowBytes = 64 * 4 + 16;
-  static_assert(kWaves * 64 * kRowBytes <= (kAStages + kBStages) * kTile, "staging fits in the rings");
   char* const mine = lds + wave * 64 * kRowBytes;
   const int64_t n = n0 + 64 * wn + 8 * (lane & 7);
   const bool wide = g.N % 8 == 0;
@@ -574,19 +568,28 @@ hipError_t run_dz(const LinearDz& a, hipStream_t stream) {
 
 }  // namespace
 
-// Tile and ranges of the contraction for a product [M, N] over K.  256 x 256 tiles where they fill
-// most of the card; else 128 x 128, the contraction in ranges of at least 4 steps until there are two
-// workgroups per CU.
+// Tile and ranges of the contraction for a product [M, N] over K: the form with the least expected time, in us, from
+// measured rates.  A step of 64 takes a 256 x 256 tile 1.55 (one workgroup per CU) and 128 x 128 tiles 0.55 alone on
+// their CU, 1.03 where two share it; a tile 9 and 4 more to begin and end.  Ranges of the contraction cost a second
+// launch and their fp32 parts, written and read at 4 TB/s.  (2310 x 1160 x 1152: 14 expected for one range, 30 for three,
+// measured 33 with three; 4096 x 2048 x 8192: 136 with 128 x 128, 206 with 256 x 256; 8192 x 2048 x 4096: 136 and 107.)
 LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel) {
   if (rows_kernel && M <= 32) return {0, 1};
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= 200) return {256, 1};
-  const int64_t small = ((M + 127) / 128) * ((N + 127) / 128), steps = (K + 63) / 64;
-  if (small == 0) return {128, 1};
-  int64_t splits = small >= 256 ? 1 : (512 + small - 1) / small;
-  if (splits > steps / 4) splits = steps / 4;
-  if (splits > 16) splits = 16;
-  return {128, splits < 1 ? 1 : (int)splits};
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t steps = (K + 63) / 64;
+  if (small == 0 || steps == 0) return {128, 1};
+  LinearForm best{256, 1};
+  double least = (double)((big + 255) / 256) * (1.55 * (double)steps + 9.0);
+  for (int64_t splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); splits *= 2) {
+    const int64_t groups = small * splits, each = (steps + splits - 1) / splits;
+    double t = groups <= 256 ? 0.55 * (double)each + 4.0 : (double)((groups + 511) / 512) * (1.03 * (double)each + 4.0);
+    if (splits > 1) t += 4.0 + (double)splits * (double)M * (double)N * 8.0 / 4e6;
+    if (t < least) {
+      least = t;
+      best = {128, (int)splits};
+    }
+  }
+  return best;
 }
 
 int64_t linear_dz_parts(int64_t M, int64_t N, int64_t groups) {
