@@ -32,14 +32,16 @@ def _fn(name):
     return fn
 
 
-def _run(name, args, t, **tensors):
-    stream = _here(t, *tensors.values())
+def _run(name, args, stream, t, **tensors):
+    """Entry point ``name`` on t's device: on ``stream`` (``_here``'s), or where that is None on the
+    device that the named tensors share, made current, and its current stream."""
     if stream is None:
         with _on(t.device, **tensors):
             st = _fn(name)(*args, _stream())
     else:
         st = _fn(name)(*args, stream)
-    _check(st, name)
+    if st:
+        _check(st, name)
 
 
 def _flags(x, activation):
@@ -53,25 +55,28 @@ def _flags(x, activation):
     raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
 
 
-def _matrix(t, name, dtype, lead, cols):
-    """A contiguous device tensor [*lead, cols]."""
+def _matrix(t, name, dtype, shape):
+    """A contiguous device tensor."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.shape[-1:] != (cols,) or (lead is not None and t.shape[:-1] != lead):
-        raise ValueError(f"{name} must have shape {(*(lead or ('..',)), cols)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _sizes(x, w):
-    if x.dim() < 1 or w.dim() != 2:
+    xs, ws = x.shape, w.shape
+    if len(xs) < 1 or len(ws) != 2:
         raise ValueError("x must be [..., K] and w [N, K]")
-    n, k = w.shape
-    _matrix(x, "x", x.dtype, None, k)
-    _matrix(w, "w", x.dtype, (n,), k)
-    m = x.numel() // k if k else 0
+    n, k = ws
+    _matrix(x, "x", x.dtype, (*xs[:-1], k))
+    _matrix(w, "w", x.dtype, ws)
+    m = 1
+    for i in xs[:-1]:
+        m *= i
     return m, n, k
 
 
@@ -123,33 +128,42 @@ def linear(x, w, bias=None, activation=None, gate=None, residual=None, out=None,
     [batch, tokens, K], [batch, N] (a slice of a modulation row goes as it is); ``residual``
     [..., N].  ``out`` may be the residual itself.  Returns y, or with ``keep`` (y, z), z
     the rounded x w^T + bias for ``linear_backward``; without an autograd graph."""
-    torch = _torch()
-    _no_graph("dense.linear", "dense.linear_backward forms it", x, w, bias, gate, residual)
+    for t in (x, w, bias, gate, residual):
+        if t is not None and t.requires_grad:
+            _no_graph("dense.linear", "dense.linear_backward forms it", t)
+            break
     flags = _flags(x, activation)
     m, n, k = _sizes(x, w)
-    lead = x.shape[:-1]
+    shape = (*x.shape[:-1], n)
+    bp = rp = gp = zp = wp = z = None
+    rows, stride, size = 1, 0, 0
     if bias is not None:
-        _matrix(bias, "bias", x.dtype, (), n)
+        _matrix(bias, "bias", x.dtype, (n,))
+        bp = bias.data_ptr()
     if residual is not None:
-        _matrix(residual, "residual", x.dtype, lead, n)
-    gp, rows, stride = _gate(gate, x, n)
+        _matrix(residual, "residual", x.dtype, shape)
+        rp = residual.data_ptr()
+    if gate is not None:
+        gp, rows, stride = _gate(gate, x, n)
     if out is None:
-        y = torch.empty((*lead, n), dtype=x.dtype, device=x.device)
+        y = x.new_empty(shape)
     else:
-        _matrix(out, "out", x.dtype, lead, n)
+        _matrix(out, "out", x.dtype, shape)
         if out.device != x.device:
             raise ValueError(f"out is on {out.device}, x on {x.device}")
         same = residual is not None and out.data_ptr() == residual.data_ptr()
         _apart(out, x=x, w=w, bias=bias, gate=gate, residual=None if same else residual)
         y = out
-    z = torch.empty((*lead, n), dtype=x.dtype, device=x.device) if keep else None
-    need = workspace_bytes(m, n, k)
-    if workspace is not None or need:
-        workspace = _workspace(workspace, need, x.device)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _run("rtl_linear", (x.data_ptr(), w.data_ptr(), ptr(bias), gp, rows, stride, ptr(residual), m, n, k, y.data_ptr(), ptr(z),
-                        ptr(workspace), 0 if workspace is None else workspace.numel(), flags),
-         x, w=w, bias=bias, gate=gate, residual=residual)
+    if keep:
+        z = x.new_empty(shape)
+        zp = z.data_ptr()
+    if m > 32:                                            # the kernel for few rows needs none
+        size = workspace_bytes(m, n, k)
+    if workspace is not None or size:
+        workspace = _workspace(workspace, size, x.device)
+        wp, size = workspace.data_ptr(), workspace.numel()
+    _run("rtl_linear", (x.data_ptr(), w.data_ptr(), bp, gp, rows, stride, rp, m, n, k, y.data_ptr(), zp, wp, size, flags),
+         _here(x, w, bias, gate, residual), x, w=w, bias=bias, gate=gate, residual=residual)
     return (y, z) if keep else y
 
 
@@ -162,25 +176,23 @@ def linear_backward(dy, x, w, z=None, activation=None, gate=None, need_dx: bool 
     """Gradients of ``linear`` from dy, its x, w and gate, and the z that it kept: (dx, dw, dbias,
     dgate), None where not asked for (dgate is None without a gate).  The residual's gradient is
     dy.  z is needed with an activation or a gate's gradient."""
-    torch = _torch()
     flags = _flags(x, activation)
     m, n, k = _sizes(x, w)
-    lead = x.shape[:-1]
-    _matrix(dy, "dy", x.dtype, lead, n)
+    shape = (*x.shape[:-1], n)
+    _matrix(dy, "dy", x.dtype, shape)
     gp, rows, stride = _gate(gate, x, n)
     need_dgate = need_dgate and gate is not None
     if z is None and (activation is not None or need_dgate):
         raise ValueError("an activation, or a gate's gradient, needs z")
     if z is not None:
-        _matrix(z, "z", x.dtype, lead, n)
-    new = lambda *s: torch.empty(s, dtype=x.dtype, device=x.device)  # noqa: E731
-    dx = new(*lead, k) if need_dx else None
-    dw = new(n, k) if need_dw else None
-    dbias = new(n) if need_dbias else None
-    dgate = new(*gate.shape) if need_dgate else None
+        _matrix(z, "z", x.dtype, shape)
+    dx = x.new_empty(x.shape) if need_dx else None
+    dw = x.new_empty((n, k)) if need_dw else None
+    dbias = x.new_empty((n,)) if need_dbias else None
+    dgate = x.new_empty(gate.shape) if need_dgate else None
     workspace = _workspace(workspace, backward_workspace_bytes(m, n, k, rows), x.device)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _run("rtl_linear_backward", (dy.data_ptr(), x.data_ptr(), w.data_ptr(), ptr(z), gp, rows, stride, m, n, k, ptr(dx), ptr(dw),
                                  ptr(dbias), ptr(dgate), workspace.data_ptr(), workspace.numel(), flags),
-         x, dy=dy, w=w, z=z, gate=gate)
+         _here(x, dy, w, z, gate), x, dy=dy, w=w, z=z, gate=gate)
     return dx, dw, dbias, dgate

@@ -37,25 +37,27 @@ def _fn(name):
     return fn
 
 
-def _run(name, args, t, **tensors):
-    stream = _here(t, *tensors.values())
+def _run(name, args, stream, t, **tensors):
+    """Entry point ``name`` on t's device: on ``stream`` (``_here``'s), or where that is None on the
+    device that the named tensors share, made current, and its current stream."""
     if stream is None:
         with _on(t.device, **tensors):
             st = _fn(name)(*args, _stream())
     else:
         st = _fn(name)(*args, stream)
-    _check(st, name)
+    if st:
+        _check(st, name)
 
 
-def _type_flag(t, name):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
+def _type_flag(torch, t, name):
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return 0
-    if t.dtype is torch.float16:
+    if dtype is torch.float16:
         return 1
-    if t.dtype is torch.float32:
+    if dtype is torch.float32:
         return 2
-    raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
 
 
 def _layout(t, name):
@@ -82,19 +84,18 @@ def _layout(t, name):
     return 1, rows, 0, shape[-1]
 
 
-def _affine(p, name, x, batched):
-    """(pointer, stride between sequences, rows) of weight or bias."""
-    torch = _torch()
-    c = x.shape[-1]
+def _affine(torch, p, name, x, shape):
+    """(pointer, stride between sequences, rows) of weight or bias for x of this shape."""
+    c, ps = shape[-1], p.shape
     if p.dtype is not x.dtype and p.dtype is not torch.float32:
         raise TypeError(f"{name} must be {x.dtype} or float32, got {p.dtype}")
-    if tuple(p.shape) == (c,):
+    if len(ps) == 1 and ps[0] == c:
         stride, rows = 0, 1
-    elif batched and tuple(p.shape) == (x.shape[0], c):
-        stride, rows = p.stride(0), p.shape[0]
+    elif len(ps) == 2 and len(shape) == 3 and ps[0] == shape[0] and ps[1] == c:
+        stride, rows = p.stride(0), ps[0]
     else:
-        raise ValueError(f"{name} must have shape {(c,)}" + (f" or {(x.shape[0], c)}" if batched else "") +
-                         f", got {tuple(p.shape)}")
+        raise ValueError(f"{name} must have shape {(c,)}" + (f" or {(shape[0], c)}" if len(shape) == 3 else "") +
+                         f", got {tuple(ps)}")
     if c > 1 and p.stride(-1) != 1:
         raise ValueError(f"{name}: the channel stride must be 1")
     return p.data_ptr(), stride, rows
@@ -122,14 +123,15 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, offset: float = 0.0
     statistics fp32 of x's shape without the channels, without an autograd graph
     (``layer_norm_backward``)."""
     torch = _torch()
-    _no_graph("norm.layer_norm", "norm.layer_norm_backward forms it", x, weight, bias)
-    flags = _type_flag(x, "x")
+    if x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad):
+        _no_graph("norm.layer_norm", "norm.layer_norm_backward forms it", x, weight, bias)
+    flags = _type_flag(torch, x, "x")
     batch, tokens, xb, xt = _layout(x, "x")
-    batched = x.dim() == 3
+    shape = x.shape
     wp = bp = None
     ws = bs = 0
     if weight is not None:
-        wp, ws, _ = _affine(weight, "weight", x, batched)
+        wp, ws, _ = _affine(torch, weight, "weight", x, shape)
         if weight.dtype is torch.float32:
             flags |= _AFFINE_FP32
     if bias is not None:
@@ -137,20 +139,20 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, offset: float = 0.0
             raise ValueError("a bias needs a weight")
         if bias.dtype is not weight.dtype:
             raise TypeError(f"bias must be {weight.dtype} like weight, got {bias.dtype}")
-        bp, bs, _ = _affine(bias, "bias", x, batched)
+        bp, bs, _ = _affine(torch, bias, "bias", x, shape)
+    c = shape[-1]
     if out is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y, yb, yt = x.new_empty(shape), tokens * c, c
     else:
         _check_out(out, x, x=x, weight=weight, bias=bias)
         y = out
-    _, _, yb, yt = _layout(y, "out")
+        _, _, yb, yt = _layout(y, "out")
     mean = rstd = mp = rp = None
     if return_stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
+        mean, rstd = x.new_empty(shape[:-1], dtype=torch.float32), x.new_empty(shape[:-1], dtype=torch.float32)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
-    _run("rtl_layer_norm", (x.data_ptr(), batch, tokens, x.shape[-1], xb, xt, wp, ws, bp, bs, float(offset), float(eps),
-                            y.data_ptr(), yb, yt, mp, rp, flags), x, weight=weight, bias=bias)
+    _run("rtl_layer_norm", (x.data_ptr(), batch, tokens, c, xb, xt, wp, ws, bp, bs, offset, eps, y.data_ptr(), yb, yt, mp, rp,
+                            flags), _here(x, weight, bias), x, weight=weight, bias=bias)
     return (y, mean, rstd) if return_stats else y
 
 
@@ -166,31 +168,36 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, offset: float = 0.0, nee
     dweight and dbias have weight's shape and type, summed over the tokens (and
     the sequences that share a row); without a weight both are None."""
     torch = _torch()
-    flags = _type_flag(x, "x")
+    flags = _type_flag(torch, x, "x")
+    shape = x.shape
     if dy.dtype is not x.dtype:
         raise TypeError(f"dy must be {x.dtype} like x, got {dy.dtype}")
-    if dy.shape != x.shape:
-        raise ValueError(f"dy must have shape {tuple(x.shape)}, got {tuple(dy.shape)}")
+    if dy.shape != shape:
+        raise ValueError(f"dy must have shape {tuple(shape)}, got {tuple(dy.shape)}")
     batch, tokens, xb, xt = _layout(x, "x")
     _, _, gb, gt = _layout(dy, "dy")
     for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype is not torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])}")
+        if t.dtype is not torch.float32 or t.shape != shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape[:-1])}")
+    c = shape[-1]
     wp, ws, groups = None, 0, 1
-    dw = db = work = None
+    dw = db = dx = None
+    dwp = dbp = dxp = work = None
+    size = 0
     if weight is not None:
-        wp, ws, groups = _affine(weight, "weight", x, x.dim() == 3)
+        wp, ws, groups = _affine(torch, weight, "weight", x, shape)
         if weight.dtype is torch.float32:
             flags |= _AFFINE_FP32
         if need_affine:
-            dw = torch.empty(weight.shape, dtype=weight.dtype, device=x.device)
-            db = torch.empty_like(dw)
-            work = _workspace(workspace, backward_workspace_bytes(batch, tokens, x.shape[-1], groups), x.device)
-    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
-    _, _, db_, dt = _layout(dx, "dx") if need_dx else (0, 0, 0, 0)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            dw, db = weight.new_empty(weight.shape), weight.new_empty(weight.shape)
+            size = backward_workspace_bytes(batch, tokens, c, groups)
+            workspace = _workspace(workspace, size, x.device)
+            dwp, dbp, work, size = dw.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel()
+    if need_dx:
+        dx = x.new_empty(shape)
+        dxp = dx.data_ptr()
     _run("rtl_layer_norm_backward",
-         (dy.data_ptr(), gb, gt, x.data_ptr(), xb, xt, mean.data_ptr(), rstd.data_ptr(), batch, tokens, x.shape[-1], wp, ws,
-          float(offset), groups, ptr(dx), db_, dt, ptr(dw), ptr(db), ptr(work), 0 if work is None else work.numel(), flags),
-         x, dy=dy, mean=mean, rstd=rstd, weight=weight)
+         (dy.data_ptr(), gb, gt, x.data_ptr(), xb, xt, mean.data_ptr(), rstd.data_ptr(), batch, tokens, c, wp, ws, offset,
+          groups, dxp, tokens * c, c, dwp, dbp, work, size, flags),
+         _here(x, dy, mean, rstd, weight), x, dy=dy, mean=mean, rstd=rstd, weight=weight)
     return dx, dw, db

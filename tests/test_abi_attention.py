@@ -8,33 +8,44 @@ torch = pytest.importorskip("torch")
 
 from activation_sparse_gemm_token_amd import attention as at  # noqa: E402
 
+class _Tensor(ctypes.Structure):
+    """rtl_attn_tensor."""
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("batch_stride", "token_stride", "head_stride")]
+
+
+class _Shape(ctypes.Structure):
+    """rtl_attn_shape."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("sequences", "tokens_q", "tokens_k", "heads_q", "heads_k", "head_dim")] + [
+        (n, ctypes.c_void_p) for n in ("q_starts", "k_starts", "k_lens")] + [("scale", ctypes.c_float)]
+
+
 OK, NULLP, SHAPE, MISAL, WS, NODEV, ARCH, HIP, FLAGS = range(9)
 P = 0x10000
 
 
 def _shape(**kw):
-    s = at._Shape(2, 5, 7, 4, 2, 64, None, None, None, 0.125)
+    s = _Shape(2, 5, 7, 4, 2, 64, None, None, None, 0.125)
     for k, v in kw.items():
         setattr(s, k, v)
-    return s
+    return ctypes.pointer(s)
 
 
 def _tensors(n, which, **kw):
-    t = [at._Tensor(P * (i + 1), 1 << 16, 256, 64) for i in range(n)]
+    t = [_Tensor(P * (i + 1), 1 << 16, 256, 64) for i in range(n)]
     for k, v in kw.items():
         setattr(t[which], k, v)
-    return t
+    return [ctypes.pointer(i) for i in t]
 
 
 def _forward(flags=0, ws=None, wsb=0, lse=None, which=0, t=None, **kw):
-    shape = {k: v for k, v in kw.items() if hasattr(at._Shape, k)}
-    tensor = {k: v for k, v in kw.items() if not hasattr(at._Shape, k)}
+    shape = {k: v for k, v in kw.items() if hasattr(_Shape, k)}
+    tensor = {k: v for k, v in kw.items() if not hasattr(_Shape, k)}
     return at._fn("rtl_attention")(*(t or _tensors(4, which, **tensor)), lse, _shape(**shape), ws, wsb, flags, None)
 
 
 def _backward(flags=0, ws=P, wsb=1 << 20, lse=P, which=0, t=None, **kw):
-    shape = {k: v for k, v in kw.items() if hasattr(at._Shape, k)}
-    tensor = {k: v for k, v in kw.items() if not hasattr(at._Shape, k)}
+    shape = {k: v for k, v in kw.items() if hasattr(_Shape, k)}
+    tensor = {k: v for k, v in kw.items() if not hasattr(_Shape, k)}
     t = t or _tensors(8, which, **tensor)
     return at._fn("rtl_attention_backward")(*t[:5], lse, *t[5:], _shape(**shape), ws, wsb, flags, None)
 
@@ -108,5 +119,7 @@ def test_binding_needs_device_tensors_that_fit():
 
 
 def test_structures_match_the_header():
-    assert ctypes.sizeof(at._Tensor) == 32 and ctypes.sizeof(at._Shape) == 80
-    assert at._Shape.scale.offset == 72
+    assert ctypes.sizeof(_Tensor) == 32 == at._TENSOR.size and ctypes.sizeof(_Shape) == 80 == at._SHAPE.size
+    assert _Shape.scale.offset == 72
+    s = _Shape.from_buffer_copy(at._SHAPE.pack(*range(1, 10), 0.5))
+    assert [getattr(s, n) for n, _ in _Shape._fields_] == [*range(1, 10), 0.5]
