@@ -108,9 +108,24 @@ __device__ __forceinline__ void bias_load(const LinearEpi& e, int64_t n, int64_t
   for (int i = 0; i < W; ++i) bias[i] = e.bias != nullptr && n + i < N ? word_to_f32<TYPE>(e.bias[n + i]) : 0.f;
 }
 
+// The gate of these channels in row m (1 without one), and the first row past its rows.
+template <int TYPE, int W>
+__device__ __forceinline__ int64_t gate_load(const LinearEpi& e, int64_t m, int64_t n, int64_t N, float (&gate)[W]) {
+  if (e.gate == nullptr) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) gate[i] = 1.f;
+    return (int64_t)1 << 62;
+  }
+  const int64_t row = m / e.gate_tokens;
+  const uint16_t* const p = e.gate + row * e.gate_stride + n;
+#pragma unroll
+  for (int i = 0; i < W; ++i) gate[i] = n + i < N ? word_to_f32<TYPE>(p[i]) : 0.f;
+  return (row + 1) * e.gate_tokens;
+}
+
 template <int TYPE, int W>
 __device__ __forceinline__ void epilogue(const LinearEpi& e, int64_t m, int64_t n, int64_t N, bool wide, const float (&bias)[W],
-                                         float (&v)[W]) {
+                                         const float (&gate)[W], float (&v)[W]) {
   const int64_t at = m * N + n;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
@@ -138,10 +153,8 @@ __device__ __forceinline__ void epilogue(const LinearEpi& e, int64_t m, int64_t 
       break;
   }
   if (e.gate != nullptr) {
-    const uint16_t* const gate = e.gate + m / e.gate_tokens * e.gate_stride + n;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (n + i < N) v[i] *= word_to_f32<TYPE>(gate[i]);
+    for (int i = 0; i < W; ++i) v[i] *= gate[i];
   }
   if (wide) {
     if (e.residual != nullptr) {
@@ -240,7 +253,7 @@ struct Operand {
   }
 };
 
-template <int TYPE, int T, bool A_ALONG, bool B_ALONG>
+template <int TYPE, int T, int STAGES, bool A_ALONG, bool B_ALONG>
 __global__ void __launch_bounds__(2 * T, T == 256 ? 1 : 2)
 linear_gemm_kernel(LinearGemm g) {
   using A = Operand<T, A_ALONG>;
@@ -248,7 +261,7 @@ linear_gemm_kernel(LinearGemm g) {
   constexpr int kWaves = T / 32, kWavesN = T / 64, kRB = T == 256 ? 8 : 4, kCB = 4;
   constexpr int kTile = A::kBytes, kRowBytes = 64 * 4 + 16, kStaging = kWaves * 64 * kRowBytes;
   static_assert(kWaves == (T / (16 * kRB)) * kWavesN, "wavefronts cover the tile");
-  __shared__ __attribute__((aligned(16))) char lds[kStaging > 4 * kTile ? kStaging : 4 * kTile];   // A, B of two steps; epilogue
+  __shared__ __attribute__((aligned(16))) char lds[kStaging > 2 * STAGES * kTile ? kStaging : 2 * STAGES * kTile];   // A, B of the steps; epilogue
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / kWavesN, wn = wave % kWavesN;
   const int64_t tiles_m = (g.M + T - 1) / T, tiles_n = (g.N + T - 1) / T, tiles = tiles_m * tiles_n;
@@ -271,10 +284,11 @@ linear_gemm_kernel(LinearGemm g) {
 #pragma unroll
     for (int j = 0; j < kCB; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
 
-  // Two stages of both operands.  Half of a step's fragments (32 of the contraction) are in registers ahead of their
+  // A ring of stages of both operands.  Half of a step's fragments (32 of the contraction) are in registers ahead of their
   // products: the other half is read from LDS during the first half's products, and the next step's first
   // half during the second's.  The barrier between them comes after the last read of a stage, so the copy of
-  // step s + 2 goes out there, a whole step before it is waited for.  (One stage more for B, the whole step's
+  // step s + STAGES goes out there: with two stages a whole step before it is waited for, which is enough where other
+  // wavefronts fill the wait; a 128 x 128 tile alone on its CU has four.  (One stage more for B, the whole step's
   // fragments read at its top: 429 us for the 4096 x 2048 x 8192 training step, 420 this way; the loop unrolled
   // over the stages is 2 % faster at 4096 x 4096 x 12288 forward but spills where operands run across.)
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)(lds);
@@ -301,25 +315,31 @@ linear_gemm_kernel(LinearGemm g) {
       for (int j = 0; j < kCB; ++j) acc[i][j] = mfma16<TYPE>(fb[h][j], fa[h][i], acc[i][j]);
   };
   if (steps > 0) {
-    copy(0, 0);
-    wait_vm<0>();
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+      if (i < steps) copy(i, i);
+    if (steps >= STAGES) wait_vm<8 * (STAGES - 1)>();
+    else wait_vm<0>();
     barrier_no_fence();
-    if (steps > 1) copy(1, 1);
     read(0, First{});
+    int stage = 0;
 #pragma unroll 1
     for (int64_t s = 0; s < steps; ++s) {
-      const int stage = (int)(s & 1);
+      const int next = stage + 1 < STAGES ? stage + 1 : 0;
       read(stage, Second{});
       multiply(First{});
       __builtin_amdgcn_sched_barrier(0);
       // This wavefront's reads of the stage are back, and its copies of the next one.
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      if (s + STAGES - 1 < steps) wait_vm<8 * (STAGES - 2)>();
+      else wait_vm<0>();
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       barrier_no_fence();
-      if (s + 2 < steps) copy(s + 2, stage);
+      if (s + STAGES < steps) copy(s + STAGES, stage);
       __builtin_amdgcn_sched_barrier(0);
-      read(1 - stage, First{});                         // after the last step: not used
+      read(next, First{});                              // after the last step: not used
       multiply(Second{});
       __builtin_amdgcn_sched_barrier(0);
+      stage = next;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
@@ -329,8 +349,9 @@ linear_gemm_kernel(LinearGemm g) {
   char* const mine = lds + wave * 64 * kRowBytes;
   const int64_t n = n0 + 64 * wn + 8 * (lane & 7);
   const bool wide = g.N % 8 == 0;
-  float bias[8];
+  float bias[8], gate[8];
   bias_load<TYPE, 8>(g.e, n, g.N, bias);
+  int64_t gate_end = 0;
 #pragma unroll
   for (int pass = 0; pass < kRB / 4; ++pass) {
 #pragma unroll
@@ -358,7 +379,8 @@ linear_gemm_kernel(LinearGemm g) {
             if (n + e < g.N) out[e] = v[e];
         }
       } else {
-        epilogue<TYPE, 8>(g.e, r, n, g.N, wide, bias, v);
+        if (r >= gate_end) gate_end = gate_load<TYPE, 8>(g.e, r, n, g.N, gate);
+        epilogue<TYPE, 8>(g.e, r, n, g.N, wide, bias, gate, v);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the next pass writes over what was read
@@ -386,7 +408,9 @@ linear_join_kernel(LinearGemm g) {
         if (n + e < g.N) v[e] += p[e];
     }
   }
-  epilogue<TYPE, 4>(g.e, m, n, g.N, wide, bias, v);
+  float gate[4];
+  gate_load<TYPE, 4>(g.e, m, n, g.N, gate);
+  epilogue<TYPE, 4>(g.e, m, n, g.N, wide, bias, gate, v);
 }
 
 // --- Few rows ------------------------------------------------------------------
@@ -449,7 +473,11 @@ linear_rows_kernel(LinearGemm g) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     float v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
-    if (16 * i + row < g.M && n < g.N) epilogue<TYPE, 4>(g.e, 16 * i + row, n, g.N, g.N % 4 == 0, bias, v);
+    if (16 * i + row < g.M && n < g.N) {
+      float gate[4];
+      gate_load<TYPE, 4>(g.e, 16 * i + row, n, g.N, gate);
+      epilogue<TYPE, 4>(g.e, 16 * i + row, n, g.N, g.N % 4 == 0, bias, gate, v);
+    }
   }
 }
 
@@ -534,8 +562,9 @@ hipError_t run_gemm(const LinearGemm& g, hipStream_t stream) {
   const int64_t T = g.tile, tiles = ((g.M + T - 1) / T) * ((g.N + T - 1) / T);
   const dim3 grid((unsigned)(tiles * g.splits));
   hipError_t e;
-  if (T == 256) e = launch(&linear_gemm_kernel<TYPE, 256, A_ALONG, B_ALONG>, grid, dim3(512), stream, g);
-  else e = launch(&linear_gemm_kernel<TYPE, 128, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
+  if (T == 256) e = launch(&linear_gemm_kernel<TYPE, 256, 2, A_ALONG, B_ALONG>, grid, dim3(512), stream, g);
+  else if (tiles * g.splits > 256) e = launch(&linear_gemm_kernel<TYPE, 128, 2, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
+  else e = launch(&linear_gemm_kernel<TYPE, 128, 4, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
   if (e != hipSuccess || g.splits == 1) return e;
   return launch(&linear_join_kernel<TYPE>, folded_grid((g.M * ((g.N + 3) / 4) + 255) / 256), dim3(256), stream, g);
 }

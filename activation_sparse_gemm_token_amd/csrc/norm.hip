@@ -17,12 +17,33 @@ namespace {
 
 constexpr int kBlock = 256;
 
+// Sum over a wavefront, the same bits in every lane: by data-parallel moves within rows of 16 lanes (xor 1
+// and 2, mirrored halves, mirrored rows), then by swaps of rows and halves; no trip through LDS.
+template <int CTRL>
+__device__ __forceinline__ float add_moved(float v) {
+  const int w = __builtin_bit_cast(int, v);
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(w, w, CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_moved<0xB1>(v);                               // quad_perm 1, 0, 3, 2
+  v = add_moved<0x4E>(v);                               // quad_perm 2, 3, 0, 1
+  v = add_moved<0x141>(v);                              // row_half_mirror
+  v = add_moved<0x140>(v);                              // row_mirror
+  const uint32_t a = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  v = __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t h0 = h[0], h1 = h[1];
+  return __builtin_bit_cast(float, h0) + __builtin_bit_cast(float, h1);
+}
+
 // Sum over the TPR threads of a row, the same bits in all of them.  `lds` is the
 // row's slots [TPR / 64], a fresh set in each call between two barriers.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) v += __shfl_xor(v, d, 64);
+  v = wave_sum(v);
   if constexpr (TPR > 64) {
     if ((threadIdx.x & 63) == 0) lds[(threadIdx.x % TPR) >> 6] = v;
     __syncthreads();
@@ -190,11 +211,8 @@ norm_backward_kernel(NormBackArgs a) {
       }
     }
     if (a.dx == nullptr) return;                        // uniform over the grid
-#pragma unroll
-    for (int d = 32; d >= 1; d /= 2) {
-      s1 += __shfl_xor(s1, d, 64);
-      s2 += __shfl_xor(s2, d, 64);
-    }
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
     if constexpr (TPR > 64) {
       float* const mine = lds[flip][sub];
       if ((threadIdx.x & 63) == 0) {

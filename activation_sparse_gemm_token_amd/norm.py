@@ -142,14 +142,15 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, offset: float = 0.0
         bp, bs, _ = _affine(torch, bias, "bias", x, shape)
     c = shape[-1]
     if out is None:
-        y, yb, yt = x.new_empty(shape), tokens * c, c
+        y, yb, yt = torch.empty_like(x, memory_format=torch.contiguous_format), tokens * c, c
     else:
         _check_out(out, x, x=x, weight=weight, bias=bias)
         y = out
         _, _, yb, yt = _layout(y, "out")
     mean = rstd = mp = rp = None
     if return_stats:
-        mean, rstd = x.new_empty(shape[:-1], dtype=torch.float32), x.new_empty(shape[:-1], dtype=torch.float32)
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     _run("rtl_layer_norm", (x.data_ptr(), batch, tokens, c, xb, xt, wp, ws, bp, bs, offset, eps, y.data_ptr(), yb, yt, mp, rp,
                             flags), _here(x, weight, bias), x, weight=weight, bias=bias)
@@ -189,12 +190,13 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, offset: float = 0.0, nee
         if weight.dtype is torch.float32:
             flags |= _AFFINE_FP32
         if need_affine:
-            dw, db = weight.new_empty(weight.shape), weight.new_empty(weight.shape)
+            dw = torch.empty_like(weight, memory_format=torch.contiguous_format)
+            db = torch.empty_like(dw)
             size = backward_workspace_bytes(batch, tokens, c, groups)
             workspace = _workspace(workspace, size, x.device)
             dwp, dbp, work, size = dw.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel()
     if need_dx:
-        dx = x.new_empty(shape)
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
         dxp = dx.data_ptr()
     _run("rtl_layer_norm_backward",
          (dy.data_ptr(), gb, gt, x.data_ptr(), xb, xt, mean.data_ptr(), rstd.data_ptr(), batch, tokens, c, wp, ws, offset,
