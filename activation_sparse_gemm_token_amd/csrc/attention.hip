@@ -417,10 +417,12 @@ attn_join_kernel(AttnArgs a) {
     head = kv * a.group + r % a.group;
   }
   float m = ninf();
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) m = __builtin_fmaxf(m, a.part_ml[(first + s * step) * 2]);
   const float mu = m == ninf() ? 0.f : m;
   float l = 0.f;
   f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float* const ml = a.part_ml + (first + s * step) * 2;
     const float f = exp2_(ml[0] - mu);
@@ -467,8 +469,8 @@ hipError_t by_blocks(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream
 
 }  // namespace
 
-// Up to 32 queries of a sequence go to attn_few_kernel, its keys in ranges of at least 512 until there
-// are three workgroups per CU.  Otherwise tiles of 128 queries; a batch's tiles are alike, so where their
+// Up to 32 queries of a sequence go to attn_few_kernel, its keys in ranges of at least 256 until there
+// is one workgroup per CU (one token, 65536 keys in 8 heads: 53 us; two 61, three 71: more parts to join).  Otherwise tiles of 128 queries; a batch's tiles are alike, so where their
 // number is no multiple of what the card holds (256 CUs times the wavefronts per SIMD) the last, partly
 // filled round would leave CUs idle: the keys of its tiles are split over workgroups, 256 keys at least for
 // each.  Causal tiles shrink towards the end by themselves, and packed ones differ anyway.
@@ -477,8 +479,8 @@ AttnPlan attn_plan(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_
   if (packed || sequences == 0 || tq == 0 || hk == 0 || hq == 0) return p;
   if (tq <= 32) {
     const int64_t rows = tq * (hq / hk), groups = sequences * hk * ((rows + 31) / 32);
-    int64_t splits = (768 + groups - 1) / groups;
-    const int64_t most = (tk + 511) / 512;
+    int64_t splits = (256 + groups - 1) / groups;
+    const int64_t most = (tk + 255) / 256;
     if (splits > most) splits = most;
     p.few = true;
     p.splits = splits < 1 ? 1 : (int)splits;
