@@ -2,9 +2,10 @@
 //
 //   1. attn_delta_kernel   D = sum of d_o o per query and head, beside the log-sum-exp in
 //                          log2 units (+inf where no key is seen: p is 0 then).
-//   2. attn_dkv_kernel     dK, dV: a wavefront holds 32 keys, its workgroup walks the
+//   2. attn_dq_kernel      dQ: as the forward pass, 32 queries a wavefront.
+//   3. attn_dkv_kernel     dK, dV: a wavefront holds 32 keys, its workgroup walks the
 //                          queries of all heads that share the key head.
-//   3. attn_dq_kernel      dQ: as the forward pass, 32 queries a wavefront.
+//   4. attn_dkv_join_kernel  where few key heads leave few workgroups, 3 splits the queries.
 //
 // S and dP are formed in both (7 products where 5 would do with atomic sums), so
 // nothing is added atomically and shared heads sum in registers.  Everything
@@ -333,10 +334,36 @@ attn_dq_kernel(AttnBackArgs a) {
     col_off[nb][0] = T::column_operand(nb, 0);
     col_off[nb][1] = T::column_operand(nb, 1);
   }
+  // Few keys: o is near the values, ds a difference of near numbers, and o's rounding in D would show (with two
+  // keys dQ and dK were 0.4 % off instead of 0.24 %).  D is the sum of p dP too: formed so where the keys fit
+  // the two tiles of LDS, and left for the dK / dV kernel, which runs after this one.
+  const bool few = steps <= 2;
+  if (few && steps > 0) {
+    if (steps == 2) copy(1);
+    wait_copies<0>();
+    group_barrier();
+    float sum = 0.f;
+    if (mine > 0) {
+      const int left = clamp_rows(limit);
+#pragma unroll 1
+      for (int kb = 0; kb < 2 * steps; ++kb) {
+        const char* const kk = lds + (kb >> 1) * 2 * kTile + (kb & 1) * 32 * T::kPitch;
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c) s = mfma32<kBf16>(lds_read16(kk + row_off[c]), qf[c], s);
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c) dp = mfma32<kBf16>(lds_read16(kk + kTile + row_off[c]), df[c], dp);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += 32 * kb + block_row(i) < left ? exp2_(__builtin_fmaf(s[i], f.c, -lse2)) * dp[i] : 0.f;
+      }
+    }
+    delta = half_sum(sum);
+    if (live && lane < 32) a.stats[w.lse_off + row] = (f32x2){lse2, delta};
+  }
   for (int j = 0; j < steps; ++j) {
     wait_copies<0>();
     group_barrier();
-    if (j + 1 < steps) copy(j + 1);
+    if (j + 1 < steps && !few) copy(j + 1);
     const int64_t k0 = (int64_t)j * kKeys;
     if (k0 >= mine) continue;
     const char* const kt = lds + (j & 1) * 2 * kTile;
@@ -375,21 +402,21 @@ template <int NB>
 hipError_t run_backward(AttnBackArgs a, hipStream_t stream) {
   const bool packed = a.f.q_starts != nullptr;
   const int64_t batch = packed ? 1 : a.f.sequences;
-  if (a.f.tk > 0 && a.f.hk > 0) {
-    a.f.tiles = packed ? a.f.tk / kKvKeys + a.f.sequences + 1 : (a.f.tk + kKvKeys - 1) / kKvKeys;
-    a.f.groups = a.f.tiles * a.f.hk * batch * a.f.splits;
-    hipError_t e = launch(&attn_dkv_kernel<NB>, folded_grid(a.f.groups), dim3(64 * kKvWaves), stream, a);
-    if (e == hipSuccess && a.f.splits > 1) {
-      const int64_t items = batch * a.f.tk * a.f.hk * (a.f.d / 8) * 2;
-      e = launch(&attn_dkv_join_kernel, folded_grid((items + 255) / 256), dim3(256), stream, a);
-    }
+  if (a.f.tq > 0 && a.f.hq > 0) {
+    AttnBackArgs q = a;
+    constexpr int kQueries = 32 * kDqWaves;
+    q.f.tiles = packed ? a.f.tq / kQueries + a.f.sequences + 1 : (a.f.tq + kQueries - 1) / kQueries;
+    q.f.groups = q.f.tiles * a.f.hq * batch;
+    const hipError_t e = launch(&attn_dq_kernel<NB>, folded_grid(q.f.groups), dim3(64 * kDqWaves), stream, q);
     if (e != hipSuccess) return e;
   }
-  if (a.f.tq == 0 || a.f.hq == 0) return hipSuccess;
-  constexpr int kQueries = 32 * kDqWaves;
-  a.f.tiles = packed ? a.f.tq / kQueries + a.f.sequences + 1 : (a.f.tq + kQueries - 1) / kQueries;
-  a.f.groups = a.f.tiles * a.f.hq * batch;
-  return launch(&attn_dq_kernel<NB>, folded_grid(a.f.groups), dim3(64 * kDqWaves), stream, a);
+  if (a.f.tk == 0 || a.f.hk == 0) return hipSuccess;
+  a.f.tiles = packed ? a.f.tk / kKvKeys + a.f.sequences + 1 : (a.f.tk + kKvKeys - 1) / kKvKeys;
+  a.f.groups = a.f.tiles * a.f.hk * batch * a.f.splits;
+  const hipError_t e = launch(&attn_dkv_kernel<NB>, folded_grid(a.f.groups), dim3(64 * kKvWaves), stream, a);
+  if (e != hipSuccess || a.f.splits == 1) return e;
+  const int64_t items = batch * a.f.tk * a.f.hk * (a.f.d / 8) * 2;
+  return launch(&attn_dkv_join_kernel, folded_grid((items + 255) / 256), dim3(256), stream, a);
 }
 
 }  // namespace

@@ -20,9 +20,9 @@ def visible(nq, nk, causal, dev):
     return m.tril(nk - nq) if causal else m
 
 
-def one(q, k, v, scale, causal, d_o=None):
+def one(q, k, v, scale, causal, d_o=None, few=False):
     """q [nq, d], k, v [nk, d] of one head: dict of o, lse and (with d_o) dq, dk, dv, each a pair
-    (value, allowance), fp64."""
+    (value, allowance), fp64.  ``few``: D is formed from p and dP, not from the rounded o (up to 128 keys)."""
     h, dtype = half(q.dtype), q.dtype
     q, k, v = (t.double() for t in (q, k, v))
     (nq, d), nk = q.shape, k.shape[0]
@@ -59,6 +59,8 @@ def one(q, k, v, scale, causal, d_o=None):
     dd_err = (g.abs() * o_err).sum(1, keepdim=True) + (d + 4) * U * (g.abs() * o.abs()).sum(1, keepdim=True)
     dp_err = (d + 4) * U * torch.mm(g.abs(), v.abs().t())
     p_err = p * (ds_ + most + (2 * nk + 48) * U)
+    if few:
+        dd_err = (p_err * dp.abs() + p * dp_err + (nk + 8) * U * p * dp.abs()).sum(1, keepdim=True)
     ds_err = h * ds.abs() + (1 + h) * (p_err * (dp - dd).abs() + (p + p_err) * (dp_err + dd_err + 4 * U * (dp.abs() + dd.abs())))
     n = 2 * (nq + nk) * U
     out["dv"] = (torch.mm(p.t(), g), torch.mm((p_err + h * p + n * p).t(), g.abs()))
