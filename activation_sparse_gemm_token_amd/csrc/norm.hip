@@ -153,7 +153,8 @@ norm_backward_kernel(NormBackArgs a) {
   extern __shared__ float lds_sums[];                   // [TPR E] floats where the sums are joined
   __shared__ float lds[2][kRows][2 * kWaves];           // alternating, so one barrier a row is enough
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const int64_t group = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int64_t group = folded_block() / a.parts, part = folded_block() - group * a.parts;
+  if (group >= a.groups) return;
   const int64_t group_rows = a.rows / a.groups;
   float dw[E], db[E];
 #pragma unroll
@@ -298,10 +299,12 @@ norm_backward_kernel(NormBackArgs a) {
 // parts p, p + 16, ..., the 16 sums are added in order.
 template <int TYPE>
 __global__ void __launch_bounds__(1024)
-norm_join_kernel(const float* __restrict__ partials, int64_t parts, int64_t C, void* dweight, void* dbias) {
+norm_join_kernel(const float* __restrict__ partials, int64_t groups, int64_t parts, int64_t C, void* dweight, void* dbias) {
   __shared__ float lds[16][64];
   const int col = threadIdx.x & 63, p = threadIdx.x >> 6;
-  const int64_t group = blockIdx.y, c = (int64_t)blockIdx.x * 64 + col;   // of 2 C: dweight, then dbias
+  const int64_t per = (2 * C + 63) / 64, group = folded_block() / per;
+  if (group >= groups) return;
+  const int64_t c = (folded_block() - group * per) * 64 + col;            // of 2 C: dweight, then dbias
   float s = 0.f;
   if (c < 2 * C)
     for (int64_t i = p; i < parts; i += 16) s += partials[(group * parts + i) * 2 * C + c];
@@ -329,14 +332,19 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   return go(&norm_kernel<TYPE, VEC, 1024, 32>, 1024, 1);
 }
 
+// Sequences with their own weights may be many: more workgroups of 1024 than one dimension holds go to z.
+dim3 grid_of_1024(int64_t blocks) {
+  constexpr int64_t kRow = (int64_t)1 << 21;
+  return blocks <= kRow ? dim3((unsigned)blocks) : dim3((unsigned)kRow, 1, (unsigned)((blocks + kRow - 1) / kRow));
+}
+
 template <int TYPE, int VEC>
 hipError_t run_backward(const NormBackArgs& a, hipStream_t stream) {
   auto go = [&](auto k, int tpr, int e) {
     NormBackArgs args = a;
     void* ptrs[] = {&args};
     const size_t lds = a.partials != nullptr && tpr < kBackBlock ? (size_t)tpr * e * 4 : 0;
-    return hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((unsigned)(a.groups * a.parts)), dim3(kBackBlock), ptrs,
-                           lds, stream);
+    return hipLaunchKernel(reinterpret_cast<const void*>(k), grid_of_1024(a.groups * a.parts), dim3(kBackBlock), ptrs, lds, stream);
   };
   if (a.C <= 512) return go(&norm_backward_kernel<TYPE, VEC, 64, 8>, 64, 8);
   if (a.C <= 1024) return go(&norm_backward_kernel<TYPE, VEC, 64, 16>, 64, 16);
@@ -375,10 +383,10 @@ hipError_t launch_norm_backward(const NormBackArgs& a, int type, int vec, hipStr
   else
     e = vec == 8 ? run_backward<kBf16, 8>(a, stream) : vec == 4 ? run_backward<kBf16, 4>(a, stream) : run_backward<kBf16, 1>(a, stream);
   if (e != hipSuccess || a.partials == nullptr) return e;
-  const dim3 grid((unsigned)((2 * a.C + 63) / 64), (unsigned)a.groups);
+  const dim3 grid = grid_of_1024((2 * a.C + 63) / 64 * a.groups);
   const int out = a.affine_fp32 ? kFp32 : type;
   auto* k = out == kFp32 ? &norm_join_kernel<kFp32> : out == kFp16 ? &norm_join_kernel<kFp16> : &norm_join_kernel<kBf16>;
-  return launch(k, grid, dim3(1024), stream, (const float*)a.partials, a.parts, (int64_t)a.C, a.dweight, a.dbias);
+  return launch(k, grid, dim3(1024), stream, (const float*)a.partials, a.groups, a.parts, (int64_t)a.C, a.dweight, a.dbias);
 }
 
 }  // namespace rtl

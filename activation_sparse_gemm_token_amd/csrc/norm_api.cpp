@@ -22,6 +22,13 @@ struct Width {
   void add(int64_t v) {
     while (v % bytes != 0) bytes /= 2;
   }
+  // Weight or bias: beside 16-bit tensors fp32 ones are read 16 bytes at a time whatever the width.
+  void affine(const void* p, int64_t stride, int elem, int wsize) {
+    if (p == nullptr) return;
+    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) & 15) | (stride * wsize & 15);
+    if (wsize > elem) bytes = at != 0 ? 2 : bytes;
+    else add(at);
+  }
   int vec(int elem) const { return bytes == 16 ? 16 / elem : bytes == 8 && elem == 2 ? 4 : 1; }
 };
 
@@ -57,9 +64,8 @@ RTL_API rtl_status rtl_layer_norm(const void* x, int64_t batch, int64_t tokens, 
   w.add(x);
   w.add(y);
   for (int64_t s : {C, x_batch_stride, x_token_stride, y_batch_stride, y_token_stride}) w.add(s * elem);
-  for (const void* p : {weight, bias}) w.add(p);
-  if (weight != nullptr) w.add(weight_batch_stride * wsize);
-  if (bias != nullptr) w.add(bias_batch_stride * wsize);
+  w.affine(weight, weight_batch_stride, elem, wsize);
+  w.affine(bias, bias_batch_stride, elem, wsize);
   rtl::NormArgs a{};
   a.x = x;
   a.y = y;
@@ -118,13 +124,13 @@ RTL_API rtl_status rtl_layer_norm_backward(const void* dy, int64_t dy_batch_stri
   if (dweight != nullptr && (workspace == nullptr || workspace_bytes < partial_bytes(rows, C, groups)))
     return RTL_ERR_WORKSPACE;
   Width w;
-  for (const void* p : {x, dy, (const void*)dx, weight}) w.add(p);
+  for (const void* p : {x, dy, (const void*)dx}) w.add(p);
   for (int64_t s : {C, x_batch_stride, x_token_stride, dy_batch_stride, dy_token_stride}) w.add(s * elem);
   if (dx != nullptr) {
     w.add(dx_batch_stride * elem);
     w.add(dx_token_stride * elem);
   }
-  if (weight != nullptr) w.add(weight_batch_stride * wsize);
+  w.affine(weight, weight_batch_stride, elem, wsize);
   rtl::NormBackArgs a{};
   a.dy = dy;
   a.x = x;

@@ -234,3 +234,19 @@ def test_same_bits_and_captured():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
+def test_fp32_weights_on_half_their_access():
+    """fp32 weight and bias that begin 8 bytes past a multiple of 16, beside bf16 rows."""
+    x, dy = rand(3, 40, 96, seed=1, dtype=BF), rand(3, 40, 96, seed=2, dtype=BF)
+    w, b = (rand(3, 98, seed=i)[:, 2:] for i in (3, 4))
+    assert w.data_ptr() % 16 == 8
+    y, m, r = norm.layer_norm(x, w, b, return_stats=True)
+    check(y, *forward_want(x, w, b, 1e-5, 0.0), "y")
+    dx = norm.layer_norm_backward(dy, x, m, r, w)[0]
+    check(dx, *backward_want(dy, x, w, 1e-5, 0.0)[:2], "dx")
+
+
+def test_weights_of_many_sequences():
+    """More sequences with rows of their own than a grid's second dimension holds."""
+    run((70_000, 1, 16), BF, "sequence", seed=5)
