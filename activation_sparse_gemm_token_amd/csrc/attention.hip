@@ -402,7 +402,7 @@ attn_join_kernel(AttnArgs a) {
     first = tile * a.splits * kForwardQueries + r;
     step = kForwardQueries;
     const int64_t id = a.whole + tile, item = id / a.tiles, t = id - item * a.tiles;
-    tok = (a.causal ? a.tiles - 1 - t : t) * kForwardQueries + r;
+    tok = t * kForwardQueries + r;
     if (tok >= a.tq) return;
     seq = item / a.hq;
     head = item - seq * a.hq;

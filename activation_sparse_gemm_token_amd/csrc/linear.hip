@@ -62,7 +62,7 @@ constexpr float kTanhA = 0.7978845608028654f, kTanhB = 0.044715f;
 __device__ __forceinline__ float act(float z, int kind) {
   switch (kind) {
     case kActGelu: {
-      const float low = z * phi_lower(z);               // z Phi(-|z|)
+      const float low = __builtin_amdgcn_fmed3f(z, -64.f, 64.f) * phi_lower(z);        // z Phi(-|z|), 0 beyond
       return z > 0.f ? z - low : low;
     }
     case kActGeluTanh:                                  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)

@@ -8,6 +8,7 @@ namespace {
 constexpr int64_t kMaxBytes = (int64_t)1 << 31;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxGateRows = 65535;
+constexpr int64_t kMaxWidth = (int64_t)1 << 25;          // 64 rows, a step of the contraction, stay below 2^32 bytes
 
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -17,7 +18,7 @@ bool bytes_ok(int64_t rows, int64_t cols) {
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && N >= 0 && M < kMaxBytes && N < kMaxBytes - 8 && K >= 8 && K < kMaxBytes && K % 8 == 0 && bytes_ok(M, K) &&
+  return M >= 0 && N >= 0 && M < kMaxBytes && N < kMaxWidth && K >= 8 && K < kMaxWidth && K % 8 == 0 && bytes_ok(M, K) &&
          bytes_ok(N, K) && bytes_ok(M, up8(N));
 }
 

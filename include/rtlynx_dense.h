@@ -47,7 +47,7 @@ extern "C" {
  *   workspace rtl_linear_workspace_bytes(M, N, K) bytes, 16-byte aligned (0
  *             for most sizes: it serves products split over K).
  *
- * M == 0 or N == 0 is a no-op.  0 <= gate_stride < 2^40.
+ * M == 0 or N == 0 is a no-op.  N, K < 2^25, every tensor below 2 GiB, 0 <= gate_stride < 2^40.
  */
 size_t rtl_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 

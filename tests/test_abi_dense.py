@@ -70,3 +70,10 @@ def test_binding_needs_device_tensors():
         dense.linear(x.float(), w.float())
     with pytest.raises(ValueError):
         dense.linear(x, w, activation="relu6")
+
+
+def test_widths():
+    for bad in (dict(m=1, n=1 << 25, k=8), dict(m=1, n=8, k=1 << 25)):
+        assert _forward(**bad) == SHAPE and _backward(**bad) == SHAPE and dense.workspace_bytes(bad["m"], bad["n"], bad["k"]) == 0, bad
+    if _no_gpu():
+        assert _forward(m=1, n=(1 << 25) - 8, k=8) == NODEV

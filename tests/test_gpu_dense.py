@@ -247,3 +247,11 @@ def test_same_bits_and_captured():
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(out, want))
         assert all(torch.equal(a, c) for a, c in zip(step(), want))
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_a_sum_past_fp32(act):
+    """z = inf is its own activation in every form."""
+    x = torch.full((40, 8), 3e38, dtype=BF, device=DEV)
+    w = torch.ones(16, 8, dtype=BF, device=DEV)
+    assert torch.isposinf(dense.linear(x, w, activation=act)).all()
