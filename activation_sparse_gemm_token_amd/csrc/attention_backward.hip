@@ -150,7 +150,7 @@ attn_dkv_kernel(AttnBackArgs a) {
     if (copy_at >= qs.len) copy_at = from, ++copy_head;
   };
   int64_t q0 = copy_at;
-  if (lo < steps) copy((int)(lo & 1));
+  if (lo < steps) copy(0);
 
   {
     TileCopy<NB, kKvKeys, kKvWaves> cv;
@@ -174,11 +174,11 @@ attn_dkv_kernel(AttnBackArgs a) {
   const bool dead = key >= ks.len;                      // this lane's key does not exist
   const bool any_dead = k0 + 32 > ks.len;
   const char* const vt = lds + wave * 32 * T::kPitch;
-  for (int64_t j = lo; j < steps; ++j) {
+  auto step = [&](int64_t j, auto stage) __attribute__((always_inline)) {   // its stage a constant, as in the forward pass
     wait_copies<0>();
     group_barrier();
-    if (j + 1 < steps) copy((int)((j + 1) & 1));
-    const char* const qt = lds + kVBytes + (j & 1) * kStage;
+    if (j + 1 < steps) copy(1 - stage);
+    const char* const qt = lds + kVBytes + decltype(stage)::value * kStage;
     const char* const dt = qt + kTile;
     const float* const st = reinterpret_cast<const float*>(dt + kTile);
     if (k0 < ks.len && !(f.causal && k0 - shift >= q0 + kQueries)) {
@@ -218,6 +218,10 @@ attn_dkv_kernel(AttnBackArgs a) {
     }
     q0 += kQueries;
     if (q0 >= qs.len) q0 = from;
+  };
+  for (int64_t j = lo; j < steps; j += 2) {
+    step(j, std::integral_constant<int, 0>{});
+    if (j + 1 < steps) step(j + 1, std::integral_constant<int, 1>{});
   }
   if (lo >= steps) wait_copies<0>();                    // V's copy must not outlive the workgroup
   // A batch's rows behind the filled ones get zeros (their sums are).
@@ -360,13 +364,13 @@ attn_dq_kernel(AttnBackArgs a) {
     delta = half_sum(sum);
     if (live && lane < 32) a.stats[w.lse_off + row] = (f32x2){lse2, delta};
   }
-  for (int j = 0; j < steps; ++j) {
+  auto step = [&](int j, auto stage) __attribute__((always_inline)) {
     wait_copies<0>();
     group_barrier();
     if (j + 1 < steps && !few) copy(j + 1);
     const int64_t k0 = (int64_t)j * kKeys;
-    if (k0 >= mine) continue;
-    const char* const kt = lds + (j & 1) * 2 * kTile;
+    if (k0 >= mine) return;
+    const char* const kt = lds + decltype(stage)::value * 2 * kTile;
     const char* const vt = kt + kTile;
     const bool cut = k0 + kKeys > all;
     const int left = (int)(limit < k0 ? 0 : limit - k0 < kKeys ? limit - k0 : kKeys);
@@ -393,6 +397,10 @@ attn_dq_kernel(AttnBackArgs a) {
         for (int nb = 0; nb < NB; ++nb) dq[nb] = mfma32<kBf16>(column_read(base, col_off[nb][0], col_off[nb][1]), dw, dq[nb]);
       }
     }
+  };
+  for (int j = 0; j < steps; j += 2) {
+    step(j, std::integral_constant<int, 0>{});
+    if (j + 1 < steps) step(j + 1, std::integral_constant<int, 1>{});
   }
   const int64_t dq_off = b * a.dq.b + w.q.start * a.dq.t + w.head * a.dq.h;
   store_rows<kBf16, NB>(a.dq.p + dq_off + q0 * a.dq.t, a.dq.t, w.q.len - q0, f.d, dq, f.scale);

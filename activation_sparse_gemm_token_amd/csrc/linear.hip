@@ -254,7 +254,7 @@ struct Operand {
 };
 
 template <int TYPE, int T, int STAGES, bool A_ALONG, bool B_ALONG>
-__global__ void __launch_bounds__(2 * T, T == 256 ? 1 : 2)
+__global__ void __launch_bounds__(2 * T, T == 256 || STAGES > 2 ? 1 : 2)
 linear_gemm_kernel(LinearGemm g) {
   using A = Operand<T, A_ALONG>;
   using B = Operand<T, B_ALONG>;
