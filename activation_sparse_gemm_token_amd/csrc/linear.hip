@@ -123,10 +123,10 @@ __device__ __forceinline__ int64_t gate_load(const LinearEpi& e, int64_t m, int6
   return (row + 1) * e.gate_tokens;
 }
 
+// gate act(v + bias) of channels n.. of row m, whose element is `at`.
 template <int TYPE, int W>
-__device__ __forceinline__ void epilogue(const LinearEpi& e, int64_t m, int64_t n, int64_t N, bool wide, const float (&bias)[W],
+__device__ __forceinline__ void activate(const LinearEpi& e, int64_t at, int64_t n, int64_t N, bool wide, const float (&bias)[W],
                                          const float (&gate)[W], float (&v)[W]) {
-  const int64_t at = m * N + n;
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
   if (e.z != nullptr) {
@@ -156,6 +156,13 @@ __device__ __forceinline__ void epilogue(const LinearEpi& e, int64_t m, int64_t 
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] *= gate[i];
   }
+}
+
+template <int TYPE, int W>
+__device__ __forceinline__ void epilogue(const LinearEpi& e, int64_t m, int64_t n, int64_t N, bool wide, const float (&bias)[W],
+                                         const float (&gate)[W], float (&v)[W]) {
+  const int64_t at = m * N + n;
+  activate<TYPE, W>(e, at, n, N, wide, bias, gate, v);
   if (wide) {
     if (e.residual != nullptr) {
       Raw<TYPE, W> r;
@@ -348,19 +355,52 @@ linear_gemm_kernel(LinearGemm g) {
   // channels of a row (16 bytes of y) and the epilogue is one short loop.
   char* const mine = lds + wave * 64 * kRowBytes;
   const int64_t n = n0 + 64 * wn + 8 * (lane & 7);
-  const bool wide = g.N % 8 == 0;
+  const bool wide = g.N % 8 == 0, whole = wide && g.splits == 1 && g.e.residual != nullptr;
+  const bool changed = g.e.bias != nullptr || g.e.gate != nullptr || g.e.z != nullptr || g.e.act != 0;
   float bias[8], gate[8];
   bias_load<TYPE, 8>(g.e, n, g.N, bias);
   int64_t gate_end = 0;
 #pragma unroll
   for (int pass = 0; pass < kRB / 4; ++pass) {
+    // The residual of the lane's 8 rows is asked for at once: one at a time, each would wait for memory.
+    const int64_t m = m0 + 16 * kRB * wm + 64 * pass + (lane >> 3);
+    Raw<TYPE, 8> residual[8];
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      residual[it].zero();
+      if (whole && m + 8 * it < g.M && n < g.N) residual[it].load(g.e.residual + (m + 8 * it) * g.N + n);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < kCB; ++j)
         *reinterpret_cast<f32x4*>(mine + (16 * i + (lane & 15)) * kRowBytes + (16 * j + 4 * (lane >> 4)) * 4) = acc[4 * pass + i][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int64_t m = m0 + 16 * kRB * wm + 64 * pass + (lane >> 3);
+    if (whole) {
+      if (changed) {
+#pragma unroll 1
+        for (int it = 0; it < 8; ++it) {
+          f32x4* const p = reinterpret_cast<f32x4*>(mine + (8 * it + (lane >> 3)) * kRowBytes + 32 * (lane & 7));
+          const f32x4 v0 = p[0], v1 = p[1];
+          float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+          const int64_t r = m + 8 * it;
+          if (r >= g.M || n >= g.N) continue;
+          if (r >= gate_end) gate_end = gate_load<TYPE, 8>(g.e, r, n, g.N, gate);
+          activate<TYPE, 8>(g.e, r * g.N + n, n, g.N, true, bias, gate, v);
+          p[0] = (f32x4){v[0], v[1], v[2], v[3]};
+          p[1] = (f32x4){v[4], v[5], v[6], v[7]};
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const f32x4* const p = reinterpret_cast<const f32x4*>(mine + (8 * it + (lane >> 3)) * kRowBytes + 32 * (lane & 7));
+        const f32x4 v0 = p[0], v1 = p[1];
+        float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += residual[it].get(e);
+        if (m + 8 * it < g.M && n < g.N) store_vec<TYPE, 8>(g.e.y + (m + 8 * it) * g.N + n, v);
+      }
+    } else
 #pragma unroll 1
     for (int it = 0; it < 8; ++it) {
       const char* const p = mine + (8 * it + (lane >> 3)) * kRowBytes + 32 * (lane & 7);
