@@ -341,11 +341,15 @@ linear_gemm_kernel(LinearGemm g) {
       else wait_vm<0>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       barrier_no_fence();
-      if (s + STAGES < steps) copy(s + STAGES, stage);
+      // A wavefront waits while its copies go out.  Of the two on a SIMD of the large tile one copies before its
+      // products, the other after, so that the matrix core has the other's meanwhile.
+      const bool more = s + STAGES < steps;
+      if (more && (T == 128 || wave < kWaves / 2)) copy(s + STAGES, stage);
       __builtin_amdgcn_sched_barrier(0);
       read(next, First{});                              // after the last step: not used
       multiply(Second{});
       __builtin_amdgcn_sched_barrier(0);
+      if (T == 256 && more && wave >= kWaves / 2) copy(s + STAGES, stage);
       stage = next;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
