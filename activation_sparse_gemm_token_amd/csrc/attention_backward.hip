@@ -1,11 +1,11 @@
 // Attention, backward (include/rtlynx_attention.h).
 //
-//   1. attn_delta_kernel   D = sum of d_o o per query and head, beside the log-sum-exp in
-//                          log2 units (+inf where no key is seen: p is 0 then).
-//   2. attn_dq_kernel      dQ: as the forward pass, 32 queries a wavefront.
-//   3. attn_dkv_kernel     dK, dV: a wavefront holds 32 keys, its workgroup walks the
+//   1. attn_dq_kernel      dQ: as the forward pass, 32 queries a wavefront.  It leaves D = sum of d_o o per
+//                          query and head, beside the log-sum-exp in log2 units (+inf where no key is
+//                          seen: p is 0 then).
+//   2. attn_dkv_kernel     dK, dV: a wavefront holds 32 keys, its workgroup walks the
 //                          queries of all heads that share the key head.
-//   4. attn_dkv_join_kernel  where few key heads leave few workgroups, 3 splits the queries.
+//   3. attn_dkv_join_kernel  where few key heads leave few workgroups, 2 splits the queries.
 //
 // S and dP are formed in both (7 products where 5 would do with atomic sums), so
 // nothing is added atomically and shared heads sum in registers.  Everything
@@ -21,34 +21,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
-
-// 16 lanes a row, 8 channels each.  Rows of a packed batch that lie in no sequence are
-// worked on too; nothing reads their values.
-__global__ void __launch_bounds__(256)
-attn_delta_kernel(AttnBackArgs a) {
-  const int lane = threadIdx.x & 15;
-  const bool packed = a.f.q_starts != nullptr;
-  const int64_t total = a.f.tq * a.f.hq * (packed ? 1 : a.f.sequences);
-  const int64_t at = folded_block() * 16 + threadIdx.x / 16;
-  if (at >= total) return;
-  const int64_t item = at / a.f.tq, row = at - item * a.f.tq, seq = packed ? 0 : item / a.f.hq, head = item - seq * a.f.hq;
-  float s = 0.f;
-  if (8 * lane < a.f.d) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(a.d_o.p + seq * a.d_o.b + row * a.d_o.t + head * a.d_o.h + 8 * lane);
-    const u32x4 y = *reinterpret_cast<const u32x4*>(a.f.o.p + seq * a.f.o.b + row * a.f.o.t + head * a.f.o.h + 8 * lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s += bf16_lo_to_f32(x[i]) * bf16_lo_to_f32(y[i]);
-      s += bf16_hi_to_f32(x[i]) * bf16_hi_to_f32(y[i]);
-    }
-  }
-#pragma unroll
-  for (int d = 8; d >= 1; d /= 2) s += __shfl_xor(s, d, 16);
-  if (lane == 0) {
-    const float l = a.f.lse[at];
-    a.stats[at] = (f32x2){l == -__builtin_inff() ? __builtin_inff() : l * kLog2e, s};
-  }
-}
 
 // --- dK, dV -------------------------------------------------------------------
 // K of a wavefront's 32 keys stays in registers, V in LDS (both in registers, with dK and dV, take more than
@@ -321,9 +293,22 @@ attn_dq_kernel(AttnBackArgs a) {
   load_rows<NB>(f.q.p + w.q_off + q0 * f.q.t, f.q.t, w.q.len - q0, f.d, qf);
   const int64_t d_off = b * a.d_o.b + w.q.start * a.d_o.t + w.head * a.d_o.h;
   load_rows<NB>(a.d_o.p + d_off + q0 * a.d_o.t, a.d_o.t, w.q.len - q0, f.d, df);
-  const bool live = row < w.q.len;
-  const f32x2 stats = live ? a.stats[w.lse_off + row] : (f32x2){__builtin_inff(), 0.f};
-  float lse2 = stats[0], delta = stats[1];
+  const bool live = row < w.q.len, few = steps <= 2;
+  float lse2 = live ? f.lse[w.lse_off + row] : -__builtin_inff();
+  lse2 = lse2 == -__builtin_inff() ? __builtin_inff() : lse2 * kLog2e;
+  float delta = 0.f;
+  if (!few) {                                           // D, 8 channels of d_o o at a time, then both halves of the wavefront
+    u32x4 of[2 * NB];
+    load_rows<NB>(f.o.p + w.o_off + q0 * f.o.t, f.o.t, w.q.len - q0, f.d, of);
+#pragma unroll
+    for (int c = 0; c < 2 * NB; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        delta += bf16_lo_to_f32(df[c][i]) * bf16_lo_to_f32(of[c][i]);
+        delta += bf16_hi_to_f32(df[c][i]) * bf16_hi_to_f32(of[c][i]);
+      }
+    delta = half_sum(delta);
+  }
   settle(qf);
   settle(df);
   asm volatile("" : "+v"(lse2), "+v"(delta));
@@ -340,8 +325,7 @@ attn_dq_kernel(AttnBackArgs a) {
   }
   // Few keys: o is near the values, ds a difference of near numbers, and o's rounding in D would show (with two
   // keys dQ and dK were 0.4 % off instead of 0.24 %).  D is the sum of p dP too: formed so where the keys fit
-  // the two tiles of LDS, and left for the dK / dV kernel, which runs after this one.
-  const bool few = steps <= 2;
+  // the two tiles of LDS.
   if (few && steps > 0) {
     if (steps == 2) copy(1);
     wait_copies<0>();
@@ -362,8 +346,8 @@ attn_dq_kernel(AttnBackArgs a) {
       }
     }
     delta = half_sum(sum);
-    if (live && lane < 32) a.stats[w.lse_off + row] = (f32x2){lse2, delta};
   }
+  if (live && lane < 32) a.stats[w.lse_off + row] = (f32x2){lse2, delta};       // for the dK / dV kernel
   auto step = [&](int j, auto stage) __attribute__((always_inline)) {
     wait_copies<0>();
     group_barrier();
@@ -441,11 +425,6 @@ int attn_back_splits(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int6
 }
 
 hipError_t launch_attention_backward(AttnBackArgs a, hipStream_t stream) {
-  const int64_t rows = a.f.tq * a.f.hq * (a.f.q_starts != nullptr ? 1 : a.f.sequences);
-  if (rows > 0) {
-    const hipError_t e = launch(&attn_delta_kernel, folded_grid((rows + 15) / 16), dim3(256), stream, a);
-    if (e != hipSuccess) return e;
-  }
   if (a.f.d <= 32) return run_backward<1>(a, stream);
   if (a.f.d <= 64) return run_backward<2>(a, stream);
   if (a.f.d <= 96) return run_backward<3>(a, stream);
