@@ -1,8 +1,8 @@
 // The dense linear layer with bias, activation, gate and residual in its
 // epilogue, and its gradients (include/rtlynx_dense.h).
 //
-// linear_gemm_kernel.  256 x 256 tiles (8 wavefronts of 128 x 64) or 128 x 128
-// (4 of 64 x 64) on v_mfma_f32_16x16x32, operands through rings of LDS tiles 64
+// linear_gemm_kernel.  256 x 256 tiles (8 wavefronts of 128 x 64), 256 x 128 (8 of
+// 64 x 64) or 128 x 128 (4 of 64 x 64) on v_mfma_f32_16x16x32, operands through rings of LDS tiles 64
 // channels deep, filled by direct copies.  An operand whose contraction runs along
 // memory rows (x and w, forward) is read with 16-byte reads; one whose contraction
 // runs across them (w in dx = dz w; dz and x in dw = dz^T x) lies in LDS as it does
@@ -187,10 +187,11 @@ __device__ __forceinline__ void epilogue(const LinearEpi& e, int64_t m, int64_t 
 // of row r in slot c ^ (r & 7).  Across: LDS rows are the 64 contraction rows, 2 T bytes each, chunk c of
 // row r in slot c ^ swizzle(r): the 4 rows x 2 chunks of a lane group's transposing read, and two groups
 // of them, fall on different banks.
-template <int T, bool ALONG>
+template <int T, int WAVES, bool ALONG>
 struct Operand {
   static constexpr int kBytes = T * 128, kPitch = ALONG ? 128 : 2 * T;
-  static constexpr int kWaves = T / 32;                 // of the workgroup; 4 copy instructions each
+  static constexpr int kCount = T / (8 * WAVES);        // copy instructions of each wavefront
+  static_assert(kCount == 4 || kCount == 2, "copies of a step");
   // The lane's offset in instruction i: first[set(i)] + i / .. * row_bytes; the swizzle makes two sets across.
   uint32_t first[ALONG ? 1 : 2];
   uint32_t row_bytes, step_bytes;                       // uniform
@@ -200,14 +201,15 @@ struct Operand {
     return ALONG ? row & 7 : (row & 3) << 1 | ((row >> 3) & 1) << 3;
   }
   static constexpr int set(int i) { return ALONG ? 0 : T == 256 ? i & 1 : i >> 1; }
+  static constexpr bool starts_set(int i) { return i == 0 || (!ALONG && i == (T == 256 ? 1 : 2)); }
   // Rows from r0 on of a tensor with rows of ld elements.
   __device__ __forceinline__ void init(int wave, int64_t r0, int64_t ld) {
     const uint32_t lane = threadIdx.x & 63, slots = kPitch / 16, rows = 1024 / kPitch;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t row = (4 * wave + i) * rows + lane / slots, c = (lane % slots) ^ swizzle(row);
+    for (int i = 0; i < kCount; ++i) {
+      const uint32_t row = (kCount * wave + i) * rows + lane / slots, c = (lane % slots) ^ swizzle(row);
       const uint32_t at = ALONG ? (uint32_t)((r0 + row) * ld * 2 + 16 * c) : (uint32_t)(row * ld * 2 + r0 * 2 + 16 * c);
-      if (i == 0 || (!ALONG && i == (T == 256 ? 1 : 2))) first[set(i)] = at - i * (uint32_t)(rows * ld * 2);
+      if (starts_set(i)) first[set(i)] = at - i * (uint32_t)(rows * ld * 2);
       if (i == 0) chunk = ALONG ? 8 * (int)c : 0;
     }
     row_bytes = __builtin_amdgcn_readfirstlane((uint32_t)(rows * ld * 2));
@@ -217,22 +219,32 @@ struct Operand {
   __device__ __forceinline__ void copy(__amdgpu_buffer_rsrc_t rs, int64_t s, int64_t K, uint32_t lds, int wave) const {
     const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)s * step_bytes);
     const bool inside = !ALONG || s * 64 + chunk < K;
-    uint32_t v[4];
+    uint32_t v[kCount];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = inside ? first[set(i)] + i * row_bytes : kOobOffset - so;
-    const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds + 4096u * wave);
+    for (int i = 0; i < kCount; ++i) v[i] = inside ? first[set(i)] + i * row_bytes : kOobOffset - so;
+    const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds + 1024u * kCount * wave);
     uint32_t saved;
-    asm volatile(
-        "s_nop 4\n\ts_mov_b32 %[sv], m0\n\t"
-        "s_mov_b32 m0, %[l0]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v0], %[rs], %[so] offen lds\n\t"
-        "s_mov_b32 m0, %[l1]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v1], %[rs], %[so] offen lds\n\t"
-        "s_mov_b32 m0, %[l2]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v2], %[rs], %[so] offen lds\n\t"
-        "s_mov_b32 m0, %[l3]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v3], %[rs], %[so] offen lds\n\t"
-        "s_mov_b32 m0, %[sv]"
-        : [sv] "=&s"(saved)
-        : [v0] "v"(v[0]), [v1] "v"(v[1]), [v2] "v"(v[2]), [v3] "v"(v[3]), [rs] "s"(rs), [so] "s"(so), [l0] "s"(l0),
-          [l1] "s"(l0 + 0x400u), [l2] "s"(l0 + 0x800u), [l3] "s"(l0 + 0xc00u)
-        : "memory");
+    if constexpr (kCount == 4)
+      asm volatile(
+          "s_nop 4\n\ts_mov_b32 %[sv], m0\n\t"
+          "s_mov_b32 m0, %[l0]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v0], %[rs], %[so] offen lds\n\t"
+          "s_mov_b32 m0, %[l1]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v1], %[rs], %[so] offen lds\n\t"
+          "s_mov_b32 m0, %[l2]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v2], %[rs], %[so] offen lds\n\t"
+          "s_mov_b32 m0, %[l3]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v3], %[rs], %[so] offen lds\n\t"
+          "s_mov_b32 m0, %[sv]"
+          : [sv] "=&s"(saved)
+          : [v0] "v"(v[0]), [v1] "v"(v[1]), [v2] "v"(v[2]), [v3] "v"(v[3]), [rs] "s"(rs), [so] "s"(so), [l0] "s"(l0),
+            [l1] "s"(l0 + 0x400u), [l2] "s"(l0 + 0x800u), [l3] "s"(l0 + 0xc00u)
+          : "memory");
+    else
+      asm volatile(
+          "s_nop 4\n\ts_mov_b32 %[sv], m0\n\t"
+          "s_mov_b32 m0, %[l0]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v0], %[rs], %[so] offen lds\n\t"
+          "s_mov_b32 m0, %[l1]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v1], %[rs], %[so] offen lds\n\t"
+          "s_mov_b32 m0, %[sv]"
+          : [sv] "=&s"(saved)
+          : [v0] "v"(v[0]), [v1] "v"(v[1]), [rs] "s"(rs), [so] "s"(so), [l0] "s"(l0), [l1] "s"(l0 + 0x400u)
+          : "memory");
     (void)saved;
   }
   // The lane's byte in the blocks of 16 rows from block `first` on (uniform).
@@ -260,24 +272,25 @@ struct Operand {
   }
 };
 
-template <int TYPE, int T, int STAGES, bool A_ALONG, bool B_ALONG>
-__global__ void __launch_bounds__(2 * T, T == 256 || STAGES > 2 ? 1 : 2)
+template <int TYPE, int TM, int TN, int STAGES, bool A_ALONG, bool B_ALONG>
+__global__ void __launch_bounds__(2 * TM, TM == 256 || STAGES > 2 ? 1 : 2)
 linear_gemm_kernel(LinearGemm g) {
-  using A = Operand<T, A_ALONG>;
-  using B = Operand<T, B_ALONG>;
-  constexpr int kWaves = T / 32, kWavesN = T / 64, kRB = T == 256 ? 8 : 4, kCB = 4;
-  constexpr int kTile = A::kBytes, kRowBytes = 64 * 4 + 16, kStaging = kWaves * 64 * kRowBytes;
-  static_assert(kWaves == (T / (16 * kRB)) * kWavesN, "wavefronts cover the tile");
-  __shared__ __attribute__((aligned(16))) char lds[kStaging > 2 * STAGES * kTile ? kStaging : 2 * STAGES * kTile];   // A, B of the steps; epilogue
+  constexpr int kWaves = TM / 32, kWavesN = TN / 64, kRB = TM * kWavesN / kWaves / 16, kCB = 4;
+  using A = Operand<TM, kWaves, A_ALONG>;
+  using B = Operand<TN, kWaves, B_ALONG>;
+  constexpr int kStage = A::kBytes + B::kBytes, kCopies = A::kCount + B::kCount;
+  constexpr int kRowBytes = 64 * 4 + 16, kStaging = kWaves * 64 * kRowBytes;
+  static_assert(kRB == 4 || kRB == 8, "wavefronts cover the tile");
+  __shared__ __attribute__((aligned(16))) char lds[kStaging > STAGES * kStage ? kStaging : STAGES * kStage];   // A, B of the steps; epilogue
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const int64_t tiles_m = (g.M + T - 1) / T, tiles_n = (g.N + T - 1) / T, tiles = tiles_m * tiles_n;
+  const int64_t tiles_m = (g.M + TM - 1) / TM, tiles_n = (g.N + TN - 1) / TN, tiles = tiles_m * tiles_n;
   const int64_t split = blockIdx.x / tiles;
   int64_t tm, tn;
   tile_coords_of(blockIdx.x - split * tiles, tiles_m, tiles_n, tm, tn);
   const int64_t all = (g.K + 63) / 64, per = (all + g.splits - 1) / g.splits, lo = split * per;
   const int64_t steps = all - lo < per ? all - lo : per;               // may be <= 0: nothing of K left
-  const int64_t m0 = tm * T, n0 = tn * T;
+  const int64_t m0 = tm * TM, n0 = tn * TN;
 
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(g.a, g.a_bytes), br = make_rsrc(g.b, g.b_bytes);
   A oa;
@@ -295,22 +308,22 @@ linear_gemm_kernel(LinearGemm g) {
   // products: the other half is read from LDS during the first half's products, and the next step's first
   // half during the second's.  The barrier between them comes after the last read of a stage, so the copy of
   // step s + STAGES goes out there: with two stages a whole step before it is waited for, which is enough where other
-  // wavefronts fill the wait; a 128 x 128 tile alone on its CU has four.  (One stage more for B, the whole step's
+  // wavefronts fill the wait; a 256 x 128 tile has three, which is what LDS holds, a 128 x 128 tile alone on its CU four.  (One stage more for B, the whole step's
   // fragments read at its top: 429 us for the 4096 x 2048 x 8192 training step, 420 this way; the loop unrolled
   // over the stages is 2 % faster at 4096 x 4096 x 12288 forward but spills where operands run across.)
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)(lds);
   auto copy = [&](int64_t s, int stage) {
-    oa.copy(ar, lo + s, g.K, lds0 + stage * 2 * kTile, wave);
-    ob.copy(br, lo + s, g.K, lds0 + stage * 2 * kTile + kTile, wave);
+    oa.copy(ar, lo + s, g.K, lds0 + stage * kStage, wave);
+    ob.copy(br, lo + s, g.K, lds0 + stage * kStage + A::kBytes, wave);
   };
   u32x4 fa[2][kRB], fb[2][kCB];
   using First = std::integral_constant<int, 0>;
   using Second = std::integral_constant<int, 1>;
   auto read = [&](int stage, auto half) {
     constexpr int h = decltype(half)::value;
-    const char* const ta = lds + stage * 2 * kTile;
+    const char* const ta = lds + stage * kStage;
 #pragma unroll
-    for (int j = 0; j < kCB; ++j) fb[h][j] = B::read(ta + kTile, at_b, j, h);
+    for (int j = 0; j < kCB; ++j) fb[h][j] = B::read(ta + A::kBytes, at_b, j, h);
 #pragma unroll
     for (int i = 0; i < kRB; ++i) fa[h][i] = A::read(ta, at_a, i, h);
   };
@@ -325,7 +338,7 @@ linear_gemm_kernel(LinearGemm g) {
 #pragma unroll
     for (int i = 0; i < STAGES; ++i)
       if (i < steps) copy(i, i);
-    if (steps >= STAGES) wait_vm<8 * (STAGES - 1)>();
+    if (steps >= STAGES) wait_vm<kCopies * (STAGES - 1)>();
     else wait_vm<0>();
     barrier_no_fence();
     read(0, First{});
@@ -337,19 +350,20 @@ linear_gemm_kernel(LinearGemm g) {
       multiply(First{});
       __builtin_amdgcn_sched_barrier(0);
       // This wavefront's reads of the stage are back, and its copies of the next one.
-      if (s + STAGES - 1 < steps) wait_vm<8 * (STAGES - 2)>();
+      if (s + STAGES - 1 < steps) wait_vm<kCopies * (STAGES - 2)>();
       else wait_vm<0>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       barrier_no_fence();
-      // A wavefront waits while its copies go out.  Of the two on a SIMD of the large tile one copies before its
-      // products, the other after, so that the matrix core has the other's meanwhile.
+      // A wavefront waits while its copies go out.  Of the two on a SIMD (8 wavefronts) one copies before its
+      // products, the other after, so that the matrix core has the other's meanwhile (4096 x 4096 x 12288 with
+      // GELU: 345 us with both before, 329).
       const bool more = s + STAGES < steps;
-      if (more && (T == 128 || wave < kWaves / 2)) copy(s + STAGES, stage);
+      if (more && (kWaves == 4 || wave < 4)) copy(s + STAGES, stage);
       __builtin_amdgcn_sched_barrier(0);
       read(next, First{});                              // after the last step: not used
       multiply(Second{});
       __builtin_amdgcn_sched_barrier(0);
-      if (T == 256 && more && wave >= kWaves / 2) copy(s + STAGES, stage);
+      if (kWaves == 8 && more && wave >= 4) copy(s + STAGES, stage);
       stage = next;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -603,19 +617,20 @@ linear_sums_kernel(const float* __restrict__ partials, int64_t parts, int64_t C,
 
 template <int TYPE, bool A_ALONG, bool B_ALONG>
 hipError_t run_gemm(const LinearGemm& g, hipStream_t stream) {
-  const int64_t T = g.tile, tiles = ((g.M + T - 1) / T) * ((g.N + T - 1) / T);
+  const int64_t tiles = ((g.M + g.tile_m - 1) / g.tile_m) * ((g.N + g.tile_n - 1) / g.tile_n);
   const dim3 grid((unsigned)(tiles * g.splits));
   hipError_t e;
-  if (T == 256) e = launch(&linear_gemm_kernel<TYPE, 256, 2, A_ALONG, B_ALONG>, grid, dim3(512), stream, g);
-  else if (tiles * g.splits > 256) e = launch(&linear_gemm_kernel<TYPE, 128, 2, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
-  else e = launch(&linear_gemm_kernel<TYPE, 128, 4, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
+  if (g.tile_n == 256) e = launch(&linear_gemm_kernel<TYPE, 256, 256, 2, A_ALONG, B_ALONG>, grid, dim3(512), stream, g);
+  else if (g.tile_m == 256) e = launch(&linear_gemm_kernel<TYPE, 256, 128, 3, A_ALONG, B_ALONG>, grid, dim3(512), stream, g);
+  else if (tiles * g.splits > 256) e = launch(&linear_gemm_kernel<TYPE, 128, 128, 2, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
+  else e = launch(&linear_gemm_kernel<TYPE, 128, 128, 4, A_ALONG, B_ALONG>, grid, dim3(256), stream, g);
   if (e != hipSuccess || g.splits == 1) return e;
   return launch(&linear_join_kernel<TYPE>, folded_grid((g.M * ((g.N + 3) / 4) + 255) / 256), dim3(256), stream, g);
 }
 
 template <int TYPE>
 hipError_t run_linear(const LinearGemm& g, hipStream_t stream) {
-  if (g.tile == 0) {
+  if (g.tile_m == 0) {
     const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * kRowWaves);
     return g.M <= 16 ? launch(&linear_rows_kernel<TYPE, 1>, grid, block, stream, g)
                      : launch(&linear_rows_kernel<TYPE, 2>, grid, block, stream, g);
@@ -642,24 +657,30 @@ hipError_t run_dz(const LinearDz& a, hipStream_t stream) {
 }  // namespace
 
 // Tile and ranges of the contraction for a product [M, N] over K: the form with the least expected time, in us, from
-// measured rates.  A step of 64 takes a 256 x 256 tile 1.55 (one workgroup per CU) and 128 x 128 tiles 0.55 alone on
-// their CU, 1.03 where two share it; a tile 9 and 4 more to begin and end.  Ranges of the contraction cost a second
-// launch and their fp32 parts, written and read at 4 TB/s.  (2310 x 1160 x 1152: 14 expected for one range, 30 for three,
-// measured 33 with three; 4096 x 2048 x 8192: 136 with 128 x 128, 206 with 256 x 256; 8192 x 2048 x 4096: 136 and 107.)
+// measured rates.  A step of 64 takes a 256 x 256 tile 1.48, a 256 x 128 tile 0.85 (one workgroup per CU each) and 128 x
+// 128 tiles 0.55 alone on their CU, 0.95 where two share it; a tile takes 9, 7 and 4 more to begin and end.  Ranges of the
+// contraction cost a second launch and their fp32 parts, written and read at 4 TB/s.  Measured with the three tiles, bf16:
+// 8192 x 2048 x 4096: 107, 122 and 129; 4096 x 2048 x 8192: 163, 116 and 126; 2048 x 2048 x 2048: 48, 31 and 28; 2310 x
+// 1160 x 1152: 18 with the smallest, 33 with it and three ranges.
 LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel) {
-  if (rows_kernel && M <= 32) return {0, 1};
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
-  const int64_t steps = (K + 63) / 64;
-  if (small == 0 || steps == 0) return {128, 1};
-  LinearForm best{256, 1};
-  double least = (double)((big + 255) / 256) * (1.55 * (double)steps + 9.0);
+  if (rows_kernel && M <= 32) return {0, 0, 1};
+  const int64_t m256 = (M + 255) / 256, m128 = (M + 127) / 128, n256 = (N + 255) / 256, n128 = (N + 127) / 128;
+  const int64_t small = m128 * n128, steps = (K + 63) / 64;
+  if (small == 0 || steps == 0) return {128, 128, 1};
+  LinearForm best{256, 256, 1};
+  double least = (double)((m256 * n256 + 255) / 256) * (1.48 * (double)steps + 9.0);
+  const double mixed = (double)((m256 * n128 + 255) / 256) * (0.85 * (double)steps + 7.0);
+  if (mixed < least) {
+    least = mixed;
+    best = {256, 128, 1};
+  }
   for (int64_t splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); splits *= 2) {
     const int64_t groups = small * splits, each = (steps + splits - 1) / splits;
-    double t = groups <= 256 ? 0.55 * (double)each + 4.0 : (double)((groups + 511) / 512) * (1.03 * (double)each + 4.0);
+    double t = groups <= 256 ? 0.55 * (double)each + 4.0 : (double)((groups + 511) / 512) * (0.95 * (double)each + 4.0);
     if (splits > 1) t += 4.0 + (double)splits * (double)M * (double)N * 8.0 / 4e6;
     if (t < least) {
       least = t;
-      best = {128, (int)splits};
+      best = {128, 128, (int)splits};
     }
   }
   return best;

@@ -77,7 +77,8 @@ RTL_API rtl_status rtl_linear(const void* x, const void* w, const void* bias, co
   g.M = M;
   g.N = N;
   g.K = K;
-  g.tile = form.tile;
+  g.tile_m = form.tile_m;
+  g.tile_n = form.tile_n;
   g.splits = form.splits;
   g.part = static_cast<float*>(workspace);
   g.e.bias = static_cast<const uint16_t*>(bias);
@@ -162,7 +163,8 @@ RTL_API rtl_status rtl_linear_backward(const void* dy, const void* x, const void
     g.M = M;
     g.N = K;
     g.K = b.np;
-    g.tile = f.tile;
+    g.tile_m = f.tile_m;
+    g.tile_n = f.tile_n;
     g.splits = f.splits;
     g.e.y = static_cast<uint16_t*>(dx);
     e = rtl::launch_linear_dx(g, fp16, stream);
@@ -179,7 +181,8 @@ RTL_API rtl_status rtl_linear_backward(const void* dy, const void* x, const void
     g.M = N;
     g.N = K;
     g.K = M;
-    g.tile = f.tile;
+    g.tile_m = f.tile_m;
+    g.tile_n = f.tile_n;
     g.splits = f.splits;
     g.e.y = static_cast<uint16_t*>(dw);
     e = rtl::launch_linear_dw(g, fp16, stream);

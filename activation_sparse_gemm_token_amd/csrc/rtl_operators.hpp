@@ -185,7 +185,7 @@ struct LinearGemm {                      // [M, N] over K
   int64_t lda, ldb;                      // elements
   int64_t a_bytes, b_bytes;              // of the whole tensors, < 2^31
   int64_t M, N, K;
-  int tile, splits;                      // tile 0: the kernel for few rows
+  int tile_m, tile_n, splits;            // tile_m 0: the kernel for few rows
   float* part;                           // [splits][M][N]
   LinearEpi e;
 };
@@ -202,7 +202,7 @@ struct LinearDz {
   int act;
 };
 struct LinearForm {
-  int tile, splits;
+  int tile_m, tile_n, splits;
 };
 LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel);
 int64_t linear_dz_parts(int64_t M, int64_t N, int64_t groups);

@@ -255,3 +255,9 @@ def test_a_sum_past_fp32(act):
     x = torch.full((40, 8), 3e38, dtype=BF, device=DEV)
     w = torch.ones(16, 8, dtype=BF, device=DEV)
     assert torch.isposinf(dense.linear(x, w, activation=act)).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 3000, 3000), (3000, 2701, 2568), (3000, 1001, 5000)])
+def test_tiles(m, n, k):
+    """Forward, dx and dw in tiles of 256 x 128 and of 256 x 256 each."""
+    run((m,), n, k, act="gelu_tanh", gate="shared", residual=True, back=True)
