@@ -2,8 +2,8 @@
 // the softmax's running maximum and sum.
 //
 // attn_forward_kernel.  A wavefront holds 32 queries: their operands, O^T in
-// fp32 and, per lane, one query's maximum and sum; its workgroup shares tiles of
-// 64 keys and values in LDS, copied one tile ahead.  Scores are compared with
+// fp32 and, per lane, one query's maximum and sum; its workgroup of 128 queries
+// shares tiles of keys and values in LDS, copied one tile ahead.  Scores are compared with
 // the maximum the accumulators are scaled by; that maximum moves (and O^T is
 // rescaled) only when some score passes it by more than 2^8, which changes no
 // result (any reference would do) and leaves the rescaling out of most steps.
@@ -57,9 +57,14 @@ __device__ __forceinline__ float max16(const f32x16& s) {
   return m;
 }
 
-// Queries and keys of a tile, wavefronts per SIMD.  Two wavefronts with tiles of 64 keys and 236
-// registers leave the matrix cores idle through each other's waits; three fit with 32 keys and 168
-// registers (head_dim 128, 2 x 4608 tokens, 24 heads: 1350 TFLOP/s while all CUs are busy, against 1210).
+// Queries and keys of a tile, wavefronts per SIMD.  One wavefront's softmax hides behind the others' products, so what
+// counts is how many share a SIMD: three with 32 keys and 168 registers, four with 64 keys up to head_dim 64.
+//
+// 2 x 4608 tokens, 24 heads of 128: 500 us with the join of the last tiles, 1040 TFLOP/s, the matrix cores 60 % busy at
+// the 1.8 GHz that the card's power leaves them then; alone they reach 1490 TFLOP/s.  Measured there and not kept: two wavefronts with
+// tiles of 64 keys 521; 8 wavefronts to a workgroup 533 (of 3 or 4 stages 588, 537); the next step's scores formed
+// during a softmax 550; 64 queries a wavefront, which halves the reads of LDS but takes 512 registers of two kinds,
+// with moves between them, 612; higher wave priority during the products 512.
 constexpr int kForwardWaves = 4, kForwardQueries = 32 * kForwardWaves;
 template <int NB>
 constexpr int forward_keys() { return NB <= 2 ? 64 : 32; }
@@ -158,8 +163,10 @@ attn_forward_kernel(AttnArgs a) {
   auto step = [&](int j, auto stage) __attribute__((always_inline)) {
     wait_copies<0>();
     group_barrier();                                    // tile j is whole, tile j - 1 is no longer read
-    if (j + 1 < steps) copy(1 - stage);
-    if (j >= my_steps) return;
+    if (j >= my_steps) {
+      if (j + 1 < steps) copy(1 - stage);
+      return;
+    }
     const char* const kt = lds + decltype(stage)::value * 2 * kTile;
     const char* const vt = kt + kTile;
     f32x16 s[kKb];
@@ -169,6 +176,7 @@ attn_forward_kernel(AttnArgs a) {
 #pragma unroll
       for (int c = 0; c < 2 * NB; ++c) s[kb] = mfma32<TYPE>(lds_read16(kt + kb * 32 * T::kPitch + row_off[c]), qf[c], s[kb]);
     }
+    if (j + 1 < steps) copy(1 - stage);                 // the matrix core has the scores to work on meanwhile
     if (j >= cut_step) {
       const int seen = clamp_rows(limit - (int64_t)j * kKeys);
 #pragma unroll
@@ -475,11 +483,14 @@ hipError_t by_blocks(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream
 
 }  // namespace
 
-// Up to 32 queries of a sequence go to attn_few_kernel, its keys in ranges of at least 256 until there
-// is one workgroup per CU (one token, 65536 keys in 8 heads: 53 us; two 61, three 71: more parts to join).  Otherwise tiles of 128 queries; a batch's tiles are alike, so where their
-// number is no multiple of what the card holds (256 CUs times the wavefronts per SIMD) the last, partly
-// filled round would leave CUs idle: the keys of its tiles are split over workgroups, 256 keys at least for
-// each.  Causal tiles shrink towards the end by themselves, and packed ones differ anyway.
+// Up to 32 queries of a sequence go to attn_few_kernel, its keys in ranges of at least 256 until there is one workgroup
+// per CU (one token, 65536 keys in 8 heads: 53 us; two 61, three 71: more parts to join).  The kernel for tiles took 490
+// us where this one takes 92 (8 sequences of 16384 keys, 8 key heads).
+//
+// Otherwise tiles of 128 queries; a batch's tiles are alike, so where their number is no multiple of what the card
+// holds (256 CUs times the wavefronts per SIMD) the last, partly filled round would leave CUs idle: the keys of its
+// tiles are split over workgroups, 256 keys at least for each.  Causal tiles shrink towards the end by themselves, and
+// packed ones differ anyway.
 AttnPlan attn_plan(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, int64_t d, bool packed, bool causal) {
   AttnPlan p{false, 1, 0};
   if (packed || sequences == 0 || tq == 0 || hk == 0 || hq == 0) return p;
