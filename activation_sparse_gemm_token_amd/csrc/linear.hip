@@ -130,11 +130,21 @@ __device__ __forceinline__ void activate(const LinearEpi& e, int64_t at, int64_t
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
   if (e.z != nullptr) {
-    if (wide) store_vec<TYPE, W>(e.z + at, v);
-    else
+    uint16_t* const z = static_cast<uint16_t*>(e.z);
+    float* const z32 = static_cast<float*>(e.z);
+    if (wide && e.z_fp32) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) store_vec<kFp32, 4>(z32 + at + i, v + i);
+    } else if (wide) {
+      store_vec<TYPE, W>(z + at, v);
+    } else {
 #pragma unroll
       for (int i = 0; i < W; ++i)
-        if (n + i < N) e.z[at + i] = from_f32<TYPE>(v[i]);
+        if (n + i < N) {
+          if (e.z_fp32) z32[at + i] = v[i];
+          else z[at + i] = from_f32<TYPE>(v[i]);
+        }
+    }
   }
   switch (e.act) {                                      // one kind per launch
     case kActGelu:
@@ -542,7 +552,7 @@ linear_rows_kernel(LinearGemm g) {
 // --- dz, dbias, dgate -------------------------------------------------------------
 // A workgroup takes 32 VEC columns and a part of a gate row's rows, 8 rows at a time; it leaves
 // one row of sums for the part.  dz rows are np elements, a multiple of 8, zeros past N.
-template <int TYPE, int VEC>
+template <int TYPE, int ZTYPE, int VEC>
 __global__ void __launch_bounds__(256)
 linear_dz_kernel(LinearDz a) {
   __shared__ float lds[8][32 * VEC];
@@ -559,12 +569,13 @@ linear_dz_kernel(LinearDz a) {
   if (c < a.np) {
     for (int64_t r = lo + sub; r < hi; r += 8) {
       const int64_t at = (group * rows + r) * a.N + c;
-      Raw<TYPE, VEC> dy, z;
+      Raw<TYPE, VEC> dy;
+      Raw<ZTYPE, VEC> z;
       dy.zero();
       z.zero();
       if (c < a.N) {                                    // VEC divides N, or is 1
         dy.load(a.dy + at);
-        if (a.z != nullptr) z.load(a.z + at);
+        if (a.z != nullptr) z.load(static_cast<const elem_t<ZTYPE>*>(a.z) + at);
       }
       float out[VEC];
 #pragma unroll
@@ -643,7 +654,9 @@ hipError_t run_dz(const LinearDz& a, hipStream_t stream) {
   const bool wide = a.N % 8 == 0;
   const int64_t cols = 32 * (wide ? 8 : 1);
   const dim3 grid((unsigned)((a.np + cols - 1) / cols), (unsigned)(a.groups * a.parts));
-  hipError_t e = launch(wide ? &linear_dz_kernel<TYPE, 8> : &linear_dz_kernel<TYPE, 1>, grid, dim3(256), stream, a);
+  auto* k = a.z_fp32 ? (wide ? &linear_dz_kernel<TYPE, kFp32, 8> : &linear_dz_kernel<TYPE, kFp32, 1>)
+                     : (wide ? &linear_dz_kernel<TYPE, TYPE, 8> : &linear_dz_kernel<TYPE, TYPE, 1>);
+  hipError_t e = launch(k, grid, dim3(256), stream, a);
   const unsigned blocks = (unsigned)((a.N + 63) / 64);
   if (e == hipSuccess && a.dbias != nullptr)
     e = launch(&linear_sums_kernel<TYPE>, dim3(blocks, 1), dim3(1024), stream, (const float*)a.bias_part, a.groups * a.parts,

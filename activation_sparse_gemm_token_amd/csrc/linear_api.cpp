@@ -26,7 +26,7 @@ bool gate_ok(int64_t M, int64_t rows, int64_t stride) {
   return rows >= 1 && rows <= kMaxGateRows && stride >= 0 && stride < kMaxStride && M % rows == 0;
 }
 
-bool flags_ok(uint32_t flags) { return (flags & 0xFu) <= RTL_DENSE_FP16 && (flags & ~0x3Fu) == 0; }
+bool flags_ok(uint32_t flags) { return (flags & 0xFu) <= RTL_DENSE_FP16 && (flags & ~(0x3Fu | RTL_DENSE_Z_FP32)) == 0; }
 
 size_t part_bytes(const rtl::LinearForm& f, int64_t M, int64_t N) {
   return f.splits > 1 ? (size_t)f.splits * (size_t)M * (size_t)N * 4 : 0;
@@ -87,7 +87,8 @@ RTL_API rtl_status rtl_linear(const void* x, const void* w, const void* bias, co
   g.e.gate_stride = gate_rows > 1 ? gate_stride : 0;
   g.e.residual = static_cast<const uint16_t*>(residual);
   g.e.y = static_cast<uint16_t*>(y);
-  g.e.z = static_cast<uint16_t*>(z);
+  g.e.z = z;
+  g.e.z_fp32 = (flags & RTL_DENSE_Z_FP32) != 0;
   g.e.act = (int)((flags >> 4) & 3u);
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const rtl_status d = rtl::check_device(stream);
@@ -131,7 +132,8 @@ RTL_API rtl_status rtl_linear_backward(const void* dy, const void* x, const void
   if ((own || dbias != nullptr || dgate != nullptr) && N > 0) {
     rtl::LinearDz a{};
     a.dy = static_cast<const uint16_t*>(dy);
-    a.z = static_cast<const uint16_t*>(z);
+    a.z = z;
+    a.z_fp32 = (flags & RTL_DENSE_Z_FP32) != 0;
     a.gate = static_cast<const uint16_t*>(gate);
     a.gate_stride = gate_rows > 1 ? gate_stride : 0;
     a.M = M;

@@ -175,7 +175,8 @@ struct LinearEpi {
   const uint16_t* gate;
   const uint16_t* residual;
   uint16_t* y;
-  uint16_t* z;
+  void* z;                               // of the tensors' type, or fp32
+  bool z_fp32;
   int64_t gate_tokens, gate_stride;      // rows of x to a gate row
   int act;
 };
@@ -191,7 +192,8 @@ struct LinearGemm {                      // [M, N] over K
 };
 struct LinearDz {
   const uint16_t* dy;
-  const uint16_t* z;
+  const void* z;                         // of the tensors' type, or fp32
+  bool z_fp32;
   const uint16_t* gate;
   uint16_t* dz;                          // [M][np], NULL: sums only
   float* bias_part;                      // [groups parts][N]

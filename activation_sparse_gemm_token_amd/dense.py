@@ -16,6 +16,8 @@ __all__ = ["linear", "linear_backward", "workspace_bytes", "backward_workspace_b
 
 ACTIVATIONS = {None: 0, "gelu": 0x10, "gelu_tanh": 0x20, "silu": 0x30}
 
+_Z_FP32 = 0x200
+
 _i64, _vp, _size, _u32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32
 _SIGNATURES = {
     "rtl_linear_workspace_bytes": (_size, [_i64] * 3),
@@ -127,7 +129,8 @@ def linear(x, w, bias=None, activation=None, gate=None, residual=None, out=None,
     ``activation`` is None, "gelu", "gelu_tanh" or "silu"; ``bias`` [N]; ``gate`` [N] or, for x
     [batch, tokens, K], [batch, N] (a slice of a modulation row goes as it is); ``residual``
     [..., N].  ``out`` may be the residual itself.  Returns y, or with ``keep`` (y, z), z
-    the rounded x w^T + bias for ``linear_backward``; without an autograd graph."""
+    x w^T + bias for ``linear_backward``, fp32 with a gate (whose gradient would carry its
+    rounding), else of x's type; without an autograd graph."""
     for t in (x, w, bias, gate, residual):
         if t is not None and t.requires_grad:
             _no_graph("dense.linear", "dense.linear_backward forms it", t)
@@ -155,7 +158,11 @@ def linear(x, w, bias=None, activation=None, gate=None, residual=None, out=None,
         _apart(out, x=x, w=w, bias=bias, gate=gate, residual=None if same else residual)
         y = out
     if keep:
-        z = x.new_empty(shape)
+        if gate is None:
+            z = x.new_empty(shape)
+        else:
+            z = x.new_empty(shape, dtype=_torch().float32)
+            flags |= _Z_FP32
         zp = z.data_ptr()
     if m > 32:                                            # the kernel for few rows needs none
         size = workspace_bytes(m, n, k)
@@ -175,7 +182,7 @@ def linear_backward(dy, x, w, z=None, activation=None, gate=None, need_dx: bool 
                     need_dbias: bool = True, need_dgate: bool = True, workspace=None):
     """Gradients of ``linear`` from dy, its x, w and gate, and the z that it kept: (dx, dw, dbias,
     dgate), None where not asked for (dgate is None without a gate).  The residual's gradient is
-    dy.  z is needed with an activation or a gate's gradient."""
+    dy.  z, of x's type or fp32, is needed with an activation or a gate's gradient."""
     flags = _flags(x, activation)
     m, n, k = _sizes(x, w)
     shape = (*x.shape[:-1], n)
@@ -185,7 +192,9 @@ def linear_backward(dy, x, w, z=None, activation=None, gate=None, need_dx: bool 
     if z is None and (activation is not None or need_dgate):
         raise ValueError("an activation, or a gate's gradient, needs z")
     if z is not None:
-        _matrix(z, "z", x.dtype, shape)
+        if z.dtype is _torch().float32:
+            flags |= _Z_FP32
+        _matrix(z, "z", z.dtype if flags & _Z_FP32 else x.dtype, shape)
     dx = x.new_empty(x.shape) if need_dx else None
     dw = x.new_empty((n, k)) if need_dw else None
     dbias = x.new_empty((n,)) if need_dbias else None

@@ -261,3 +261,22 @@ def test_a_sum_past_fp32(act):
 def test_tiles(m, n, k):
     """Forward, dx and dw in tiles of 256 x 128 and of 256 x 256 each."""
     run((m,), n, k, act="gelu_tanh", gate="shared", residual=True, back=True)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("n", [64, 65])
+def test_a_gate_keeps_z_in_fp32(act, n):
+    """One row to a gate row, where nothing averages z's rounding out: dgate is off by the result's half step."""
+    x, w, dy = rand(50, 1, 72, seed=1), rand(n, 72, seed=2, std=72 ** -0.5), rand(50, 1, n, seed=3)
+    gate = rand(50, n, seed=4)
+    y, z = dense.linear(x, w, activation=act, gate=gate, keep=True)
+    assert z.dtype is torch.float32
+    dg = dense.linear_backward(dy, x, w, z, activation=act, gate=gate)[3]
+    z64 = x.double() @ w.double().t()
+    want = (dy.double() * act64(z64, act))[:, 0]
+    err = 1.13 * (72 + 4) * U * (x.double().abs() @ w.double().t().abs()) + (2e-5 * act64(z64, act).abs() if act else 0)
+    check(dg, want, (dy.double().abs() * err)[:, 0] + 2 * U * want.abs(), "dgate")
+    rounded = z.to(BF)                                             # is taken too
+    dg = dense.linear_backward(dy, x, w, rounded, activation=act, gate=gate)[3]
+    want = (dy.double() * act64(rounded.double(), act))[:, 0]
+    check(dg, want, 2e-5 * want.abs(), "dgate of a rounded z")
