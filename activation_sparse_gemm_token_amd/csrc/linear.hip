@@ -608,13 +608,20 @@ linear_dz_kernel(LinearDz a) {
   }
 }
 
-// out[row][c] = the sum of `parts` rows of partials [row][part][c], in order (16 threads a column).
+// dbias, the sum of all parts' rows, and dgate, of each gate row's parts, in order (16 threads a column).
+// Workgroups: dbias's columns (where it is wanted), then dgate's by rows.
 template <int TYPE>
 __global__ void __launch_bounds__(1024)
-linear_sums_kernel(const float* __restrict__ partials, int64_t parts, int64_t C, uint16_t* out) {
+linear_sums_kernel(LinearDz a) {
   __shared__ float lds[16][64];
   const int col = threadIdx.x & 63, p = threadIdx.x >> 6;
-  const int64_t row = blockIdx.y, c = (int64_t)blockIdx.x * 64 + col;
+  const int64_t C = a.N, per = (C + 63) / 64, bias = a.dbias != nullptr ? per : 0, id = folded_block();
+  const bool is_gate = id >= bias;
+  const int64_t row = is_gate ? (id - bias) / per : 0, c = ((is_gate ? id - bias : id) - row * per) * 64 + col;
+  if (row >= (a.dgate != nullptr || !is_gate ? a.groups : 0)) return;
+  const float* const partials = is_gate ? a.gate_part : a.bias_part;
+  const int64_t parts = is_gate ? a.parts : a.groups * a.parts;
+  uint16_t* const out = is_gate ? a.dgate : a.dbias;
   float s = 0.f;
   if (c < C)
     for (int64_t i = p; i < parts; i += 16) s += partials[(row * parts + i) * C + c];
@@ -657,14 +664,9 @@ hipError_t run_dz(const LinearDz& a, hipStream_t stream) {
   auto* k = a.z_fp32 ? (wide ? &linear_dz_kernel<TYPE, kFp32, 8> : &linear_dz_kernel<TYPE, kFp32, 1>)
                      : (wide ? &linear_dz_kernel<TYPE, TYPE, 8> : &linear_dz_kernel<TYPE, TYPE, 1>);
   hipError_t e = launch(k, grid, dim3(256), stream, a);
-  const unsigned blocks = (unsigned)((a.N + 63) / 64);
-  if (e == hipSuccess && a.dbias != nullptr)
-    e = launch(&linear_sums_kernel<TYPE>, dim3(blocks, 1), dim3(1024), stream, (const float*)a.bias_part, a.groups * a.parts,
-               a.N, a.dbias);
-  if (e == hipSuccess && a.dgate != nullptr)
-    e = launch(&linear_sums_kernel<TYPE>, dim3(blocks, (unsigned)a.groups), dim3(1024), stream, (const float*)a.gate_part,
-               a.parts, a.N, a.dgate);
-  return e;
+  const int64_t blocks = (a.N + 63) / 64 * ((a.dbias != nullptr ? 1 : 0) + (a.dgate != nullptr ? a.groups : 0));
+  if (e != hipSuccess || blocks == 0) return e;
+  return launch(&linear_sums_kernel<TYPE>, folded_grid_of_1024(blocks), dim3(1024), stream, a);
 }
 
 }  // namespace

@@ -33,7 +33,8 @@ struct Width {
 };
 
 size_t partial_bytes(int64_t rows, int64_t C, int64_t groups) {
-  return (size_t)(groups * rtl::norm_parts(rows, groups, C)) * 2 * (size_t)C * 4;
+  const int64_t parts = rtl::norm_parts(rows, groups, C);
+  return parts > 1 ? (size_t)(groups * parts) * 2 * (size_t)C * 4 : 0;
 }
 
 bool type_flags_ok(uint32_t flags) {
@@ -121,8 +122,8 @@ RTL_API rtl_status rtl_layer_norm_backward(const void* dy, int64_t dy_batch_stri
       !rtl::aligned(dweight, wsize) || !rtl::aligned(dbias, wsize) || !rtl::aligned(mean, 4) || !rtl::aligned(rstd, 4) ||
       !rtl::aligned(workspace, 16))
     return RTL_ERR_MISALIGNED;
-  if (dweight != nullptr && (workspace == nullptr || workspace_bytes < partial_bytes(rows, C, groups)))
-    return RTL_ERR_WORKSPACE;
+  const size_t need = dweight != nullptr ? partial_bytes(rows, C, groups) : 0;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return RTL_ERR_WORKSPACE;
   Width w;
   for (const void* p : {x, dy, (const void*)dx}) w.add(p);
   for (int64_t s : {C, x_batch_stride, x_token_stride, dy_batch_stride, dy_token_stride}) w.add(s * elem);
@@ -140,7 +141,7 @@ RTL_API rtl_status rtl_layer_norm_backward(const void* dy, int64_t dy_batch_stri
   a.dx = dx;
   a.dweight = dweight;
   a.dbias = dbias;
-  a.partials = dweight != nullptr ? static_cast<float*>(workspace) : nullptr;
+  a.partials = static_cast<float*>(workspace);
   a.rows = rows;
   a.tokens = tokens > 0 ? tokens : 1;
   a.groups = groups;

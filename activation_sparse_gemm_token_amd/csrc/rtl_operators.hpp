@@ -17,6 +17,11 @@ inline dim3 folded_grid(int64_t blocks, unsigned y = 1) {
   constexpr int64_t kRow = (int64_t)1 << 22;
   return blocks <= kRow ? dim3((unsigned)blocks, y) : dim3((unsigned)kRow, y, (unsigned)((blocks + kRow - 1) / kRow));
 }
+// The same for workgroups of 1024, in rows of 2^21.
+inline dim3 folded_grid_of_1024(int64_t blocks) {
+  constexpr int64_t kRow = (int64_t)1 << 21;
+  return blocks <= kRow ? dim3((unsigned)blocks) : dim3((unsigned)kRow, 1, (unsigned)((blocks + kRow - 1) / kRow));
+}
 __device__ __forceinline__ int64_t folded_block() { return (int64_t)blockIdx.z * gridDim.x + blockIdx.x; }
 
 // Rotary positions.  One tensor [batch, tokens, heads, dim] and its result
@@ -115,7 +120,7 @@ struct NormBackArgs {
   void* dx;
   void* dweight;
   void* dbias;
-  float* partials;                       // [groups][parts][2][C], NULL without dweight
+  float* partials;                       // [groups][parts][2][C], where there is more than one part
   int64_t rows, tokens, groups, parts;
   int64_t gb, gt, xb, xt, db, dt, wb;
   float offset, inv_c;

@@ -193,8 +193,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, offset: float = 0.0, nee
             dw = torch.empty_like(weight, memory_format=torch.contiguous_format)
             db = torch.empty_like(dw)
             size = backward_workspace_bytes(batch, tokens, c, groups)
-            workspace = _workspace(workspace, size, x.device)
-            dwp, dbp, work, size = dw.data_ptr(), db.data_ptr(), workspace.data_ptr(), workspace.numel()
+            dwp, dbp = dw.data_ptr(), db.data_ptr()
+            if workspace is not None or size:
+                workspace = _workspace(workspace, size, x.device)
+                work, size = workspace.data_ptr(), workspace.numel()
     if need_dx:
         dx = torch.empty_like(x, memory_format=torch.contiguous_format)
         dxp = dx.data_ptr()

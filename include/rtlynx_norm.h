@@ -64,7 +64,8 @@ rtl_status rtl_layer_norm(const void* x, int64_t batch, int64_t tokens, int64_t 
  *   dx              may be NULL.  dweight, dbias: [groups, C], densely
  *                   packed, of the weight's type; both or neither NULL.
  *   workspace       rtl_layer_norm_backward_workspace_bytes(batch, tokens, C,
- *                   groups) bytes, 16-byte aligned; may be NULL without dweight.
+ *                   groups) bytes (0 for few rows), 16-byte aligned; may be NULL
+ *                   without dweight.
  *
  * The sums over tokens are formed in an order that only the sizes fix.  With
  * no tokens dweight and dbias are zeros.

@@ -49,9 +49,10 @@ def test_backward_refusals():
     for bad in (dict(dy=P + 1), dict(x=P2 + 1), dict(dx=P6 + 1), dict(dw=P7 + 1), dict(mean=P3 + 1), dict(ws=P + 8),
                 dict(dw=P7 + 2, flags=0x10)):
         assert _backward(**bad) == MISAL, bad
-    need = norm.backward_workspace_bytes(2, 3, 64, 1)
-    assert need > 0 and _backward(wsb=need - 1) == WS and _backward(ws=None) == WS
-    assert norm.backward_workspace_bytes(2, 3, 64, 2) > 0 and norm.backward_workspace_bytes(2, 3, 64, 3) == 0
+    need = norm.backward_workspace_bytes(2, 300, 64, 1)
+    assert need > 0 and _backward(t=300, wsb=need - 1) == WS and _backward(t=300, ws=None) == WS
+    assert norm.backward_workspace_bytes(2, 300, 64, 2) > 0 and norm.backward_workspace_bytes(2, 300, 64, 3) == 0
+    assert norm.backward_workspace_bytes(2, 3, 64, 1) == 0                  # one workgroup has all rows
     assert _backward(b=0, groups=0) == OK and _backward(t=0, dw=None, db=None, dy=None) == OK
     assert _backward(dx=None, dw=None, db=None) == OK
     if _no_gpu():
