@@ -20,9 +20,11 @@ Entry points (same names as the C ABI in include/rtlynx.h, without the
 * ``sparse_linear_workspace_bytes(M, K, r)``
 
 No call records an autograd graph: results have no ``grad_fn``, and a gradient is a
-call of its own (``training.sparse_linear_backward``, ``rotary.rope_backward``), for
-instance in a ``torch.autograd.Function``.  The layers, ``w4.linear`` and
-``rotary.rope`` warn where gradients are enabled and an input requires one.
+call of its own (``training.sparse_linear_backward``, ``rotary.rope_backward``,
+``norm.layer_norm_backward``, ``dense.linear_backward``, ``attention.attention_backward``), for
+instance in a ``torch.autograd.Function``.  The layers, ``w4.linear``, ``rotary.rope``,
+``norm.layer_norm``, ``dense.linear`` and ``attention.attention`` warn where gradients are
+enabled and an input requires one.
 """
 from __future__ import annotations
 

@@ -61,8 +61,8 @@ __device__ __forceinline__ float max16(const f32x16& s) {
 // counts is how many share a SIMD: three with 32 keys and 168 registers, four with 64 keys up to head_dim 64.
 //
 // 2 x 4608 tokens, 24 heads of 128: 500 us with the join of the last tiles, 1040 TFLOP/s, the matrix cores 60 % busy at
-// the 1.8 GHz that the card's power leaves them then; alone they reach 1490 TFLOP/s.  Measured there and not kept: two wavefronts with
-// tiles of 64 keys 521; 8 wavefronts to a workgroup 533 (of 3 or 4 stages 588, 537); the next step's scores formed
+// the 1.8 GHz that the card's power leaves them then; alone they reach 1490 TFLOP/s.  Measured there and not kept: two
+// wavefronts with tiles of 64 keys 521; 8 wavefronts to a workgroup 533 (of 3 or 4 stages 588, 537); the next step's scores formed
 // during a softmax 550; 64 queries a wavefront, which halves the reads of LDS but takes 512 registers of two kinds,
 // with moves between them, 612; higher wave priority during the products 512.
 constexpr int kForwardWaves = 4, kForwardQueries = 32 * kForwardWaves;

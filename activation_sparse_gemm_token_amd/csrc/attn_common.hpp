@@ -11,7 +11,7 @@
 // channels wanted along the operand's rows), which ds_read_b64_tr_b16 delivers
 // four rows at a time.
 //
-// Tiles of 64 rows (32 in the kernel for few queries) go from memory to LDS by direct copies, 16 bytes a lane.  A
+// Tiles of 32 or 64 rows go from memory to LDS by direct copies, 16 bytes a lane.  A
 // row takes 128 or 256 bytes of LDS (head_dim up to 64, or 128), channels past
 // head_dim and rows past the sequence arrive as zeros.  Chunk c of 16 bytes of row r
 // lies in slot c ^ swizzle(r): the 16 rows at one chunk that an ordinary

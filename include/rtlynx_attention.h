@@ -84,7 +84,8 @@ rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor* k, con
                          void* workspace, size_t workspace_bytes, uint32_t flags, void* hip_stream);
 
 /*
- * rtl_attention_backward - with p from lse, D = sum over channels of d_o o:
+ * rtl_attention_backward - with p from lse, D = sum over channels of d_o o
+ * (up to 128 keys formed as the sum over keys of p d_o v^T, without o's rounding):
  *
  *   dv = p^T d_o,  ds = p * (d_o v^T - D),  dq = scale ds k,  dk = scale ds^T q
  *
