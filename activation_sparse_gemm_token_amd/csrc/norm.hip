@@ -6,7 +6,7 @@
 // and 6 backward in 16 bits.  9216 rows of 4096 in bf16: 29.9 us, 5.0 TB/s, a
 // copy's rate; backward, 8192 rows of 4096: 49 us, 4.1 TB/s, and 6 for the join.
 //
-// TPR threads share a row (64: a wavefront, no barrier; 256; 1024), each
+// TPR threads share a row (up to 64, a wavefront, without a barrier; 128 to 1024), each
 // holds E elements in E / VEC pieces of VEC, piece i at channel
 // VEC (TPR i + thread).  VEC is the widest access that divides every row.
 #include "rtl_elem.hpp"
@@ -18,22 +18,25 @@ namespace {
 
 constexpr int kBlock = 256;
 
-// Sum over a wavefront, the same bits in every lane: by data-parallel moves within rows of 16 lanes (xor 1
+// Sum over LANES lanes (16, 32 or a wavefront), the same bits in every one of them: by data-parallel moves within rows of 16 lanes (xor 1
 // and 2, mirrored halves, mirrored rows), then by swaps of rows and halves; no trip through LDS.
 template <int CTRL>
 __device__ __forceinline__ float add_moved(float v) {
   const int w = __builtin_bit_cast(int, v);
   return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(w, w, CTRL, 0xf, 0xf, false));
 }
-__device__ __forceinline__ float wave_sum(float v) {
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float v) {
   v = add_moved<0xB1>(v);                               // quad_perm 1, 0, 3, 2
   v = add_moved<0x4E>(v);                               // quad_perm 2, 3, 0, 1
   v = add_moved<0x141>(v);                              // row_half_mirror
   v = add_moved<0x140>(v);                              // row_mirror
+  if constexpr (LANES == 16) return v;
   const uint32_t a = __builtin_bit_cast(uint32_t, v);
   const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
   const uint32_t r0 = r[0], r1 = r[1];
   v = __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+  if constexpr (LANES == 32) return v;
   const uint32_t b = __builtin_bit_cast(uint32_t, v);
   const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
   const uint32_t h0 = h[0], h1 = h[1];
@@ -44,7 +47,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // row's slots [TPR / 64], a fresh set in each call between two barriers.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
-  v = wave_sum(v);
+  v = lane_sum<TPR < 64 ? TPR : 64>(v);
   if constexpr (TPR > 64) {
     if ((threadIdx.x & 63) == 0) lds[(threadIdx.x % TPR) >> 6] = v;
     __syncthreads();
@@ -83,7 +86,7 @@ norm_kernel(NormArgs a) {
   __shared__ float lds[2][kThreads / 64];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int64_t row = folded_block() * kRows + sub;
-  // Rows past the last one: TPR is 64 then (no barrier), or there is none.
+  // Rows past the last one: TPR is 64 or less then (no barrier), or there is none.
   if (row >= a.rows) return;
   const int64_t b = row / a.tokens, tok = row - b * a.tokens;
   const T* x = static_cast<const T*>(a.x) + b * a.xb + tok * a.xt;
@@ -150,7 +153,7 @@ constexpr int kBackBlock = 1024;
 template <int TYPE, int VEC, int TPR, int E>
 __global__ void __launch_bounds__(kBackBlock)
 norm_backward_kernel(NormBackArgs a) {
-  constexpr int kRows = kBackBlock / TPR, kPieces = E / VEC, kWaves = TPR / 64;
+  constexpr int kRows = kBackBlock / TPR, kPieces = E / VEC, kWaves = TPR < 64 ? 1 : TPR / 64;
   using T = elem_t<TYPE>;
   __shared__ __attribute__((aligned(16))) float sums[kRows > 1 ? 8 * kBackBlock : 1];
   __shared__ float lds[2][kRows][2 * kWaves];           // alternating, so one barrier a row is enough
@@ -214,8 +217,8 @@ norm_backward_kernel(NormBackArgs a) {
       }
     }
     if (a.dx == nullptr) return;                        // uniform over the grid
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
+    s1 = lane_sum<TPR < 64 ? TPR : 64>(s1);
+    s2 = lane_sum<TPR < 64 ? TPR : 64>(s2);
     if constexpr (TPR > 64) {
       float* const mine = lds[flip][sub];
       if ((threadIdx.x & 63) == 0) {
@@ -252,16 +255,26 @@ norm_backward_kernel(NormBackArgs a) {
   };
   // Every thread of the workgroup makes the same number of steps (barriers).
   const int64_t step = a.parts * kRows;
+  // The next rows are loaded ahead where 128 registers hold two sets (2730 rows of 12288 in fp32, with spills: 160
+  // us, 98 without).
+  constexpr bool kAhead = E * (int)sizeof(T) <= 32;
   Row r0, r1;
   int64_t at = part * kRows;
-  if (at < group_rows) load(r0, at + sub);
-  for (; at < group_rows; at += 2 * step) {
-    const bool more = at + step < group_rows;
-    if (more) load(r1, at + step + sub);
-    use(r0, at + sub);
-    if (more) {
-      if (at + 2 * step < group_rows) load(r0, at + 2 * step + sub);
-      use(r1, at + step + sub);
+  if constexpr (kAhead) {
+    if (at < group_rows) load(r0, at + sub);
+    for (; at < group_rows; at += 2 * step) {
+      const bool more = at + step < group_rows;
+      if (more) load(r1, at + step + sub);
+      use(r0, at + sub);
+      if (more) {
+        if (at + 2 * step < group_rows) load(r0, at + 2 * step + sub);
+        use(r1, at + step + sub);
+      }
+    }
+  } else {
+    for (; at < group_rows; at += step) {
+      load(r0, at + sub);
+      use(r0, at + sub);
     }
   }
   if (a.dweight == nullptr) return;
@@ -322,12 +335,14 @@ norm_join_kernel(const float* __restrict__ partials, int64_t groups, int64_t par
 }
 
 // Elements per thread and threads per row by C: up to 2048 channels a wavefront
-// a row, up to 8192 four, else sixteen.
+// a row (or a quarter or half of it, where a whole one would have idle lanes), up to 8192 four, else sixteen.
 template <int TYPE, int VEC>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   auto go = [&](auto k, int64_t threads, int64_t rows) {
     return launch(k, folded_grid((a.rows + rows - 1) / rows), dim3((unsigned)threads), stream, a);
   };
+  if (a.C <= 128) return go(&norm_kernel<TYPE, VEC, 16, 8>, 256, 16);
+  if (a.C <= 256) return go(&norm_kernel<TYPE, VEC, 32, 8>, 256, 8);
   if (a.C <= 512) return go(&norm_kernel<TYPE, VEC, 64, 8>, 256, 4);
   if (a.C <= 1024) return go(&norm_kernel<TYPE, VEC, 64, 16>, 256, 4);
   if (a.C <= 2048) return go(&norm_kernel<TYPE, VEC, 64, 32>, 256, 4);
@@ -336,13 +351,25 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   return go(&norm_kernel<TYPE, VEC, 1024, 32>, 1024, 1);
 }
 
+// As few threads to a row as hold it and its sums in 128 registers: more rows on their way.  (32768 x 1024 in fp32 126
+// us with 16 elements a thread, 85 with 8; 13106 x 5120 in bf16 137 us with 1024 threads, 107 with 512.)
 template <int TYPE, int VEC>
 hipError_t run_backward(const NormBackArgs& a, hipStream_t stream) {
   auto go = [&](auto k) { return launch(k, folded_grid_of_1024(a.groups * a.parts), dim3(kBackBlock), stream, a); };
+  if (a.C <= 128) return go(&norm_backward_kernel<TYPE, VEC, 16, 8>);
+  if (a.C <= 256) return go(&norm_backward_kernel<TYPE, VEC, 32, 8>);
   if (a.C <= 512) return go(&norm_backward_kernel<TYPE, VEC, 64, 8>);
-  if (a.C <= 1024) return go(&norm_backward_kernel<TYPE, VEC, 64, 16>);
-  if (a.C <= 2048) return go(&norm_backward_kernel<TYPE, VEC, 256, 8>);
-  if (a.C <= 4096) return go(&norm_backward_kernel<TYPE, VEC, 256, 16>);
+  if constexpr (TYPE == kFp32) {
+    if (a.C <= 1024) return go(&norm_backward_kernel<TYPE, VEC, 128, 8>);
+    if (a.C <= 2048) return go(&norm_backward_kernel<TYPE, VEC, 256, 8>);
+    if (a.C <= 4096) return go(&norm_backward_kernel<TYPE, VEC, 512, 8>);
+    if (a.C <= 8192) return go(&norm_backward_kernel<TYPE, VEC, 1024, 8>);
+  } else {
+    if (a.C <= 1024) return go(&norm_backward_kernel<TYPE, VEC, 64, 16>);
+    if (a.C <= 2048) return go(&norm_backward_kernel<TYPE, VEC, 128, 16>);
+    if (a.C <= 4096) return go(&norm_backward_kernel<TYPE, VEC, 256, 16>);
+    if (a.C <= 8192) return go(&norm_backward_kernel<TYPE, VEC, 512, 16>);
+  }
   if (a.C <= 16384) return go(&norm_backward_kernel<TYPE, VEC, 1024, 16>);
   return go(&norm_backward_kernel<TYPE, VEC, 1024, 32>);
 }
@@ -354,7 +381,8 @@ hipError_t run_backward(const NormBackArgs& a, hipStream_t stream) {
 // than the second launch's (64 rows of 256: a call of 12 us, 16 in four parts).  A rule on sizes alone, so that the
 // sums' order is the same everywhere.
 int64_t norm_parts(int64_t rows, int64_t groups, int64_t C) {
-  const int64_t per = C <= 1024 ? 16 : C <= 4096 ? 4 : 1;         // rows a workgroup takes at once
+  // Rows a workgroup takes at once (half as many in fp32 from 513 channels on).
+  const int64_t per = C <= 128 ? 64 : C <= 256 ? 32 : C <= 1024 ? 16 : C <= 2048 ? 8 : C <= 4096 ? 4 : C <= 8192 ? 2 : 1;
   const int64_t group_rows = rows / groups;
   int64_t parts = (256 + groups - 1) / groups;
   const int64_t most = (group_rows + per - 1) / per;

@@ -112,7 +112,7 @@ def run(shape, dtype, affine, offset=0.0, eps=1e-5, wtype=None, std=1.0, mean=0.
     assert only[0] is None and torch.equal(only[1], dw) and torch.equal(only[2], db)
 
 
-CHANNELS = [1, 2, 7, 8, 63, 64, 65, 100, 512, 520, 1023, 1024, 1028, 2048, 2052, 2049, 4096, 4100, 5001, 8192, 8200, 12288, 16384,
+CHANNELS = [1, 2, 7, 8, 63, 64, 65, 100, 128, 129, 200, 256, 260, 512, 520, 1023, 1024, 1028, 2048, 2052, 2049, 4096, 4100, 5001, 8192, 8200, 12288, 16384,
             16392, 20001, 32768]
 
 
