@@ -14,7 +14,7 @@
 // for 2048 cycles of products; the smaller ones where there are too few tiles for the card
 // (linear_form).
 //
-// linear_rows_kernel.  Up to 32 rows of x are bound by reading w: a workgroup takes 16
+// linear_rows_kernel.  Up to 16 or 32 rows of x are bound by reading w: a workgroup takes 16
 // channels of w, its wavefronts share out K.  3 x 4099 x 4096: 10.9 us, 3.1 TB/s.
 //
 // Sizes with too few tiles for the card split the contraction; linear_join_kernel
@@ -684,8 +684,11 @@ hipError_t run_dz(const LinearDz& a, hipStream_t stream) {
 // contraction cost a second launch and their fp32 parts, written and read at 4 TB/s.  Measured with the three tiles, bf16:
 // 8192 x 2048 x 4096: 107, 122 and 129; 4096 x 2048 x 8192: 163, 116 and 126; 2048 x 2048 x 2048: 48, 31 and 28; 2310 x
 // 1160 x 1152: 18 with the smallest, 33 with it and three ranges.
+//
+// Up to 16 rows go to the kernel for few rows, 17 to 32 where it is expected to take less (its time and the tiles' measured,
+// 3 us more than above in these sizes): 32 x 4096 x 4096: 15 us, tiles 18; 32 x 12288 x 4096: 43 and 30.
 LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel) {
-  if (rows_kernel && M <= 32) return {0, 0, 1};
+  if (rows_kernel && M <= 16) return {0, 0, 1};
   const int64_t m256 = (M + 255) / 256, m128 = (M + 127) / 128, n256 = (N + 255) / 256, n128 = (N + 127) / 128;
   const int64_t small = m128 * n128, steps = (K + 63) / 64;
   if (small == 0 || steps == 0) return {128, 128, 1};
@@ -705,6 +708,7 @@ LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel) {
       best = {128, 128, (int)splits};
     }
   }
+  if (rows_kernel && M <= 32 && 2.0 + 2e-6 * (double)N * (double)K * (0.21 + 0.0064 * (double)M) < least + 3.0) return {0, 0, 1};
   return best;
 }
 

@@ -164,7 +164,7 @@ def linear(x, w, bias=None, activation=None, gate=None, residual=None, out=None,
             z = x.new_empty(shape, dtype=_torch().float32)
             flags |= _Z_FP32
         zp = z.data_ptr()
-    if m > 32:                                            # the kernel for few rows needs none
+    if m > 16:                                            # the kernel for few rows needs none
         size = workspace_bytes(m, n, k)
     if workspace is not None or size:
         workspace = _workspace(workspace, size, x.device)

@@ -280,3 +280,9 @@ def test_a_gate_keeps_z_in_fp32(act, n):
     dg = dense.linear_backward(dy, x, w, rounded, activation=act, gate=gate)[3]
     want = (dy.double() * act64(rounded.double(), act))[:, 0]
     check(dg, want, 2e-5 * want.abs(), "dgate of a rounded z")
+
+
+def test_17_to_32_rows_of_a_large_weight():
+    """Tiles, the contraction in ranges: a workspace, where 16 rows need none."""
+    assert dense.workspace_bytes(20, 9000, 3336) > 0 and dense.workspace_bytes(16, 9000, 3336) == 0
+    run((20,), 9000, 3336, act="silu", gate="shared", residual=True)
