@@ -284,5 +284,5 @@ def test_a_gate_keeps_z_in_fp32(act, n):
 
 def test_17_to_32_rows_of_a_large_weight():
     """Tiles, the contraction in ranges: a workspace, where 16 rows need none."""
-    assert dense.workspace_bytes(20, 9000, 3336) > 0 and dense.workspace_bytes(16, 9000, 3336) == 0
-    run((20,), 9000, 3336, act="silu", gate="shared", residual=True)
+    assert dense.workspace_bytes(30, 12001, 4096) > 0 and dense.workspace_bytes(16, 12001, 4096) == 0
+    run((30,), 12001, 4096, act="silu", gate="shared", residual=True)
