@@ -64,16 +64,23 @@ __device__ __forceinline__ float sigmoid2(float v) { return rcp_(1.f + exp2_(-v)
 
 constexpr float kTanhA = 0.7978845608028654f, kTanhB = 0.044715f;
 
+// z where it multiplies what vanishes at both ends, or at the lower one: the other factor is exactly 0 from `end` on, so no
+// finite z's result changes, and an infinite one (a sum past fp32, or past the type that z is kept in) has its limit
+// where inf * 0 would not be a number.  NaN stays: the other factor is NaN then.
+__device__ __forceinline__ float within(float z, float end) { return __builtin_amdgcn_fmed3f(z, -end, end); }
+__device__ __forceinline__ float above(float z, float end) { return __builtin_amdgcn_fmed3f(z, -end, __builtin_inff()); }
+constexpr float kGeluEnd = 64.f, kTanhEnd = 16.f, kSiluEnd = 128.f;
+
 __device__ __forceinline__ float act(float z, int kind) {
   switch (kind) {
     case kActGelu: {
-      const float low = __builtin_amdgcn_fmed3f(z, -64.f, 64.f) * phi_lower(z);        // z Phi(-|z|), 0 beyond
+      const float low = within(z, kGeluEnd) * phi_lower(z);                            // z Phi(-|z|)
       return z > 0.f ? z - low : low;
     }
     case kActGeluTanh:                                  // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-      return z * sigmoid2(2.f * kLog2e * kTanhA * (z + kTanhB * z * z * z));
+      return above(z, kTanhEnd) * sigmoid2(2.f * kLog2e * kTanhA * (z + kTanhB * z * z * z));
     case kActSilu:
-      return z * sigmoid2(kLog2e * z);
+      return above(z, kSiluEnd) * sigmoid2(kLog2e * z);
     default:
       return z;
   }
@@ -83,20 +90,20 @@ __device__ __forceinline__ float act(float z, int kind) {
 __device__ __forceinline__ float act_slope(float z, int kind, float& value) {
   switch (kind) {
     case kActGelu: {
-      const float low = phi_lower(z), phi = z > 0.f ? 1.f - low : low;
-      value = z > 0.f ? z - z * low : z * low;
-      return phi + z * 0.3989422804014327f * exp2_(-0.5f * kLog2e * z * z);
+      const float c = within(z, kGeluEnd), low = phi_lower(c), phi = c > 0.f ? 1.f - low : low;
+      value = c > 0.f ? z - c * low : c * low;
+      return phi + c * 0.3989422804014327f * exp2_(-0.5f * kLog2e * c * c);
     }
     case kActGeluTanh: {
       const float s = sigmoid2(2.f * kLog2e * kTanhA * (z + kTanhB * z * z * z));
-      value = z * s;
-      const float c = __builtin_amdgcn_fmed3f(z, -16.f, 16.f);          // s (1 - s) is 0 beyond, z^3 may be infinite
+      value = above(z, kTanhEnd) * s;
+      const float c = within(z, kTanhEnd);              // z^3 may be infinite too
       return s + 2.f * c * s * (1.f - s) * kTanhA * (1.f + 3.f * kTanhB * c * c);
     }
     case kActSilu: {
       const float s = sigmoid2(kLog2e * z);
-      value = z * s;
-      return s * (1.f + z * (1.f - s));
+      value = above(z, kSiluEnd) * s;
+      return s * (1.f + within(z, kSiluEnd) * (1.f - s));
     }
     default:
       value = z;

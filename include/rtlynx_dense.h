@@ -9,6 +9,8 @@
  *
  * Accumulation, bias, activation, gate and residual are fp32 and y is rounded
  * once.  act is none, GELU (z Phi(z)), its tanh form, or SiLU (z / (1 + e^-z)).
+ * An infinite z (a sum past fp32, or kept in a type that it passes) has its
+ * limits: act inf and 0, slope 1 and 0.
  * The gate has one value per output channel, or one row per sequence (rows of
  * x in equal parts).
  *
