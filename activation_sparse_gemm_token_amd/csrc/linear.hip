@@ -90,9 +90,9 @@ __device__ __forceinline__ float act(float z, int kind) {
 __device__ __forceinline__ float act_slope(float z, int kind, float& value) {
   switch (kind) {
     case kActGelu: {
-      const float c = within(z, kGeluEnd), low = phi_lower(c), phi = c > 0.f ? 1.f - low : low;
-      value = c > 0.f ? z - c * low : c * low;
-      return phi + c * 0.3989422804014327f * exp2_(-0.5f * kLog2e * c * c);
+      const float low = phi_lower(z), phi = z > 0.f ? 1.f - low : low, c = within(z, kGeluEnd);
+      value = z > 0.f ? z - c * low : c * low;
+      return phi + c * 0.3989422804014327f * exp2_(-0.5f * kLog2e * z * z);
     }
     case kActGeluTanh: {
       const float s = sigmoid2(2.f * kLog2e * kTanhA * (z + kTanhB * z * z * z));
