@@ -339,7 +339,8 @@ norm_join_kernel(const float* __restrict__ partials, int64_t groups, int64_t par
 template <int TYPE, int VEC>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   auto go = [&](auto k, int64_t threads, int64_t rows) {
-    return launch(k, folded_grid((a.rows + rows - 1) / rows), dim3((unsigned)threads), stream, a);
+    const int64_t blocks = (a.rows + rows - 1) / rows;
+    return launch(k, threads > 512 ? folded_grid_of_1024(blocks) : folded_grid(blocks), dim3((unsigned)threads), stream, a);
   };
   if (a.C <= 128) return go(&norm_kernel<TYPE, VEC, 16, 8>, 256, 16);
   if (a.C <= 256) return go(&norm_kernel<TYPE, VEC, 32, 8>, 256, 8);
