@@ -21,9 +21,9 @@ def forward(rows, c):
 
 
 def backward(rows, c, batch=1, groups=1):
-    t = rows // batch
-    return "rtl_layer_norm_backward", [P, t * c, c, P, t * c, c, P, P, batch, t, c, P, c, "f32(0)", groups, P, t * c, c, P, P, P,
-                                       1 << 50, *HIDDEN]
+    """Rows one after another: of one sequence, or one of each."""
+    b, t = (0, rows) if batch == 1 else (c, 1)
+    return "rtl_layer_norm_backward", [P, b, c, P, b, c, P, P, batch, t, c, P, c, "f32(0)", groups, P, b, c, P, P, P, 1 << 50, *HIDDEN]
 
 
 CHANNELS = [1, 16, 128, 256, 512, 1024, 2048, 4096, 8192, 8193, 16384, 16385, 32768]
