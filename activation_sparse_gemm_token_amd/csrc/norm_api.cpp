@@ -12,7 +12,7 @@ bool stride_ok(int64_t s) { return s >= 0 && s < kMaxStride; }
 
 bool sizes_ok(int64_t batch, int64_t tokens, int64_t C) {
   return batch >= 0 && tokens >= 0 && batch < kMaxRows && tokens < kMaxRows && C >= 1 && C <= RTL_NORM_MAX_CHANNELS &&
-         (tokens == 0 || batch < kMaxRows / tokens);
+         (tokens == 0 || batch <= (kMaxRows - 1) / tokens);
 }
 
 // The widest access, in elements, that divides every address.

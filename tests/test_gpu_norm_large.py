@@ -38,3 +38,7 @@ def in_place(rows, c, seed):
 
 def test_more_workgroups_of_1024_than_a_dimension_holds():
     in_place((1 << 22) + 1, 8200, 1)                               # 69 GB
+
+
+def test_more_than_two_to_the_30_rows():
+    in_place((1 << 30) + 9, 8, 2)

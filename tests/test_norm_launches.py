@@ -46,3 +46,13 @@ def test_gradients_of_many_rows_and_sequences(lib):
     for call, (status, got) in zip(calls, launches.record(lib, calls)):
         assert status == 0 and got
         assert all(launches.launchable(*g) for g in got), (call, got)
+
+
+def test_up_to_two_to_the_31_rows(lib):
+    """batch * tokens < 2^31: the last number below it, and the first that is not."""
+    most = (1 << 31) - 1
+    for c in (1, 9000):
+        for (status, got), fits in zip(launches.record(lib, [forward(most, c), backward(most, c), forward((1 << 30) + 1, c),
+                                                            backward(most, c, most, most), forward(most + 1, c)]), (1, 1, 1, 1, 0)):
+            assert status == (0 if fits else 2)                    # RTL_ERR_BAD_SHAPE
+            assert bool(got) == bool(fits) and all(launches.launchable(*g) for g in got)
