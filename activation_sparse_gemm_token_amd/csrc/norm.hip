@@ -102,7 +102,9 @@ norm_kernel(NormArgs a) {
   for (int i = 0; i < kPieces; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) sum += raw[i].get(j);
-  const float mean = row_sum<TPR>(sum, lds[0]) * a.inv_c;
+  // Divided by C, not multiplied by its rounded inverse: rows of one value have exactly that mean, and so 0 as their
+  // result.  (1000 channels of 1000: the inverse gives a mean half a step too large, and results of -0.019.)
+  const float mean = row_sum<TPR>(sum, lds[0]) / (float)a.C;
   float sq = 0.f;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
