@@ -257,9 +257,10 @@ norm_backward_kernel(NormBackArgs a) {
   };
   // Every thread of the workgroup makes the same number of steps (barriers).
   const int64_t step = a.parts * kRows;
-  // The next rows are loaded ahead where 128 registers hold two sets (2730 rows of 12288 in fp32, with spills: 160
-  // us, 98 without).
-  constexpr bool kAhead = E * (int)sizeof(T) <= 32;
+  // The next rows are loaded ahead where 128 registers hold two sets of them beside the sums, counted in the words that
+  // they take: one element an access fills a register each.  (2730 rows of 12288 in fp32, ahead with spills: 160 us, 98
+  // one row at a time; forward and backward over 8186 rows of 4099 in bf16: 386 and 237.)
+  constexpr bool kAhead = kPieces * Raw<TYPE, VEC>::kWords <= 8;
   Row r0, r1;
   int64_t at = part * kRows;
   if constexpr (kAhead) {
@@ -355,7 +356,8 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
 }
 
 // As few threads to a row as hold it and its sums in 128 registers: more rows on their way.  (32768 x 1024 in fp32 126
-// us with 16 elements a thread, 85 with 8; 13106 x 5120 in bf16 137 us with 1024 threads, 107 with 512.)
+// us with 16 elements a thread, 85 with 8; 13106 x 5120 in bf16 137 us with 1024 threads, 107 with 512.)  They do not
+// with 32 elements a thread, past 16384 channels, nor quite with 16 of one access each from 8193 on: 4 to 199 spills.
 template <int TYPE, int VEC>
 hipError_t run_backward(const NormBackArgs& a, hipStream_t stream) {
   auto go = [&](auto k) { return launch(k, folded_grid_of_1024(a.groups * a.parts), dim3(kBackBlock), stream, a); };
