@@ -161,8 +161,7 @@ attn_forward_kernel(AttnArgs a) {
   // A step's LDS stage is a constant, so that its addresses are the reads' offsets and not additions, 16 of the
   // step's 70 vector instructions (2 x 4608 tokens, 24 heads of 128: 488 us, 508 with a stage from j).
   auto step = [&](int j, auto stage) __attribute__((always_inline)) {
-    wait_copies<0>();
-    group_barrier();                                    // tile j is whole, tile j - 1 is no longer read
+    tile_barrier();                                     // tile j is whole, tile j - 1 is no longer read
     if (j >= my_steps) {
       if (j + 1 < steps) copy(1 - stage);
       return;

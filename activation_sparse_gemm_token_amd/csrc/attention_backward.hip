@@ -152,8 +152,7 @@ attn_dkv_kernel(AttnBackArgs a) {
   const bool any_dead = k0 + 32 > ks.len;
   const char* const vt = lds + wave * 32 * T::kPitch;
   auto step = [&](int64_t j, auto stage) __attribute__((always_inline)) {   // its stage a constant, as in the forward pass
-    wait_copies<0>();
-    group_barrier();
+    tile_barrier();
     if (j + 1 < steps) copy(1 - stage);
     const char* const qt = lds + kVBytes + decltype(stage)::value * kStage;
     const char* const dt = qt + kTile;
@@ -333,8 +332,7 @@ attn_dq_kernel(AttnBackArgs a) {
   // the two tiles of LDS.
   if (few && steps > 0) {
     if (steps == 2) copy(1);
-    wait_copies<0>();
-    group_barrier();
+    tile_barrier();
     float sum = 0.f;
     if (mine > 0) {
       const int left = clamp_rows(limit);
@@ -354,8 +352,7 @@ attn_dq_kernel(AttnBackArgs a) {
   }
   if (live && lane < 32) a.stats[w.lse_off + row] = (f32x2){lse2, delta};       // for the dK / dV kernel
   auto step = [&](int j, auto stage) __attribute__((always_inline)) {
-    wait_copies<0>();
-    group_barrier();
+    tile_barrier();
     if (j + 1 < steps && !few) copy(j + 1);
     const int64_t k0 = (int64_t)j * kKeys;
     if (k0 >= mine) return;

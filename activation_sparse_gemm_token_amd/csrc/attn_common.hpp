@@ -315,8 +315,9 @@ __device__ __forceinline__ int64_t xcd_order4(int64_t id, int64_t total) {
 // Number of copies still in flight that may stay so.
 template <int N>
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void group_barrier() { asm volatile("s_barrier" ::: "memory"); }
-
+// The workgroup's barrier between two tiles: this wavefront's copies have arrived, and its reads of the tile before, which
+// the next copy writes over, are back (in one block: products, and the waits that they bring, may move across an asm).
+__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // What a workgroup of query tiles works on: rows [row, row + ..) of one sequence's queries in one head.
 struct QueryWork {
