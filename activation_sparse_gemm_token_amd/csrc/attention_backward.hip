@@ -297,7 +297,9 @@ attn_dq_kernel(AttnBackArgs a) {
   load_rows<NB>(f.q.p + w.q_off + q0 * f.q.t, f.q.t, w.q.len - q0, f.d, qf);
   const int64_t d_off = b * a.d_o.b + w.q.start * a.d_o.t + w.head * a.d_o.h;
   load_rows<NB>(a.d_o.p + d_off + q0 * a.d_o.t, a.d_o.t, w.q.len - q0, f.d, df);
+  // Whether all of the tile's queries, or some of them, see no more keys than the two tiles of LDS hold.
   const bool live = row < w.q.len, few = steps <= 2;
+  const bool near = steps > 0 && (few || (f.causal && w.tile * kQueries + shift < 2 * kKeys));
   float lse2 = live ? f.lse[w.lse_off + row] : -__builtin_inff();
   lse2 = lse2 == -__builtin_inff() ? __builtin_inff() : lse2 * kLog2e;
   float delta = 0.f;
@@ -328,16 +330,16 @@ attn_dq_kernel(AttnBackArgs a) {
     col_off[nb][1] = T::column_operand(nb, 1);
   }
   // Few keys: o is near the values, ds a difference of near numbers, and o's rounding in D would show (with two
-  // keys dQ and dK were 0.4 % off instead of 0.24 %).  D is the sum of p dP too: formed so where the keys fit
-  // the two tiles of LDS.
-  if (few && steps > 0) {
-    if (steps == 2) copy(1);
+  // keys dQ and dK were 0.4 % off instead of 0.24 %).  D is the sum of p dP too: formed so for the queries
+  // whose keys fit the two tiles of LDS.
+  if (near) {
+    if (steps >= 2) copy(1);
     tile_barrier();
     float sum = 0.f;
-    if (mine > 0) {
+    if (mine > 0 && (few || q0 + shift < 2 * kKeys)) {
       const int left = clamp_rows(limit);
 #pragma unroll 1
-      for (int kb = 0; kb < 2 * steps; ++kb) {
+      for (int kb = 0; kb < (steps >= 2 ? 4 : 2); ++kb) {
         const char* const kk = lds + (kb >> 1) * 2 * kTile + (kb & 1) * 32 * T::kPitch;
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
@@ -348,12 +350,13 @@ attn_dq_kernel(AttnBackArgs a) {
         for (int i = 0; i < 16; ++i) sum += 32 * kb + block_row(i) < left ? exp2_(__builtin_fmaf(s[i], f.c, -lse2)) * dp[i] : 0.f;
       }
     }
-    delta = half_sum(sum);
+    sum = half_sum(sum);
+    delta = limit <= 2 * kKeys ? sum : delta;
   }
   if (live && lane < 32) a.stats[w.lse_off + row] = (f32x2){lse2, delta};       // for the dK / dV kernel
   auto step = [&](int j, auto stage) __attribute__((always_inline)) {
     tile_barrier();
-    if (j + 1 < steps && !few) copy(j + 1);
+    if (j + 1 < steps && !(near && j == 0)) copy(j + 1);
     const int64_t k0 = (int64_t)j * kKeys;
     if (k0 >= mine) return;
     const char* const kt = lds + decltype(stage)::value * 2 * kTile;

@@ -85,7 +85,8 @@ rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor* k, con
 
 /*
  * rtl_attention_backward - with p from lse, D = sum over channels of d_o o
- * (up to 128 keys formed as the sum over keys of p d_o v^T, without o's rounding):
+ * (for a query that sees up to 128 keys formed as the sum over them of p d_o v^T,
+ * without o's rounding):
  *
  *   dv = p^T d_o,  ds = p * (d_o v^T - D),  dq = scale ds k,  dk = scale ds^T q
  *
