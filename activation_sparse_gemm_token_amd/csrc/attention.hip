@@ -92,6 +92,7 @@ attn_forward_kernel(AttnArgs a) {
   }
   QueryWork w;
   if (!query_work(a, id, kForwardQueries, w)) {
+    if (w.tile < 0) return;
     // No tile left: some rows may lie in no sequence.
     const int64_t spare = a.groups - (id - w.tile);
     rest_rows(a.q_starts, a.sequences, a.tq, a.hq, w.tile, spare, [&](int64_t row, int64_t head) {

@@ -51,6 +51,7 @@ attn_dkv_kernel(AttnBackArgs a) {
   if (packed) {
     const PackedTile p = packed_tile(f.k_starts, f.sequences, f.tk, kKvKeys, f.hk, id);
     if (!p.found) {
+      if (p.tile < 0) return;
       const int64_t spare = f.groups / f.splits - (id - p.tile);
       rest_rows(f.k_starts, f.sequences, f.tk, f.hk, p.tile, spare, [&](int64_t row, int64_t head) {
         if (f.splits > 1) {
@@ -262,6 +263,7 @@ attn_dq_kernel(AttnBackArgs a) {
   const int64_t id = f.q_starts != nullptr ? xcd_order4(folded_block(), f.groups) : xcd_order(folded_block(), f.groups);
   QueryWork w;
   if (!query_work(f, id, kQueries, w)) {
+    if (w.tile < 0) return;
     const int64_t spare = f.groups - (id - w.tile);
     rest_rows(f.q_starts, f.sequences, f.tq, f.hq, w.tile, spare, [&](int64_t row, int64_t head) {
       uint16_t* p = a.dq.p + row * a.dq.t + head * a.dq.h;

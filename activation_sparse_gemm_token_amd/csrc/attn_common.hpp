@@ -263,38 +263,71 @@ __device__ __forceinline__ Span packed_span(const int32_t* starts, int64_t s, in
   return {lo, hi - lo};
 }
 
-// Number `id` of the workgroups of a packed batch: tile `tile` of `rows` rows of a sequence in a head.
-// Up to 64 sequences go longest first (a long one started last would run alone at the end), then
-// heads, then tiles.  Not found: none left, `tile` counts those past the last one.
+// Number `id` of the workgroups of a packed batch: tile `tile` of `rows` rows of a sequence in a head; sequences go
+// one after another, then heads, then tiles.  Not found: this workgroup has nothing to do (`tile` < 0), or none is left and
+// `tile` counts those past the last one.
 struct PackedTile {
   bool found;
   int64_t seq, head, tile;
 };
+
+// Up to 64 sequences, a lane to each: the longest first (a long one started last would run alone at the end).
+__device__ __forceinline__ PackedTile longest_first(const int32_t* starts, int64_t sequences, int64_t total, int rows,
+                                                    int64_t heads, int64_t id) {
+  const int lane = threadIdx.x & 63, count = (int)sequences;
+  int32_t n = 0;
+  if (lane < count) n = (int32_t)((packed_span(starts, lane, total).len + rows - 1) / rows);
+  int64_t before = 0, all = 0;                          // tiles of the sequences before this lane's, of all
+  for (int k = 0; k < count; ++k) {
+    const int32_t other = __builtin_amdgcn_readlane(n, k);
+    before += ((other > n) | ((other == n) & (k < lane))) ? other : 0;      // no branch: `all` would lose its scalar register
+    all += other;
+  }
+  const uint64_t hit = __ballot(id >= before * heads && id < (before + n) * heads);
+  if (hit == 0) return {false, 0, 0, id - all * heads};
+  const int at = __builtin_ctzll(hit);
+  const int64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)before, at);
+  const int64_t hi = __builtin_amdgcn_readlane((int)(before >> 32), at);
+  const int64_t in = id - (hi << 32 | lo) * heads, tiles = __builtin_amdgcn_readlane(n, at), head = in / tiles;
+  return {true, at, head, in - head * tiles};
+}
+
+// More sequences: sequence s has the slots from first(s) = floor((its start - the first's) / rows) + s on, which is as
+// many as its tiles or one more, so that it is found by a search and not by a walk over those before it (for 100 000
+// sequences of a token in 8 heads the walks would take seconds).  64 places a step: 2 steps up to 4096 sequences, 4 up to
+// 16 million.
+__device__ __forceinline__ PackedTile by_slot(const int32_t* starts, int64_t sequences, int64_t total, int rows, int64_t heads,
+                                              int64_t id) {
+  const int lane = threadIdx.x & 63;
+  const int64_t begin = packed_span(starts, 0, total).start;
+  auto place = [&](int64_t s) {                         // where sequence s starts, and the last one ends
+    if (s < sequences) return packed_span(starts, s, total).start;
+    const Span last = packed_span(starts, sequences - 1, total);
+    return last.start + last.len;
+  };
+  auto first = [&](int64_t s) { return (place(s) - begin) / rows + s; };
+  const int64_t slot = id / heads;
+  int64_t seq = 0, width = sequences + 1;               // the last s with first(s) <= slot is one of `width` from seq on
+  while (width > 1) {
+    const int64_t step = (width + 63) / 64, off = lane * step;
+    const uint64_t hit = __ballot(off < width && first(seq + (off < width ? off : 0)) <= slot);
+    const int64_t at = hit == 0 ? 0 : (63 - __builtin_clzll(hit)) * step;
+    seq += at;
+    width = width - at < step ? width - at : step;
+  }
+  const int64_t here = first(seq), in = id - here * heads;
+  if (seq == sequences) return {false, 0, 0, in};
+  const int64_t slots = first(seq + 1) - here;
+  if (in < 0 || in >= slots * heads) return {false, 0, 0, -1};        // starts that do not rise
+  const int64_t head = in / slots, tile = in - head * slots;
+  const int64_t t = tile * rows < packed_span(starts, seq, total).len ? tile : -1;
+  return {t >= 0, seq, head, t};
+}
+
 __device__ __forceinline__ PackedTile packed_tile(const int32_t* starts, int64_t sequences, int64_t total, int rows,
                                                   int64_t heads, int64_t id) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t base = 0; base < sequences; base += 64) {
-    int32_t n = 0;
-    if (base + lane < sequences) n = (int32_t)((packed_span(starts, base + lane, total).len + rows - 1) / rows);
-    int64_t before = 0, all = 0;                        // tiles of the sequences before this lane's, of all 64
-    const int count = sequences - base < 64 ? (int)(sequences - base) : 64;
-    for (int k = 0; k < count; ++k) {
-      const int32_t other = __builtin_amdgcn_readlane(n, k);
-      const bool first = sequences <= 64 ? other > n || (other == n && k < lane) : k < lane;
-      before += first ? other : 0;
-      all += other;
-    }
-    const uint64_t hit = __ballot(id >= before * heads && id < (before + n) * heads);
-    if (hit != 0) {
-      const int at = __builtin_ctzll(hit);
-      const int64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)before, at);
-      const int64_t hi = __builtin_amdgcn_readlane((int)(before >> 32), at);
-      const int64_t in = id - (hi << 32 | lo) * heads, tiles = __builtin_amdgcn_readlane(n, at), head = in / tiles;
-      return {true, base + at, head, in - head * tiles};
-    }
-    id -= all * heads;
-  }
-  return {false, 0, 0, id};
+  return sequences <= 64 ? longest_first(starts, sequences, total, rows, heads, id)
+                         : by_slot(starts, sequences, total, rows, heads, id);
 }
 
 __device__ __forceinline__ int clamp_rows(int64_t v) { return (int)(v < 0 ? 0 : v < 1 << 20 ? v : 1 << 20); }
@@ -328,7 +361,7 @@ struct QueryWork {
 };
 
 // Number `id` of the grid.  Causal tiles go from the last, which sees the most keys, to the first.  False: no
-// such tile, `tile` then counts the workgroups without one.
+// such tile, `tile` then counts the workgroups past the last one, or is negative.
 __device__ __forceinline__ bool query_work(const AttnArgs& a, int64_t id, int rows, QueryWork& w) {
   int64_t t;
   if (a.q_starts != nullptr) {
@@ -363,7 +396,7 @@ __device__ __forceinline__ bool query_work(const AttnArgs& a, int64_t id, int ro
 }
 
 // The rows of a packed tensor that lie in no sequence, in every head: f(row, head) for the share of workgroup
-// number `part` of those without a tile, which are at least one; `parts` of 256 threads at most stride over them.
+// number `part` of those past the last tile, which are at least one; `parts` of 256 threads at most stride over them.
 template <typename F>
 __device__ __forceinline__ void rest_rows(const int32_t* starts, int64_t sequences, int64_t total, int64_t heads, int64_t part,
                                           int64_t parts, F f) {
