@@ -23,6 +23,7 @@ __all__ = ["attention", "attention_backward", "workspace_bytes", "backward_works
 
 MAX_HEAD_DIM = 128
 _CAUSAL, _ZERO_REST = 0x10, 0x20
+_TOKEN_STRIDE = 1 << 23                                   # what the header's token strides are below
 
 _i64, _vp, _size, _u32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32
 
@@ -70,7 +71,7 @@ def _tensor(t, name, dtype, dims):
     if s[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the channel stride must be 1")
     b, tok, h = s[:3] if dims == 4 else (0, *s[:2])
-    if (b | tok | h) % 8:                                 # of a dimension of 1 it does not matter
+    if (b | tok | h) % 8 or tok >= _TOKEN_STRIDE:         # of a dimension of 1 it does not matter
         used = [0 if n <= 1 or not t.numel() else i for n, i in zip(t.shape, s)]
         b, tok, h = used[:3] if dims == 4 else (0, *used[:2])
         if (b | tok | h) % 8:
