@@ -14,13 +14,15 @@ int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 bool bytes_ok(int64_t rows, int64_t cols) {
-  return rows == 0 || cols == 0 || (cols < kMaxBytes / 2 && rows < kMaxBytes / (cols * 2));
+  return rows == 0 || cols == 0 || (cols < kMaxBytes / 2 && rows <= (kMaxBytes - 1) / (cols * 2));
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 0 && N >= 0 && M < kMaxBytes && N < kMaxWidth && K >= 8 && K < kMaxWidth && K % 8 == 0 && bytes_ok(M, K) &&
-         bytes_ok(N, K) && bytes_ok(M, up8(N));
+         bytes_ok(N, K) && bytes_ok(M, N);
 }
+// dz has rows of np elements.
+bool back_sizes_ok(int64_t M, int64_t N, int64_t K) { return sizes_ok(M, N, K) && bytes_ok(M, up8(N)); }
 
 bool gate_ok(int64_t M, int64_t rows, int64_t stride) {
   return rows >= 1 && rows <= kMaxGateRows && stride >= 0 && stride < kMaxStride && M % rows == 0;
@@ -97,7 +99,7 @@ RTL_API rtl_status rtl_linear(const void* x, const void* w, const void* bias, co
 }
 
 RTL_API size_t rtl_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t gate_rows) {
-  if (!sizes_ok(M, N, K) || !gate_ok(M, gate_rows, 0) || N == 0) return 0;
+  if (!back_sizes_ok(M, N, K) || !gate_ok(M, gate_rows, 0) || N == 0) return 0;
   return backward_bytes(M, N, K, gate_rows).total;
 }
 
@@ -106,7 +108,7 @@ RTL_API rtl_status rtl_linear_backward(const void* dy, const void* x, const void
                                        void* dw, void* dbias, void* dgate, void* workspace, size_t workspace_bytes,
                                        uint32_t flags, void* hip_stream) {
   if (!flags_ok(flags)) return RTL_ERR_BAD_FLAGS;
-  if (!sizes_ok(M, N, K) || !gate_ok(M, gate_rows, gate_stride)) return RTL_ERR_BAD_SHAPE;
+  if (!back_sizes_ok(M, N, K) || !gate_ok(M, gate_rows, gate_stride)) return RTL_ERR_BAD_SHAPE;
   if (N == 0 && (M == 0 || dx == nullptr)) return RTL_OK;
   if (dx == nullptr && dw == nullptr && dbias == nullptr && dgate == nullptr) return RTL_OK;
   const int act = (int)((flags >> 4) & 3u);

@@ -70,7 +70,8 @@ rtl_status rtl_linear(const void* x, const void* w, const void* bias, const void
  * (The residual's gradient is dy.)  dx [M, K], dw [N, K], dbias [N], dgate
  * [gate_rows, N] densely packed; each may be NULL.  z is needed with an activation
  * or for dgate, x for dw, w for dx.  dz is rounded to the tensors' type before the two
- * products, not before dbias.  Sums have an order that only the sizes fix.
+ * products, not before dbias, and its rows are N rounded up to 8 long (below 2 GiB so
+ * too).  Sums have an order that only the sizes fix.
  * With M == 0 dw, dbias and dgate are zeros.
  */
 size_t rtl_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t gate_rows);
