@@ -13,10 +13,11 @@
 // stand (attn_common.hpp).  P and dS are rounded to bf16 there; S, dP and all sums
 // are fp32.
 //
-// Bound as the forward pass by what the matrix cores' and the softmax's share of the
-// card's power allows: 4 packed sequences of 423 to 2955 tokens, 16 heads on 8 of 128,
-// 175 us for dQ, 234 for dK and dV and 18 for the join, the matrix cores 47 and 44 % busy
-// (the longest sequence's tiles run on when the others' are done).
+// 4 packed sequences of 423 to 2955 tokens, 16 heads on 8 of 128: 173 us for dQ, 231 for dK
+// and dV and 17 for the join.  The matrix cores are 47 and 44 % busy, the vector units 38 and
+// 23, LDS 23 and 33 with the wavefronts' reads: no unit is full.  Two wavefronts share a SIMD,
+// whose products and softmax overlap in part, and the longest sequence's tiles run on when the
+// others' are done.
 #include "attn_common.hpp"
 
 namespace rtl {

@@ -9,13 +9,13 @@
 // in memory and is read transposed (ds_read_b64_tr_b16), so no matrix is ever
 // transposed in memory.
 //
-// 4096 x 12288 x 4096 with GELU: 330 us, 1250 TFLOP/s, the matrix cores 63 % busy at the 2.0 GHz
+// 4096 x 12288 x 4096 with tanh GELU: 335 us, 1230 TFLOP/s, the matrix cores 62 % busy at the 1.9 GHz
 // that power leaves them (a plain library product of 8192^3: 1490).  256 x 256 because a step then moves 64 KiB
 // for 2048 cycles of products; the smaller ones where there are too few tiles for the card
 // (linear_form).
 //
 // linear_rows_kernel.  Up to 16 or 32 rows of x are bound by reading w: a workgroup takes 16
-// channels of w, its wavefronts share out K.  3 x 4099 x 4096: 10.9 us, 3.1 TB/s.
+// channels of w, its wavefronts share out K.  3 x 4099 x 4096: 11.0 us, 3.1 TB/s.
 //
 // Sizes with too few tiles for the card split the contraction; linear_join_kernel
 // adds the parts in order and applies the epilogue.
@@ -693,7 +693,8 @@ hipError_t run_dz(const LinearDz& a, hipStream_t stream) {
 // 1160 x 1152: 18 with the smallest, 33 with it and three ranges.
 //
 // Up to 16 rows go to the kernel for few rows, 17 to 32 where it is expected to take less (its time and the tiles' measured,
-// 3 us more than above in these sizes): 32 x 4096 x 4096: 15 us, tiles 18; 32 x 12288 x 4096: 43 and 30.
+// 3 us more than above in these sizes): 32 x 4096 x 4096: 15 us, tiles 18; 32 x 12288 x 4096: 43 and 30.  (Of very wide
+// weights tiles would do for 16 rows too: 16 x 24576 x 4096 46 us, 17 rows in tiles 41.)
 LinearForm linear_form(int64_t M, int64_t N, int64_t K, bool rows_kernel) {
   if (rows_kernel && M <= 16) return {0, 0, 1};
   const int64_t m256 = (M + 255) / 256, m128 = (M + 127) / 128, n256 = (N + 255) / 256, n128 = (N + 127) / 128;

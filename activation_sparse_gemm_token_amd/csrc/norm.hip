@@ -2,9 +2,10 @@
 //
 // A row of x stays in the registers of the threads that share it, so x is
 // read once: its sum gives the mean, the centred squares the variance, and
-// the same registers the result.  Bound by memory: 4 bytes an element forward
-// and 6 backward in 16 bits.  9216 rows of 4096 in bf16: 29.9 us, 5.0 TB/s, a
-// copy's rate; backward, 8192 rows of 4096: 49 us, 4.1 TB/s, and 6 for the join.
+// the same registers the result.  4 bytes an element forward and 6 backward in 16
+// bits.  9216 rows of 4096 in bf16: 29.0 to 30.1 us, 5.0 TB/s, bound by memory at a
+// copy's rate; backward, 8192 rows of 4096: 49 us, 4.1 TB/s with the vector units 76 %
+// busy and one workgroup's barrier a row between loads and results, and 6 for the join.
 //
 // TPR threads share a row (up to 64, a wavefront, without a barrier; 128 to 1024), each
 // holds E elements in E / VEC pieces of VEC, piece i at channel

@@ -1,6 +1,7 @@
 """Dense linear layers with what follows them in one launch, and their gradients
-(include/rtlynx_dense.h): the layers that a ``LayerPolicy`` leaves dense, output
-projections into the residual stream, an MLP's first half.
+(include/rtlynx_dense.h): output projections into the residual stream, an MLP's first
+half, a modulation.  (``layers.LayerPolicy`` calls the plain ``dense_linear`` for the layers that
+it leaves dense; those with a bias or an activation of their own go here.)
 
     z = x w^T + bias,  y = residual + gate * act(z)
 

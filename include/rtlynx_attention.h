@@ -70,7 +70,8 @@ typedef struct {
  *            [sequences, heads_q, tokens_q], packed: [heads_q, tokens_q].
  *   workspace  rtl_attention_workspace_bytes(shape, flags) bytes, 16-byte aligned:
  *            where there are fewer queries than the card needs, keys are shared
- *            out over workgroups and the parts joined (0: not for this shape).
+ *            out over workgroups and the parts joined (0: not for this shape; packed
+ *            sequences and causal batches of more than 32 queries never are).
  *
  * q_starts and k_starts go together and must rise; starts and lengths outside
  * the tensors are cut to them.  No tokens, heads or sequences is a no-op.

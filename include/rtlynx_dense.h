@@ -1,8 +1,8 @@
 /*
  * rtlynx_dense.h - the dense linear layer with what follows it in its
- * epilogue, and its gradients: the layers of a block that a layer policy
- * leaves dense, the output projection into the residual stream, an MLP's
- * first half.
+ * epilogue, and its gradients: the output projection into the residual
+ * stream, an MLP's first half, a modulation.  (rtl_layer_linear's dense layers
+ * are the plain rtl_dense_linear.)
  *
  *   z = x w^T + bias
  *   y = residual + gate * act(z)
