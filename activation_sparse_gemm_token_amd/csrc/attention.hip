@@ -20,14 +20,18 @@ namespace rtl {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-// p relative to the reference maximum stays below 2^8: exact enough in fp16 too (65504).
 constexpr float kSlack = 8.f;
+// Weights are formed relative to 2^-kLift of the reference maximum.  fp16 has no steps below 2^-24: with the largest weight
+// at 1, 400 000 keys of 2^-26 each beside it would all round to 0.  At 2^7 they keep 2^-32 of it, under half a step of the result
+// for a million keys, and with the slack stay below 65504.
+template <int TYPE>
+constexpr float kLift = TYPE == kFp16 ? 7.f : 0.f;
 
 __device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ float ninf() { return -__builtin_inff(); }
 
-// A lane's running softmax: maximum the sums are scaled by (log2 units), its stand-in where no
-// key was seen, this half's share of the sum.
+// A lane's running softmax: reference maximum (log2 units), what the sums are scaled by (kLift below it, 0 where no
+// key was seen), this half's share of the sum.
 struct Running {
   float m, mu, l;
   __device__ __forceinline__ void init() { m = ninf(), mu = 0.f, l = 0.f; }
@@ -35,12 +39,12 @@ struct Running {
 
 // One block of scores into weights; O^T is rescaled where the maximum moved.  `top`: the largest
 // score of the lane's query in this step, in log2 units.
-template <int NB>
+template <int TYPE, int NB>
 __device__ __forceinline__ void move_maximum(Running& r, float top, f32x16 (&o)[NB]) {
   if (__any(top > r.m + kSlack)) {
-    const float m = __builtin_fmaxf(r.m, top);
-    r.mu = m == ninf() ? 0.f : m;
-    const float f = exp2_(r.m - r.mu);
+    const float m = __builtin_fmaxf(r.m, top), mu = m == ninf() ? 0.f : m;
+    const float f = exp2_(r.m - mu);
+    r.mu = mu - kLift<TYPE>;
     r.m = m;
     r.l *= f;
 #pragma unroll
@@ -48,6 +52,18 @@ __device__ __forceinline__ void move_maximum(Running& r, float top, f32x16 (&o)[
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[nb][i] *= f;
   }
+}
+
+// A block's weights from its scores, and their sum: added up by themselves, because one at a time faint weights would vanish
+// beside a running sum that a strong key has gone into.
+__device__ __forceinline__ float weights(f32x16& p, const f32x16& s, float c, float mu) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    p[i] = exp2_(__builtin_fmaf(s[i], c, -mu));
+    sum = i == 0 ? p[0] : sum + p[i];
+  }
+  return sum;
 }
 
 __device__ __forceinline__ float max16(const f32x16& s) {
@@ -188,15 +204,12 @@ attn_forward_kernel(AttnArgs a) {
     }
     float top = max16(s[0]);
     if constexpr (kKb == 2) top = __builtin_fmaxf(top, max16(s[kKb - 1]));
-    move_maximum<NB>(run, half_max(top) * a.c, o);
+    move_maximum<TYPE, NB>(run, half_max(top) * a.c, o);
 #pragma unroll
     for (int kb = 0; kb < kKb; ++kb) {
       f32x16 p;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[i] = exp2_(__builtin_fmaf(s[kb][i], a.c, -run.mu));
-        run.l += p[i];
-      }
+      const float sum = weights(p, s[kb], a.c, run.mu);
+      run.l += sum;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const u32x4 pw = pack_half<TYPE>(p, half);
@@ -328,13 +341,10 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = block_row(i) < left ? s[i] : ninf();
     }
-    move_maximum<NB>(run, half_max(max16(s)) * a.c, o);
+    move_maximum<TYPE, NB>(run, half_max(max16(s)) * a.c, o);
     f32x16 p;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      p[i] = exp2_(__builtin_fmaf(s[i], a.c, -run.mu));
-      run.l += p[i];
-    }
+    const float sum = weights(p, s, a.c, run.mu);
+    run.l += sum;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const u32x4 pw = pack_half<TYPE>(p, half);
@@ -400,7 +410,7 @@ attn_few_kernel(AttnArgs a) {
                                                    pack2<TYPE>(sum[4 * q + 2] * inv, sum[4 * q + 3] * inv)};
   }
   if (a.lse != nullptr && wave == 0 && h == 0)
-    a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu + __builtin_amdgcn_logf(l)) * kLn2;
+    a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu - kLift<TYPE> + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Adds up the splits' parts: 4 channels of a row per thread.  TILES: parts [tile][split][row] of the
@@ -449,7 +459,7 @@ attn_join_kernel(AttnArgs a) {
   *reinterpret_cast<u32x2*>(a.o.p + seq * a.o.b + tok * a.o.t + head * a.o.h + c) =
       (u32x2){pack2<TYPE>(sum[0] * inv, sum[1] * inv), pack2<TYPE>(sum[2] * inv, sum[3] * inv)};
   if (a.lse != nullptr && c == 0)
-    a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu + __builtin_amdgcn_logf(l)) * kLn2;
+    a.lse[(seq * a.hq + head) * a.tq + tok] = l == 0.f ? ninf() : (mu - kLift<TYPE> + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <int TYPE, int NB>
