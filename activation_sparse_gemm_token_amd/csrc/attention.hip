@@ -31,11 +31,15 @@ __device__ __forceinline__ float exp2_(float v) { return __builtin_amdgcn_exp2f(
 __device__ __forceinline__ float ninf() { return -__builtin_inff(); }
 
 // A lane's running softmax: reference maximum (log2 units), what the sums are scaled by (kLift below it, 0 where no
-// key was seen), this half's share of the sum.
+// key was seen), this half's share of the sum, and of the last steps' part of it.  In one sum faint weights, added one at a time,
+// would vanish beside a strong key's; the part goes into the sum every kPart steps (a sum for each step, formed
+// before it is added, cost 4 % of the time).
 struct Running {
-  float m, mu, l;
-  __device__ __forceinline__ void init() { m = ninf(), mu = 0.f, l = 0.f; }
+  float m, mu, l, part;
+  __device__ __forceinline__ void init() { m = ninf(), mu = 0.f, l = part = 0.f; }
+  __device__ __forceinline__ void join() { l += part, part = 0.f; }
 };
+constexpr int kPart = 16;
 
 // One block of scores into weights; O^T is rescaled where the maximum moved.  `top`: the largest
 // score of the lane's query in this step, in log2 units.
@@ -47,23 +51,12 @@ __device__ __forceinline__ void move_maximum(Running& r, float top, f32x16 (&o)[
     r.mu = mu - kLift<TYPE>;
     r.m = m;
     r.l *= f;
+    r.part *= f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[nb][i] *= f;
   }
-}
-
-// A block's weights from its scores, and their sum: added up by themselves, because one at a time faint weights would vanish
-// beside a running sum that a strong key has gone into.
-__device__ __forceinline__ float weights(f32x16& p, const f32x16& s, float c, float mu) {
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    p[i] = exp2_(__builtin_fmaf(s[i], c, -mu));
-    sum = i == 0 ? p[0] : sum + p[i];
-  }
-  return sum;
 }
 
 __device__ __forceinline__ float max16(const f32x16& s) {
@@ -208,8 +201,11 @@ attn_forward_kernel(AttnArgs a) {
 #pragma unroll
     for (int kb = 0; kb < kKb; ++kb) {
       f32x16 p;
-      const float sum = weights(p, s[kb], a.c, run.mu);
-      run.l += sum;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[i] = exp2_(__builtin_fmaf(s[kb][i], a.c, -run.mu));
+        run.part += p[i];
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const u32x4 pw = pack_half<TYPE>(p, half);
@@ -222,7 +218,9 @@ attn_forward_kernel(AttnArgs a) {
   for (int j = from; j < steps; j += 2) {
     step(j, std::integral_constant<int, 0>{});
     if (j + 1 < steps) step(j + 1, std::integral_constant<int, 1>{});
+    if ((j - from) % kPart == kPart - 2) run.join();
   }
+  run.join();
   const float l = half_sum(run.l);
   const int64_t rows = w.q.len - q0;
   if (part >= 0) {
@@ -343,8 +341,11 @@ attn_few_kernel(AttnArgs a) {
     }
     move_maximum<TYPE, NB>(run, half_max(max16(s)) * a.c, o);
     f32x16 p;
-    const float sum = weights(p, s, a.c, run.mu);
-    run.l += sum;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      p[i] = exp2_(__builtin_fmaf(s[i], a.c, -run.mu));
+      run.part += p[i];
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const u32x4 pw = pack_half<TYPE>(p, half);
@@ -352,9 +353,11 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) o[nb] = mfma32<TYPE>(column_read(base, col_off[nb][0], col_off[nb][1]), pw, o[nb]);
     }
+    if ((k0 - first) % (kPart * kRound) == (kPart - 1) * kRound) run.join();
     // The next step copies over the buffer read here.
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
+  run.join();
   // The wavefronts' results joined: every one brings its own, then sums a block of 32 channels.
   __syncthreads();
   float* const jo = reinterpret_cast<float*>(lds);                      // [wave][16 NB][64]

@@ -5,9 +5,9 @@ and as much in every channel.  Allowed: the result's and the weights' half steps
 weight in fp16 (half its smallest step, 2^-25, where the largest stands for 2^7).
 
 The sum of the weights: a score is off by a few half steps of 26, which is the weight's relative error; a lane holds half
-of its query's keys and adds up 16 of them before it adds them to its sum, so that n / 32 additions are off by 2^-24 of the
-whole each, and the 16 by as much of themselves.  That error, relative to 1 + w, goes into o by as much of o and into
-the log-sum-exp as it is."""
+of its query's keys and adds 256 or 512 of them up, one at a time, before it adds them to its sum: at most 512 additions
+beside the strong key, and n / 512 of parts, off by 2^-24 of the whole each.  That error, relative to 1 + w, goes into o
+by as much of o and into the log-sum-exp as it is."""
 import math
 
 import pytest
@@ -43,6 +43,6 @@ def test_faint_keys(dtype, tq, packed, strong, bits):
     w = n * 2.0 ** -bits
     h = torch.finfo(dtype).eps / 2
     tiny = n * 2.0 ** -32 if dtype is torch.float16 else 0.0
-    sums = (4 * bits + 64 + n / 32) * 2.0 ** -24
+    sums = (4 * bits + 64 + 512 + n / 512) * 2.0 ** -24
     assert ((o.double() - w / (1 + w)).abs() <= (2 * h * 1.01 + sums) * w / (1 + w) + tiny).all()
     assert ((lse.double() - math.log1p(w)).abs() <= sums).all()
