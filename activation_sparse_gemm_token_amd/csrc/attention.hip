@@ -69,7 +69,7 @@ __device__ __forceinline__ float max16(const f32x16& s) {
 // Queries and keys of a tile, wavefronts per SIMD.  One wavefront's softmax hides behind the others' products, so what
 // counts is how many share a SIMD: three with 32 keys and 168 registers, four with 64 keys up to head_dim 64.
 //
-// 2 x 4608 tokens, 24 heads of 128: 487 us with the join of the last tiles, 1070 TFLOP/s.  The matrix cores are 61 % busy
+// 2 x 4608 tokens, 24 heads of 128: 489 us with the join of the last tiles, 1070 TFLOP/s.  The matrix cores are 61 % busy
 // and the vector units 47 at 1.8 GHz, where a lighter kernel has 2.2 and more, so power takes its part; LDS is 31 % busy with
 // the wavefronts' reads, without conflicts, and not what bounds it.  A large product reaches 1490 TFLOP/s.  Measured when
 // this took 500 to 508 us, and not kept: two
@@ -506,9 +506,9 @@ hipError_t by_blocks(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream
 // holds (256 CUs times the wavefronts per SIMD) the last, partly filled round would leave CUs idle: the keys of its
 // tiles are split over workgroups, 256 keys at least for each.  Tiles of causal batches are never split: with about as
 // many keys as queries they differ, and the short ones come last.  More than 32 causal queries over many more keys have
-// alike tiles all the same and too few of them (64 over 30000 keys of 8 heads: 8 workgroups, 722 us; 32 queries 35, 512
-// queries without the mask 77).  Nor are packed ones, whose lengths only the device knows (8 of one query over 16384 keys
-// each, 32 heads on 8: 383 us, 91 as a batch).
+// alike tiles all the same and too few of them (64 over 30000 keys of 8 heads: 8 workgroups, 715 us; 32 queries 35, 512
+// queries without the mask 78).  Nor are packed ones, whose lengths only the device knows (8 of one query over 16384 keys
+// each, 32 heads on 8: 382 us, 91 as a batch).
 AttnPlan attn_plan(int64_t sequences, int64_t tq, int64_t tk, int64_t hq, int64_t hk, int64_t d, bool packed, bool causal) {
   AttnPlan p{false, 1, 0};
   if (packed || sequences == 0 || tq == 0 || hk == 0 || hq == 0) return p;

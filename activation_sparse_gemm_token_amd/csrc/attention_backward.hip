@@ -13,7 +13,7 @@
 // stand (attn_common.hpp).  P and dS are rounded to bf16 there; S, dP and all sums
 // are fp32.
 //
-// 4 packed sequences of 423 to 2955 tokens, 16 heads on 8 of 128: 173 us for dQ, 231 for dK
+// 4 packed sequences of 423 to 2955 tokens, 16 heads on 8 of 128: 174 us for dQ, 233 for dK
 // and dV and 17 for the join.  The matrix cores are 47 and 44 % busy, the vector units 38 and
 // 23, LDS 23 and 33 with the wavefronts' reads: no unit is full.  Two wavefronts share a SIMD,
 // whose products and softmax overlap in part, and the longest sequence's tiles run on when the
