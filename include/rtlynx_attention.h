@@ -93,7 +93,8 @@ rtl_status rtl_attention(const rtl_attn_tensor* q, const rtl_attn_tensor* k, con
  *
  * dk and dv sum over the query heads that share a key head.  Nothing is added
  * atomically: the results have the same bits in every run.  Rows of dq, dk and
- * dv that lie in no sequence, or behind a filled length, are set to zero.
+ * dv that lie in no sequence, or behind a filled length, are set to zero.  No
+ * sequences is a no-op, as in the forward pass.
  */
 size_t rtl_attention_backward_workspace_bytes(const rtl_attn_shape* shape);
 
